@@ -410,6 +410,162 @@ LLMINT8_API llmint8_status llmint8_noalloc_read_device_status(int32_t *bits_out,
 /* Largest s the decode kernel accepts. */
 LLMINT8_API int64_t llmint8_decode_max_rows(void);
 
+/* ---------------------------------------------------------------------------
+ * Operators next to the projection: low-rank adapters beside it, the gradient
+ * of its input, the layer norm in front of it, and clipping of the gradients
+ * they leave. They follow the conventions at the top of this file (device
+ * pointers, caller workspaces, asynchronous calls, validation before anything
+ * is enqueued, 16-byte alignment of fp16/int8/fp32 tensors unless stated; h
+ * and o obey the shape rules; s <= 2^31 - 1 and s == 0 gives the results of
+ * an empty sum). Half-precision tensors are binary16 unless a type is given.
+ * Their workspaces start with the same state block as llmint8_matmul's: clear
+ * it once with llmint8_workspace_init, read it with
+ * llmint8_read_device_status. A workspace may serve calls of any of them
+ * whose size it covers, one after another on one stream (captured graphs
+ * included); calls that can overlap need one each.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of the operators below. */
+#define LLMINT8_F16 0
+#define LLMINT8_F32 1
+#define LLMINT8_BF16 2
+
+/* Low-rank adapters of many requests that share one projection X.W (W is
+ * [h][o]): adapter a adds scale[a] * X.A[a]^T.B[a] to the rows that use it.
+ * n adapters (1 <= n <= 65535) of r rank slots each (8 <= r <= 128, a multiple
+ * of 8); adapter a uses its first rank[a] slots (rank_dev == NULL: all r;
+ * values are clamped to [0, r]), and what its other slots hold is never used.
+ * A factor's row t is one rank-one term, contiguous over the features. */
+typedef struct {
+    int64_t h, o;
+    int32_t n, r;
+    const uint16_t *a_dev;    /* fp16 [n][r][h] */
+    const uint16_t *b_dev;    /* fp16 [n][r][o] */
+    const float *scale_dev;   /* fp32 [n] (4-byte aligned) */
+    const int32_t *rank_dev;  /* int32 [n] (4-byte aligned) or NULL */
+} llmint8_adapters;
+
+/* Bytes of workspace for llmint8_adapters_forward and _backward with up to s
+ * rows; 0 on invalid sizes. */
+LLMINT8_API size_t llmint8_adapters_workspace_size(int64_t s, int64_t h, int64_t o, int32_t n,
+                                                   int32_t r);
+
+/* Adds every row's adapter to the projection's output (prompts, single tokens
+ * and mixtures of both in one call):
+ *   v[i][t]   = X[i] . A[a][t]                      a = ids[i], t < rank[a]
+ *   out[i][j] = fp16(base[i][j] + scale[a] * sum_t v[i][t] * B[a][t][j])
+ * with fp32 sums. ids_dev is int32 [s] (4-byte aligned), in any order; a row
+ * whose id is outside [0, n) uses no adapter: its out is its base, unchanged.
+ * base_dev (fp16 [s][o]) is llmint8_matmul's output; NULL stands for zeros.
+ * out_dev (fp16 [s][o]) may be base_dev itself; else it must not overlap it,
+ * nor X_dev (LLMINT8_ERR_ARG).
+ * v_dev, when not NULL, receives v (fp32 [s][r], 16-byte aligned; 0 where a
+ * row has no adapter or t >= rank[a]) for the backward pass. A row's result
+ * depends on its own row of X and its own adapter only: infinities and NaN of
+ * other rows or adapters do not reach it. */
+LLMINT8_API llmint8_status llmint8_adapters_forward(
+    const uint16_t *X_dev, int64_t s, const llmint8_adapters *ad, const int32_t *ids_dev,
+    const uint16_t *base_dev, uint16_t *out_dev, float *v_dev, void *ws_dev, size_t ws_bytes,
+    void *stream);
+
+/* Backward pass of the adapters for dY (fp16 [s][o]), the gradient of out:
+ *   g[i][t]     = dY[i] . B[a][t]                   a = ids[i], t < rank[a]
+ *   dX[i][k]    = fp16(base[i][k] + scale[a] * sum_t g[i][t] * A[a][t][k])
+ *   dA[a][t][k] = scale[a] * sum_{i: ids[i] = a} g[i][t] * X[i][k]
+ *   dB[a][t][j] = scale[a] * sum_{i: ids[i] = a} v[i][t] * dY[i][j]
+ * X_dev, s, ad and ids_dev are the forward call's. v_dev is what it left
+ * there, or NULL: then v is computed again from X. base_dev (fp16 [s][h]) is
+ * the gradient that reaches X through the projection itself
+ * (llmint8_matmul_backward); NULL stands for zeros. dX_dev (fp16 [s][h]) may
+ * be base_dev itself, and overlaps no other input (LLMINT8_ERR_ARG). dA_dev, dB_dev: fp32, the factors' shapes, written
+ * whole (zeros for unused slots and adapters without rows). Any of the three
+ * outputs may be NULL (not wanted); X_dev may be NULL when dA_dev is and v
+ * need not be computed. The sums over rows run in a fixed order. */
+LLMINT8_API llmint8_status llmint8_adapters_backward(
+    const uint16_t *X_dev, const uint16_t *dY_dev, int64_t s, const llmint8_adapters *ad,
+    const int32_t *ids_dev, const float *v_dev, const uint16_t *base_dev, uint16_t *dX_dev,
+    float *dA_dev, float *dB_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
+/* Gradient of the projection's input through the frozen int8 weight:
+ *   dX[i][k] = fp16(base[i][k] + sum_j dY[i][j] * WR[k][j])
+ *   WR[k][j] = fp16(fp32(fp32(wq[j][k]) * aw[j]) / 127)
+ * the fp16 weight that llmint8_matmul recovers for its outlier rows (w16_dev
+ * is not used), with fp32 sums; the rounding of X to int8 counts as the
+ * identity. dY_dev fp16 [s][o]; base_dev (fp16 [s][h]) another gradient to add
+ * or NULL; dX_dev fp16 [s][h], may be base_dev itself, and overlaps no other
+ * input (LLMINT8_ERR_ARG). */
+LLMINT8_API size_t llmint8_matmul_backward_workspace_size(int64_t s, int64_t h, int64_t o);
+LLMINT8_API llmint8_status llmint8_matmul_backward(const uint16_t *dY_dev, int64_t s,
+                                                   const llmint8_weight *w,
+                                                   const uint16_t *base_dev, uint16_t *dX_dev,
+                                                   void *ws_dev, size_t ws_bytes, void *stream);
+
+/* Layer norm of the rows of x [s][h] (the projection's input):
+ *   mean = sum_j x_j / h, rstd = 1 / sqrt(sum_j (x_j - mean)^2 / h + eps)
+ *   y_j = fp16((x_j - mean) * rstd * gamma_j + beta_j)
+ * x is fp16 or fp32 (x_type), gamma and beta [h] fp16 or fp32 (p_type);
+ * beta_dev may be NULL (zeros). mean_dev, rstd_dev (fp32 [s], 4-byte aligned,
+ * or NULL) keep the statistics for the backward pass. eps >= 0 and finite. */
+LLMINT8_API llmint8_status llmint8_layernorm_forward(const void *x_dev, int32_t x_type, int64_t s,
+                                                     int64_t h, const void *gamma_dev,
+                                                     const void *beta_dev, int32_t p_type,
+                                                     float eps, uint16_t *y_dev, float *mean_dev,
+                                                     float *rstd_dev, void *stream);
+
+/* Backward pass of the layer norm for dy (fp16 [s][h]):
+ *   xh = (x - mean) * rstd, g = dy * gamma
+ *   dx = rstd * (g - sum_j g / h - xh * sum_j (g * xh) / h)     in x's type
+ *   dgamma_j = sum_i dy_ij * xh_ij,  dbeta_j = sum_i dy_ij      fp32 [h]
+ * dx_dev, dgamma_dev and dbeta_dev may be NULL (not wanted). The sums over
+ * rows run in a fixed order. */
+LLMINT8_API size_t llmint8_layernorm_workspace_size(int64_t s, int64_t h);
+LLMINT8_API llmint8_status llmint8_layernorm_backward(
+    const uint16_t *dy_dev, const void *x_dev, int32_t x_type, int64_t s, int64_t h,
+    const void *gamma_dev, int32_t p_type, const float *mean_dev, const float *rstd_dev,
+    void *dx_dev, float *dgamma_dev, float *dbeta_dev, void *ws_dev, size_t ws_bytes,
+    void *stream);
+
+/* One gradient of a list: n elements of `type` at grad_dev (aligned to its
+ * element size; n == 0 is allowed, with any pointers). Its clipped form goes
+ * to out_dev, which is grad_dev itself (or NULL: the same) for clipping in
+ * place, or another buffer of n elements. */
+typedef struct {
+    const void *grad_dev;
+    void *out_dev;
+    int64_t n;
+    int32_t type;
+} llmint8_grad;
+
+/* A list of gradients laid out once for repeated calls. The caller sets
+ * table_dev (device memory, 256-byte aligned) and table_bytes (at least
+ * llmint8_grad_list_size(n)); llmint8_grad_list_init fills the rest and the
+ * table. No two outputs, and no output and another entry's gradient, may
+ * overlap. */
+typedef struct {
+    void *table_dev;
+    size_t table_bytes;
+    int64_t n;      /* gradients */
+    int64_t chunks; /* pieces they are cut into */
+} llmint8_grad_list;
+
+/* Bytes of the table of a list of n gradients; 0 for n < 0 or n > 2^24. */
+LLMINT8_API size_t llmint8_grad_list_size(int64_t n);
+
+/* grads_host (host memory) is read before the call returns. Asynchronous on
+ * `stream`. */
+LLMINT8_API llmint8_status llmint8_grad_list_init(const llmint8_grad *grads_host, int64_t n,
+                                                  llmint8_grad_list *list, void *stream);
+
+/* Global norm over a list, and clipping:
+ *   norm = sqrt(sum of all squares)  (fp64 sums in a fixed order)
+ *   out = g * min(1, max_norm / (norm + 1e-6))
+ * *norm_dev (fp32) receives the norm before clipping. max_norm >= 0; +inf asks
+ * for the norm alone (in place nothing is written, other outputs get copies).
+ * A norm of inf or NaN clips every element by 0 or NaN: test the norm before
+ * using the gradients. Calls that can overlap need a list each. */
+LLMINT8_API llmint8_status llmint8_clip_grads(const llmint8_grad_list *list, float max_norm,
+                                              float *norm_dev, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

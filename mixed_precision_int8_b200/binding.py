@@ -49,6 +49,19 @@ class llmint8_matmul_opts(ctypes.Structure):
                 ("status_host", _vp), ("wo_build", _c_i32)]
 
 
+class llmint8_adapters(ctypes.Structure):
+    _fields_ = [("h", _c_i64), ("o", _c_i64), ("n", _c_i32), ("r", _c_i32),
+                ("a_dev", _vp), ("b_dev", _vp), ("scale_dev", _vp), ("rank_dev", _vp)]
+
+
+class llmint8_grad(ctypes.Structure):
+    _fields_ = [("grad_dev", _vp), ("out_dev", _vp), ("n", _c_i64), ("type", _c_i32)]
+
+
+class llmint8_grad_list(ctypes.Structure):
+    _fields_ = [("table_dev", _vp), ("table_bytes", _sz), ("n", _c_i64), ("chunks", _c_i64)]
+
+
 class Llmint8Error(RuntimeError):
     def __init__(self, fn: str, code: int):
         self.code = code
@@ -108,6 +121,23 @@ def load_library():
                                     _c_f32, _vp, _vp], _c_i32),
         "llmint8_wait_selftest": ([_vp, _sz, ctypes.c_uint64, _vp], _c_i32),
         "llmint8_noalloc_read_device_status": ([_vp, _vp], _c_i32),
+        "llmint8_adapters_workspace_size": ([_c_i64, _c_i64, _c_i64, _c_i32, _c_i32], _sz),
+        "llmint8_adapters_forward": ([_vp, _c_i64, ctypes.POINTER(llmint8_adapters), _vp, _vp,
+                                      _vp, _vp, _vp, _sz, _vp], _c_i32),
+        "llmint8_adapters_backward": ([_vp, _vp, _c_i64, ctypes.POINTER(llmint8_adapters),
+                                       _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _c_i32),
+        "llmint8_matmul_backward_workspace_size": ([_c_i64, _c_i64, _c_i64], _sz),
+        "llmint8_matmul_backward": ([_vp, _c_i64, ctypes.POINTER(llmint8_weight), _vp, _vp,
+                                     _vp, _sz, _vp], _c_i32),
+        "llmint8_layernorm_forward": ([_vp, _c_i32, _c_i64, _c_i64, _vp, _vp, _c_i32, _c_f32,
+                                       _vp, _vp, _vp, _vp], _c_i32),
+        "llmint8_layernorm_workspace_size": ([_c_i64, _c_i64], _sz),
+        "llmint8_layernorm_backward": ([_vp, _vp, _c_i32, _c_i64, _c_i64, _vp, _c_i32, _vp,
+                                        _vp, _vp, _vp, _vp, _vp, _sz, _vp], _c_i32),
+        "llmint8_grad_list_size": ([_c_i64], _sz),
+        "llmint8_grad_list_init": ([ctypes.POINTER(llmint8_grad), _c_i64,
+                                    ctypes.POINTER(llmint8_grad_list), _vp], _c_i32),
+        "llmint8_clip_grads": ([ctypes.POINTER(llmint8_grad_list), _c_f32, _vp, _vp], _c_i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -128,7 +158,12 @@ EXPORTED = ("llmint8_status_string", "llmint8_workspace_size",
             "llmint8_matmul_host_ex", "llmint8_workspace_size_ex",
             "llmint8_workspace_size_host_ex", "llmint8_read_outlier_tiles_ex",
             "llmint8_noalloc_read_device_status", "llmint8_prepare_weight_cols",
-            "llmint8_prefill_kernel")
+            "llmint8_prefill_kernel",
+            "llmint8_adapters_workspace_size", "llmint8_adapters_forward",
+            "llmint8_adapters_backward", "llmint8_matmul_backward_workspace_size",
+            "llmint8_matmul_backward", "llmint8_layernorm_forward",
+            "llmint8_layernorm_workspace_size", "llmint8_layernorm_backward",
+            "llmint8_grad_list_size", "llmint8_grad_list_init", "llmint8_clip_grads")
 
 
 def status_string(code: int) -> str:
@@ -424,6 +459,326 @@ def llmint8_read_device_status(workspace: Workspace, stream=None) -> int:
     if rc not in (OK, -6):
         _check("llmint8_read_device_status", rc)
     return bits.value
+
+
+# ------------------------------------------------ operators next to the layer
+
+_TYPES = {torch.float16: 0, torch.float32: 1, torch.bfloat16: 2}  # LLMINT8_F16 / F32 / BF16
+
+
+class _Launch:
+    """The device and stream a call runs on: the tensors' own device, made
+    current for the call, and `stream` (which must be that device's) or its
+    current stream. What the call allocates belongs to that stream."""
+
+    __slots__ = ("device", "stream", "_prev", "_ctx")
+
+    def __init__(self, device: torch.device, stream=None):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        self.device = device
+        self.stream = stream
+
+    def __enter__(self):
+        self._ctx = None
+        self._prev = torch.cuda.current_device()
+        if self._prev != self.device.index:
+            torch.cuda.set_device(self.device)
+        if self.stream is not None:
+            self._ctx = torch.cuda.stream(self.stream)
+            self._ctx.__enter__()
+            return _vp(self.stream.cuda_stream)
+        return _vp(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+        if self._prev != self.device.index:
+            torch.cuda.set_device(self._prev)
+        return False
+
+
+def _tensor(t: torch.Tensor, name: str, dtype, shape, device=None):
+    """t must be a contiguous CUDA tensor of this dtype (or one of these) and
+    shape, on `device` when given."""
+    ok = t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype
+    if not ok or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype} and shape "
+                         f"{tuple(shape)}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    return t.shape
+
+
+class _OpWorkspace:
+    """A caller-owned device workspace (torch uint8 buffer) for one stream."""
+
+    def __init__(self, nbytes: int, args, device=None):
+        self.nbytes = int(nbytes)
+        if self.nbytes == 0:
+            raise ValueError(f"invalid workspace size arguments {args}")
+        device = torch.empty(0, device=device or "cuda").device
+        with _Launch(device) as st:
+            self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+            _check("llmint8_workspace_init",
+                   load_library().llmint8_workspace_init(_ptr(self.buf), self.nbytes, st))
+
+
+class AdapterWorkspace(_OpWorkspace):
+    """Workspace of llmint8_adapters_forward and _backward for up to s rows."""
+
+    def __init__(self, s: int, h: int, o: int, n: int, r: int, device=None):
+        super().__init__(load_library().llmint8_adapters_workspace_size(s, h, o, n, r),
+                         (s, h, o, n, r), device)
+
+
+class BackwardWorkspace(_OpWorkspace):
+    """Workspace of llmint8_matmul_backward for [s, o] gradients of an [h, o] weight."""
+
+    def __init__(self, s: int, h: int, o: int, device=None):
+        super().__init__(load_library().llmint8_matmul_backward_workspace_size(s, h, o),
+                         (s, h, o), device)
+
+
+class LayerNormWorkspace(_OpWorkspace):
+    """Workspace of llmint8_layernorm_backward for [s, h] rows."""
+
+    def __init__(self, s: int, h: int, device=None):
+        super().__init__(load_library().llmint8_layernorm_workspace_size(s, h), (s, h), device)
+
+
+def _ws_on(workspace: _OpWorkspace, device):
+    if workspace.buf.device != device:
+        raise ValueError(f"workspace is on {workspace.buf.device}, not on {device}")
+    return workspace
+
+
+class Adapters:
+    """n low-rank adapters beside one projection: A fp16 [n, r, h], B fp16
+    [n, r, o] (row t of each: one rank-one term), scale float32 [n], and
+    optionally the rank each adapter uses (int32 [n], default all r). The
+    tensors are kept, not copied: their values may change between calls."""
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
+                 ranks: Optional[torch.Tensor] = None):
+        if A.dim() != 3 or B.dim() != 3:
+            raise ValueError("A must be [n, r, h] and B [n, r, o]")
+        n, r, h = A.shape
+        o = B.shape[2]
+        dev = A.device
+        _tensor(A, "A", torch.float16, (n, r, h))
+        _tensor(B, "B", torch.float16, (n, r, o), dev)
+        _tensor(scale, "scale", torch.float32, (n,), dev)
+        if ranks is not None:
+            _tensor(ranks, "ranks", torch.int32, (n,), dev)
+        self.A, self.B, self.scale, self.ranks = A, B, scale, ranks
+        self.n, self.r, self.h, self.o, self.device = n, r, h, o, dev
+        self.c = llmint8_adapters(h, o, n, r, A.data_ptr(), B.data_ptr(), scale.data_ptr(),
+                                  ranks.data_ptr() if ranks is not None else None)
+
+
+def llmint8_adapters_forward(X: torch.Tensor, adapters: Adapters, ids: torch.Tensor,
+                             base: Optional[torch.Tensor] = None,
+                             out: Optional[torch.Tensor] = None,
+                             v: Optional[torch.Tensor] = None,
+                             workspace: Optional[AdapterWorkspace] = None,
+                             stream=None) -> torch.Tensor:
+    """out = base + every row's adapter: X fp16 [s,h], ids int32 [s] (a row
+    whose id is outside [0, n) uses none) -> fp16 [s,o].
+
+    base (fp16 [s,o], default zeros) is the projection's output; out may be
+    base itself. v (float32 [s,r]) receives X . A for the backward pass."""
+    ad = adapters
+    s, h = _matrix(X, "X")
+    _tensor(X, "X", torch.float16, (s, ad.h), ad.device)
+    _tensor(ids, "ids", torch.int32, (s,), ad.device)
+    if base is not None:
+        _tensor(base, "base", torch.float16, (s, ad.o), ad.device)
+    if out is not None:
+        _tensor(out, "out", torch.float16, (s, ad.o), ad.device)
+    if v is not None:
+        _tensor(v, "v", torch.float32, (s, ad.r), ad.device)
+    with _Launch(ad.device, stream) as st:
+        if out is None:
+            out = torch.empty((s, ad.o), dtype=torch.float16, device=ad.device)
+        if workspace is None:
+            workspace = AdapterWorkspace(s, ad.h, ad.o, ad.n, ad.r, ad.device)
+        _check("llmint8_adapters_forward", load_library().llmint8_adapters_forward(
+            _ptr(X), s, ctypes.byref(ad.c), _ptr(ids), _ptr(base), _ptr(out), _ptr(v),
+            _ptr(_ws_on(workspace, ad.device).buf), workspace.nbytes, st))
+    return out
+
+
+def llmint8_adapters_backward(X: Optional[torch.Tensor], dY: torch.Tensor, adapters: Adapters,
+                              ids: torch.Tensor, v: Optional[torch.Tensor] = None,
+                              base: Optional[torch.Tensor] = None,
+                              dX: Optional[torch.Tensor] = None,
+                              dA: Optional[torch.Tensor] = None,
+                              dB: Optional[torch.Tensor] = None,
+                              workspace: Optional[AdapterWorkspace] = None, stream=None,
+                              want=(True, True, True)):
+    """(dX fp16 [s,h], dA float32 [n,r,h], dB float32 [n,r,o]) for dY fp16
+    [s,o], the gradient of llmint8_adapters_forward's out.
+
+    v is what the forward call left there (default: computed again); base
+    (fp16 [s,h], default zeros) is the gradient that reaches X through the
+    projection and is added into dX, which may be base itself. want = (dX, dA,
+    dB) leaves out what is not wanted (None is returned in its place)."""
+    ad = adapters
+    s, o = _matrix(dY, "dY")
+    dev = ad.device
+    _tensor(dY, "dY", torch.float16, (s, ad.o), dev)
+    _tensor(ids, "ids", torch.int32, (s,), dev)
+    want = [w or t is not None for w, t in zip(want, (dX, dA, dB))]
+    if X is None and (want[1] or (want[2] and v is None)):
+        raise ValueError("X is needed for dA, and for dB without v")
+    for t, name, dtype, shape in ((X, "X", torch.float16, (s, ad.h)),
+                                  (v, "v", torch.float32, (s, ad.r)),
+                                  (base, "base", torch.float16, (s, ad.h)),
+                                  (dX, "dX", torch.float16, (s, ad.h)),
+                                  (dA, "dA", torch.float32, (ad.n, ad.r, ad.h)),
+                                  (dB, "dB", torch.float32, (ad.n, ad.r, ad.o))):
+        if t is not None:
+            _tensor(t, name, dtype, shape, dev)
+    with _Launch(dev, stream) as st:
+        if dX is None and want[0]:
+            dX = torch.empty((s, ad.h), dtype=torch.float16, device=dev)
+        if dA is None and want[1]:
+            dA = torch.empty((ad.n, ad.r, ad.h), dtype=torch.float32, device=dev)
+        if dB is None and want[2]:
+            dB = torch.empty((ad.n, ad.r, ad.o), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = AdapterWorkspace(s, ad.h, ad.o, ad.n, ad.r, dev)
+        _check("llmint8_adapters_backward", load_library().llmint8_adapters_backward(
+            _ptr(X), _ptr(dY), s, ctypes.byref(ad.c), _ptr(ids), _ptr(v), _ptr(base), _ptr(dX),
+            _ptr(dA), _ptr(dB), _ptr(_ws_on(workspace, dev).buf), workspace.nbytes, st))
+    return dX, dA, dB
+
+
+def llmint8_matmul_backward(dY: torch.Tensor, w: PreparedWeight,
+                            base: Optional[torch.Tensor] = None,
+                            out: Optional[torch.Tensor] = None,
+                            workspace: Optional[BackwardWorkspace] = None,
+                            stream=None) -> torch.Tensor:
+    """dX = dY . W^T through the frozen int8 weight (+ base): dY fp16 [s,o]
+    -> fp16 [s,h]. out may be base itself."""
+    s, o = _matrix(dY, "dY")
+    dev = w.wq.device
+    _tensor(dY, "dY", torch.float16, (s, w.o), dev)
+    if base is not None:
+        _tensor(base, "base", torch.float16, (s, w.h), dev)
+    if out is not None:
+        _tensor(out, "out", torch.float16, (s, w.h), dev)
+    with _Launch(dev, stream) as st:
+        if out is None:
+            out = torch.empty((s, w.h), dtype=torch.float16, device=dev)
+        if workspace is None:
+            workspace = BackwardWorkspace(s, w.h, w.o, dev)
+        _check("llmint8_matmul_backward", load_library().llmint8_matmul_backward(
+            _ptr(dY), s, ctypes.byref(w.c), _ptr(base), _ptr(out),
+            _ptr(_ws_on(workspace, dev).buf), workspace.nbytes, st))
+    return out
+
+
+_LN_TYPES = (torch.float16, torch.float32)
+
+
+def llmint8_layernorm_forward(X: torch.Tensor, gamma: torch.Tensor,
+                              beta: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                              out: Optional[torch.Tensor] = None, stream=None):
+    """(Y fp16 [s,h], mean float32 [s], rstd float32 [s]) = layer norm of the
+    rows of X (fp16 or fp32 [s,h]); gamma and beta [h] are fp16 or fp32 alike."""
+    s, h = _matrix(X, "X")
+    dev = X.device
+    _tensor(X, "X", _LN_TYPES, (s, h))
+    _tensor(gamma, "gamma", _LN_TYPES, (h,), dev)
+    if beta is not None:
+        _tensor(beta, "beta", gamma.dtype, (h,), dev)
+    if out is not None:
+        _tensor(out, "out", torch.float16, (s, h), dev)
+    with _Launch(dev, stream) as st:
+        if out is None:
+            out = torch.empty((s, h), dtype=torch.float16, device=dev)
+        mean, rstd = torch.empty((2, s), dtype=torch.float32, device=dev).unbind(0)
+        _check("llmint8_layernorm_forward", load_library().llmint8_layernorm_forward(
+            _ptr(X), _TYPES[X.dtype], s, h, _ptr(gamma), _ptr(beta), _TYPES[gamma.dtype],
+            float(eps), _ptr(out), _ptr(mean), _ptr(rstd), st))
+    return out, mean, rstd
+
+
+def llmint8_layernorm_backward(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tensor,
+                               mean: torch.Tensor, rstd: torch.Tensor,
+                               dX: Optional[torch.Tensor] = None,
+                               workspace: Optional[LayerNormWorkspace] = None, stream=None):
+    """(dX in X's type, dgamma float32 [h], dbeta float32 [h]) for dY fp16
+    [s,h], with the forward call's mean and rstd."""
+    s, h = _matrix(X, "X")
+    dev = X.device
+    _tensor(X, "X", _LN_TYPES, (s, h))
+    _tensor(dY, "dY", torch.float16, (s, h), dev)
+    _tensor(gamma, "gamma", _LN_TYPES, (h,), dev)
+    _tensor(mean, "mean", torch.float32, (s,), dev)
+    _tensor(rstd, "rstd", torch.float32, (s,), dev)
+    if dX is not None:
+        _tensor(dX, "dX", X.dtype, (s, h), dev)
+    with _Launch(dev, stream) as st:
+        if dX is None:
+            dX = torch.empty_like(X)
+        dgamma, dbeta = torch.empty((2, h), dtype=torch.float32, device=dev).unbind(0)
+        if workspace is None:
+            workspace = LayerNormWorkspace(s, h, dev)
+        _check("llmint8_layernorm_backward", load_library().llmint8_layernorm_backward(
+            _ptr(dY), _ptr(X), _TYPES[X.dtype], s, h, _ptr(gamma), _TYPES[gamma.dtype],
+            _ptr(mean), _ptr(rstd), _ptr(dX), _ptr(dgamma), _ptr(dbeta),
+            _ptr(_ws_on(workspace, dev).buf), workspace.nbytes, st))
+    return dX, dgamma, dbeta
+
+
+class GradList:
+    """Gradients laid out once for llmint8_clip_grads: contiguous CUDA tensors
+    (fp16, bf16 or fp32) on one device, clipped in place, or into `outs`
+    (tensors of the same sizes and types). The tensors are kept, not copied."""
+
+    def __init__(self, grads, outs=None, device=None):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.grads) != len(self.outs):
+            raise ValueError("outs must match grads one for one")
+        device = self.grads[0].device if self.grads else torch.empty(
+            0, device=device or "cuda").device
+        n = len(self.grads)
+        items = (llmint8_grad * max(n, 1))()
+        for i, (g, out) in enumerate(zip(self.grads, self.outs)):
+            _tensor(g, f"grads[{i}]", tuple(_TYPES), g.shape, device)
+            _tensor(out, f"outs[{i}]", g.dtype, g.shape, device)
+            items[i] = llmint8_grad(g.data_ptr(), out.data_ptr(), g.numel(), _TYPES[g.dtype])
+        self.device = device
+        lib = load_library()
+        nbytes = int(lib.llmint8_grad_list_size(n))
+        with _Launch(device) as st:
+            self.table = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+            self.c = llmint8_grad_list(self.table.data_ptr(), nbytes, 0, 0)
+            _check("llmint8_grad_list_init", lib.llmint8_grad_list_init(
+                items, n, ctypes.byref(self.c), st))
+
+
+def llmint8_clip_grads(grads: GradList, max_norm: float, norm: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """The global norm of a list's gradients (float32 [1]); they are scaled so
+    that it does not exceed max_norm (inf: the norm alone)."""
+    if norm is not None:
+        _tensor(norm, "norm", torch.float32, (1,), grads.device)
+    with _Launch(grads.device, stream) as st:
+        if norm is None:
+            norm = torch.empty((1,), dtype=torch.float32, device=grads.device)
+        _check("llmint8_clip_grads", load_library().llmint8_clip_grads(
+            ctypes.byref(grads.c), float(max_norm), _ptr(norm), st))
+    return norm
 
 
 _cudart = None

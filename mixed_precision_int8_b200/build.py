@@ -15,7 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libllmint8.so")
-SOURCES = [os.path.join(CSRC, "llmint8_api.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("llmint8_api.cu", "finetune_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
                   if f.endswith(".cuh")] + [os.path.join(INCLUDE, "llmint8.h")]
 
@@ -39,9 +39,19 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             and os.path.getmtime(LIB) >= max(os.path.getmtime(d) for d in DEPS)):
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc_path()] + nvcc_flags(verbose_ptxas) + ["-shared", "-o", tmp] + SOURCES
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    nvcc = [nvcc_path()] + nvcc_flags(verbose_ptxas)
+    objs = [f"{tmp}.{os.path.basename(s)}.o" for s in SOURCES]
+    try:
+        # one compiler per source file, all at once
+        procs = [subprocess.Popen(nvcc + ["-c", "-o", o, s]) for s, o in zip(SOURCES, objs)]
+        for p in [p for p in procs if p.wait() != 0]:
+            raise subprocess.CalledProcessError(p.returncode, p.args)
+        subprocess.run(nvcc + ["-shared", "-o", tmp] + objs, check=True)
+        os.replace(tmp, LIB)
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
     return LIB
 
 

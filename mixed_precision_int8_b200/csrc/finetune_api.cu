@@ -1,0 +1,468 @@
+// C ABI of the operators next to the projection (declared in
+// include/llmint8.h): low-rank adapters, the gradient of the projection's
+// input, layer norm and gradient clipping. Argument validation, workspace
+// layout and launches; host code only enqueues work and never allocates
+// device memory.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "llmint8.h"
+#include "host_common.cuh"
+#include "adapters.cuh"
+#include "grad_clip.cuh"
+#include "input_grad_sm100.cuh"
+#include "layernorm.cuh"
+
+namespace {
+
+using namespace llmint8;
+
+struct Device {
+  bool init = false;
+  bool supported = false;
+  int sm_count = 0;
+};
+Device g_device[kMaxDevices];
+std::mutex g_device_mutex;
+
+llmint8_status current_device(Device **out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return LLMINT8_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(g_device_mutex);
+  Device &d = g_device[dev];
+  if (!d.init) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return LLMINT8_ERR_CUDA;
+    d.supported = major == 10 && minor == 0;
+    d.init = true;
+  }
+  if (!d.supported) return LLMINT8_ERR_UNSUPPORTED;
+  *out = &d;
+  return LLMINT8_OK;
+}
+
+llmint8_status check_rows(int64_t s) {
+  return s < 0 || s > (int64_t)INT32_MAX ? LLMINT8_ERR_SHAPE : LLMINT8_OK;
+}
+
+llmint8_status check_width(int64_t h) {
+  return h < 16 || h > kMaxH || (h % 16) != 0 ? LLMINT8_ERR_SHAPE : LLMINT8_OK;
+}
+
+unsigned blocks_for(int64_t work, int64_t per_block) {
+  return (unsigned)((work + per_block - 1) / per_block);
+}
+
+// Whether [p, p + pn) and [q, q + qn) share a byte.
+bool overlap(const void *p, size_t pn, const void *q, size_t qn) {
+  if (!p || !q || pn == 0 || qn == 0) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + qn && b < a + pn;
+}
+
+// ------------------------------------------------------------- adapters
+
+struct AdapterLayout {
+  size_t v, g, end;
+};
+
+AdapterLayout adapter_layout(int64_t s, int32_t r) {
+  AdapterLayout L;
+  L.v = kStateBytes;
+  L.g = align256(L.v + 4 * (size_t)s * r);
+  L.end = align256(L.g + 4 * (size_t)s * r);
+  return L;
+}
+
+llmint8_status check_adapter_sizes(int64_t s, int64_t h, int64_t o, int32_t n, int32_t r) {
+  llmint8_status rc = check_hw(h, o);
+  if (rc) return rc;
+  if (n < 1 || n > 65535 || r < 8 || r > lora::MAX_R || r % 8 != 0) return LLMINT8_ERR_SHAPE;
+  return check_rows(s);
+}
+
+llmint8_status check_adapters(const llmint8_adapters *ad, int64_t s) {
+  if (!ad || !ad->a_dev || !ad->b_dev || !ad->scale_dev) return LLMINT8_ERR_NULL;
+  llmint8_status rc = check_adapter_sizes(s, ad->h, ad->o, ad->n, ad->r);
+  if (rc) return rc;
+  if (!aligned(ad->a_dev, 16) || !aligned(ad->b_dev, 16) || !aligned(ad->scale_dev, 4) ||
+      !aligned(ad->rank_dev, 4))
+    return LLMINT8_ERR_ALIGN;
+  return LLMINT8_OK;
+}
+
+const __half *as_half(const uint16_t *p) { return reinterpret_cast<const __half *>(p); }
+__half *as_half(uint16_t *p) { return reinterpret_cast<__half *>(p); }
+
+llmint8_status enqueue_shrink(const uint16_t *X, int64_t s, int64_t h, const uint16_t *F,
+                              const llmint8_adapters *ad, const int32_t *ids, float *v,
+                              cudaStream_t st) {
+  if (launch(lora::k_shrink_simple, dim3(blocks_for(s * ad->r, 8)), dim3(256), 0, st, false,
+             as_half(X), s, (int32_t)h, as_half(F), ids, ad->rank_dev, ad->n, ad->r,
+             v) != cudaSuccess)
+    return LLMINT8_ERR_CUDA;
+  return LLMINT8_OK;
+}
+
+llmint8_status enqueue_expand(const float *v, int64_t s, int64_t o, const uint16_t *F,
+                              const llmint8_adapters *ad, const int32_t *ids,
+                              const uint16_t *base, uint16_t *out, cudaStream_t st) {
+  if (launch(lora::k_expand_simple, dim3(blocks_for(s * (o / 8), 256)), dim3(256), 0, st, false, v,
+             s, (int32_t)o, as_half(F), ids, ad->scale_dev, ad->rank_dev, ad->n, ad->r,
+             as_half(base), as_half(out)) != cudaSuccess)
+    return LLMINT8_ERR_CUDA;
+  return LLMINT8_OK;
+}
+
+llmint8_status enqueue_outer(const float *p, const uint16_t *Q, int64_t s, int64_t w,
+                             const llmint8_adapters *ad, const int32_t *ids, float *d,
+                             cudaStream_t st) {
+  if (launch(lora::k_outer_simple, dim3(blocks_for((int64_t)ad->n * ad->r * (w / 8), 256)),
+             dim3(256), 0, st, false, p, as_half(Q), s, (int32_t)w, ids, ad->scale_dev,
+             ad->rank_dev, ad->n, ad->r, d) != cudaSuccess)
+    return LLMINT8_ERR_CUDA;
+  return LLMINT8_OK;
+}
+
+// ----------------------------------------------------------- layer norm
+
+// Threads and vectors of eight per thread for a row of h <= ln::MAX_ROW.
+void ln_shape(int64_t h, int *threads, int *nv) {
+  const int64_t vecs = h / 8;
+  *nv = (int)((vecs + ln::MAX_THREADS - 1) / ln::MAX_THREADS);
+  const int64_t t = (vecs + *nv - 1) / *nv;
+  *threads = (int)((t + 31) / 32 * 32);
+}
+
+template <typename TX, typename TP>
+cudaError_t ln_forward(const void *x, int64_t s, int64_t h, const void *gamma, const void *beta,
+                       float eps, uint16_t *y, float *mean, float *rstd, cudaStream_t st) {
+  const TX *xp = static_cast<const TX *>(x);
+  const TP *gp = static_cast<const TP *>(gamma), *bp = static_cast<const TP *>(beta);
+  const dim3 grid((unsigned)s);
+  if (h > ln::MAX_ROW)
+    return launch(ln::k_ln_forward_long<TX, TP>, grid, dim3(ln::MAX_THREADS), 0, st, false, xp,
+                  (int32_t)h, gp, bp, eps, as_half(y), mean, rstd);
+  int threads, nv;
+  ln_shape(h, &threads, &nv);
+  auto *k = nv == 1   ? ln::k_ln_forward<TX, TP, 1>
+            : nv == 2 ? ln::k_ln_forward<TX, TP, 2>
+            : nv == 3 ? ln::k_ln_forward<TX, TP, 3>
+                      : ln::k_ln_forward<TX, TP, 4>;
+  return launch(k, grid, dim3(threads), 0, st, false, xp, (int32_t)h, gp, bp, eps, as_half(y),
+                mean, rstd);
+}
+
+// Blocks of the backward kernel: up to kLnBlocksPerSm per SM, never more
+// than rows.
+constexpr int kLnBlocksPerSm = 2;
+constexpr int kLnMaxBlocks = 512;
+int64_t ln_blocks(int64_t s, int sm_count) {
+  return std::max<int64_t>(
+      1, std::min<int64_t>({s, (int64_t)kLnBlocksPerSm * sm_count, (int64_t)kLnMaxBlocks}));
+}
+
+template <typename TX, typename TP>
+cudaError_t ln_backward(const uint16_t *dy, const void *x, int64_t s, int64_t h, const void *gamma,
+                        const float *mean, const float *rstd, void *dx, float *part,
+                        int64_t blocks, cudaStream_t st) {
+  const TX *xp = static_cast<const TX *>(x);
+  const TP *gp = static_cast<const TP *>(gamma);
+  TX *dxp = static_cast<TX *>(dx);
+  const dim3 grid((unsigned)blocks);
+  if (h > ln::MAX_ROW)
+    return launch(ln::k_ln_backward_long<TX, TP>, grid, dim3(ln::MAX_THREADS), 0, st, false,
+                  as_half(dy), xp, s, (int32_t)h, gp, mean, rstd, dxp, part);
+  int threads, nv;
+  ln_shape(h, &threads, &nv);
+  auto *k = nv == 1   ? ln::k_ln_backward<TX, TP, 1>
+            : nv == 2 ? ln::k_ln_backward<TX, TP, 2>
+            : nv == 3 ? ln::k_ln_backward<TX, TP, 3>
+                      : ln::k_ln_backward<TX, TP, 4>;
+  return launch(k, grid, dim3(threads), 0, st, false, as_half(dy), xp, s, (int32_t)h, gp, mean,
+                rstd, dxp, part);
+}
+
+bool ln_types_ok(int32_t x_type, int32_t p_type) {
+  return (x_type == LLMINT8_F16 || x_type == LLMINT8_F32) &&
+         (p_type == LLMINT8_F16 || p_type == LLMINT8_F32);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t llmint8_adapters_workspace_size(int64_t s, int64_t h, int64_t o, int32_t n, int32_t r) {
+  if (check_adapter_sizes(s, h, o, n, r)) return 0;
+  return adapter_layout(s, r).end;
+}
+
+llmint8_status llmint8_adapters_forward(const uint16_t *X_dev, int64_t s,
+                                        const llmint8_adapters *ad, const int32_t *ids_dev,
+                                        const uint16_t *base_dev, uint16_t *out_dev, float *v_dev,
+                                        void *ws_dev, size_t ws_bytes, void *stream) {
+  llmint8_status rc = check_adapters(ad, s);
+  if (rc) return rc;
+  if (s == 0) return LLMINT8_OK;
+  if (!X_dev || !ids_dev || !out_dev || !ws_dev) return LLMINT8_ERR_NULL;
+  if (!aligned(X_dev, 16) || !aligned(ids_dev, 4) || !aligned(base_dev, 16) ||
+      !aligned(out_dev, 16) || !aligned(v_dev, 16) || !aligned(ws_dev, 256))
+    return LLMINT8_ERR_ALIGN;
+  const size_t in_bytes = 2 * (size_t)s * ad->h, out_bytes = 2 * (size_t)s * ad->o;
+  if (overlap(out_dev, out_bytes, X_dev, in_bytes) ||
+      (base_dev != out_dev && overlap(out_dev, out_bytes, base_dev, out_bytes)))
+    return LLMINT8_ERR_ARG;
+  const AdapterLayout L = adapter_layout(s, ad->r);
+  if (ws_bytes < L.end) return LLMINT8_ERR_WORKSPACE;
+  Device *dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  cudaStream_t st = as_stream(stream);
+  float *v = v_dev ? v_dev : reinterpret_cast<float *>(static_cast<uint8_t *>(ws_dev) + L.v);
+  if ((rc = enqueue_shrink(X_dev, s, ad->h, ad->a_dev, ad, ids_dev, v, st))) return rc;
+  if ((rc = enqueue_expand(v, s, ad->o, ad->b_dev, ad, ids_dev, base_dev, out_dev, st))) return rc;
+  return last_launch();
+}
+
+llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *dY_dev, int64_t s,
+                                         const llmint8_adapters *ad, const int32_t *ids_dev,
+                                         const float *v_dev, const uint16_t *base_dev,
+                                         uint16_t *dX_dev, float *dA_dev, float *dB_dev,
+                                         void *ws_dev, size_t ws_bytes, void *stream) {
+  llmint8_status rc = check_adapters(ad, s);
+  if (rc) return rc;
+  const bool need_v = dB_dev && !v_dev;
+  if (s > 0 && (!dY_dev || !ids_dev || !ws_dev || ((dA_dev || need_v) && !X_dev)))
+    return LLMINT8_ERR_NULL;
+  if (!aligned(X_dev, 16) || !aligned(dY_dev, 16) || !aligned(ids_dev, 4) || !aligned(v_dev, 16) ||
+      !aligned(base_dev, 16) || !aligned(dX_dev, 16) || !aligned(dA_dev, 16) ||
+      !aligned(dB_dev, 16) || !aligned(ws_dev, 256))
+    return LLMINT8_ERR_ALIGN;
+  const size_t in_bytes = 2 * (size_t)s * ad->h, out_bytes = 2 * (size_t)s * ad->o;
+  if (overlap(dX_dev, in_bytes, X_dev, in_bytes) || overlap(dX_dev, in_bytes, dY_dev, out_bytes) ||
+      (base_dev != dX_dev && overlap(dX_dev, in_bytes, base_dev, in_bytes)))
+    return LLMINT8_ERR_ARG;
+  const AdapterLayout L = adapter_layout(s, ad->r);
+  if (s > 0 && ws_bytes < L.end) return LLMINT8_ERR_WORKSPACE;
+  Device *dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  cudaStream_t st = as_stream(stream);
+  const size_t factor = 4 * (size_t)ad->n * ad->r;
+  if (s == 0) {  // no rows: empty sums
+    if ((dA_dev && cudaMemsetAsync(dA_dev, 0, factor * ad->h, st) != cudaSuccess) ||
+        (dB_dev && cudaMemsetAsync(dB_dev, 0, factor * ad->o, st) != cudaSuccess))
+      return LLMINT8_ERR_CUDA;
+    return LLMINT8_OK;
+  }
+  uint8_t *wsb = static_cast<uint8_t *>(ws_dev);
+  float *v = reinterpret_cast<float *>(wsb + L.v), *g = reinterpret_cast<float *>(wsb + L.g);
+  const float *vp = v_dev ? v_dev : v;
+  if (need_v && (rc = enqueue_shrink(X_dev, s, ad->h, ad->a_dev, ad, ids_dev, v, st))) return rc;
+  if ((dX_dev || dA_dev) && (rc = enqueue_shrink(dY_dev, s, ad->o, ad->b_dev, ad, ids_dev, g, st)))
+    return rc;
+  if (dX_dev && (rc = enqueue_expand(g, s, ad->h, ad->a_dev, ad, ids_dev, base_dev, dX_dev, st)))
+    return rc;
+  if (dA_dev && (rc = enqueue_outer(g, X_dev, s, ad->h, ad, ids_dev, dA_dev, st))) return rc;
+  if (dB_dev && (rc = enqueue_outer(vp, dY_dev, s, ad->o, ad, ids_dev, dB_dev, st))) return rc;
+  return last_launch();
+}
+
+size_t llmint8_matmul_backward_workspace_size(int64_t s, int64_t h, int64_t o) {
+  if (check_hw(h, o) || check_rows(s)) return 0;
+  return kStateBytes;
+}
+
+llmint8_status llmint8_matmul_backward(const uint16_t *dY_dev, int64_t s, const llmint8_weight *w,
+                                       const uint16_t *base_dev, uint16_t *dX_dev, void *ws_dev,
+                                       size_t ws_bytes, void *stream) {
+  if (!w || !w->wq_dev || !w->aw_dev) return LLMINT8_ERR_NULL;
+  llmint8_status rc = check_hw(w->h, w->o);
+  if (rc) return rc;
+  if ((rc = check_rows(s))) return rc;
+  if (!aligned(w->wq_dev, 16) || !aligned(w->aw_dev, 16)) return LLMINT8_ERR_ALIGN;
+  if (s == 0) return LLMINT8_OK;
+  if (!dY_dev || !dX_dev || !ws_dev) return LLMINT8_ERR_NULL;
+  if (!aligned(dY_dev, 16) || !aligned(base_dev, 16) || !aligned(dX_dev, 16) ||
+      !aligned(ws_dev, 256))
+    return LLMINT8_ERR_ALIGN;
+  const size_t dx_bytes = 2 * (size_t)s * w->h;
+  if (overlap(dX_dev, dx_bytes, dY_dev, 2 * (size_t)s * w->o) ||
+      (base_dev != dX_dev && overlap(dX_dev, dx_bytes, base_dev, dx_bytes)))
+    return LLMINT8_ERR_ARG;
+  if (ws_bytes < llmint8_matmul_backward_workspace_size(s, w->h, w->o))
+    return LLMINT8_ERR_WORKSPACE;
+  Device *dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  if (launch(igrad::k_input_grad_simple, dim3(blocks_for(w->h, 64), blocks_for(s, 64)), dim3(256),
+             0, as_stream(stream), false, as_half(dY_dev), s, (int32_t)w->h, (int32_t)w->o,
+             (const int8_t *)w->wq_dev, (const float *)w->aw_dev, as_half(base_dev),
+             as_half(dX_dev)) != cudaSuccess)
+    return LLMINT8_ERR_CUDA;
+  return last_launch();
+}
+
+llmint8_status llmint8_layernorm_forward(const void *x_dev, int32_t x_type, int64_t s, int64_t h,
+                                         const void *gamma_dev, const void *beta_dev,
+                                         int32_t p_type, float eps, uint16_t *y_dev,
+                                         float *mean_dev, float *rstd_dev, void *stream) {
+  llmint8_status rc = check_width(h);
+  if (rc) return rc;
+  if ((rc = check_rows(s))) return rc;
+  if (!ln_types_ok(x_type, p_type) || !std::isfinite(eps) || eps < 0.0f) return LLMINT8_ERR_ARG;
+  if (s == 0) return LLMINT8_OK;
+  if (!x_dev || !gamma_dev || !y_dev) return LLMINT8_ERR_NULL;
+  if (!aligned(x_dev, 16) || !aligned(gamma_dev, 16) || !aligned(beta_dev, 16) ||
+      !aligned(y_dev, 16) || !aligned(mean_dev, 4) || !aligned(rstd_dev, 4))
+    return LLMINT8_ERR_ALIGN;
+  Device *dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  cudaStream_t st = as_stream(stream);
+  auto *f = x_type == LLMINT8_F16
+                ? (p_type == LLMINT8_F16 ? ln_forward<__half, __half> : ln_forward<__half, float>)
+                : (p_type == LLMINT8_F16 ? ln_forward<float, __half> : ln_forward<float, float>);
+  if (f(x_dev, s, h, gamma_dev, beta_dev, eps, y_dev, mean_dev, rstd_dev, st) != cudaSuccess)
+    return LLMINT8_ERR_CUDA;
+  return last_launch();
+}
+
+size_t llmint8_layernorm_workspace_size(int64_t s, int64_t h) {
+  if (check_width(h) || check_rows(s)) return 0;
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(s, kLnMaxBlocks));
+  return align256(kStateBytes + 8 * (size_t)blocks * h);
+}
+
+llmint8_status llmint8_layernorm_backward(const uint16_t *dy_dev, const void *x_dev,
+                                          int32_t x_type, int64_t s, int64_t h,
+                                          const void *gamma_dev, int32_t p_type,
+                                          const float *mean_dev, const float *rstd_dev,
+                                          void *dx_dev, float *dgamma_dev, float *dbeta_dev,
+                                          void *ws_dev, size_t ws_bytes, void *stream) {
+  llmint8_status rc = check_width(h);
+  if (rc) return rc;
+  if ((rc = check_rows(s))) return rc;
+  if (!ln_types_ok(x_type, p_type)) return LLMINT8_ERR_ARG;
+  if (s > 0 && (!dy_dev || !x_dev || !gamma_dev || !mean_dev || !rstd_dev || !ws_dev))
+    return LLMINT8_ERR_NULL;
+  if (!aligned(dy_dev, 16) || !aligned(x_dev, 16) || !aligned(gamma_dev, 16) ||
+      !aligned(mean_dev, 4) || !aligned(rstd_dev, 4) || !aligned(dx_dev, 16) ||
+      !aligned(dgamma_dev, 16) || !aligned(dbeta_dev, 16) || !aligned(ws_dev, 256))
+    return LLMINT8_ERR_ALIGN;
+  if (s > 0 && ws_bytes < llmint8_layernorm_workspace_size(s, h)) return LLMINT8_ERR_WORKSPACE;
+  Device *dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
+  cudaStream_t st = as_stream(stream);
+  if (s == 0) {  // no rows: empty sums
+    if ((dgamma_dev && cudaMemsetAsync(dgamma_dev, 0, 4 * (size_t)h, st) != cudaSuccess) ||
+        (dbeta_dev && cudaMemsetAsync(dbeta_dev, 0, 4 * (size_t)h, st) != cudaSuccess))
+      return LLMINT8_ERR_CUDA;
+    return LLMINT8_OK;
+  }
+  const int64_t blocks = ln_blocks(s, dev->sm_count);
+  float *part = dgamma_dev || dbeta_dev
+                    ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws_dev) + kStateBytes)
+                    : nullptr;
+  auto *f = x_type == LLMINT8_F16
+                ? (p_type == LLMINT8_F16 ? ln_backward<__half, __half> : ln_backward<__half, float>)
+                : (p_type == LLMINT8_F16 ? ln_backward<float, __half> : ln_backward<float, float>);
+  if (f(dy_dev, x_dev, s, h, gamma_dev, mean_dev, rstd_dev, dx_dev, part, blocks, st) !=
+      cudaSuccess)
+    return LLMINT8_ERR_CUDA;
+  if (part && launch(ln::k_ln_reduce, dim3(blocks_for(2 * h, ln::RED_COLS)),
+                     dim3(ln::RED_COLS * ln::RED_LANES), 0, st, true, (const float *)part,
+                     (int32_t)blocks, (int32_t)h, dgamma_dev, dbeta_dev) != cudaSuccess)
+    return LLMINT8_ERR_CUDA;
+  return last_launch();
+}
+
+size_t llmint8_grad_list_size(int64_t n) {
+  if (n < 0 || n > (int64_t)1 << 24) return 0;
+  return align256(clip::kPartialBytes + sizeof(clip::Entry) * (size_t)n);
+}
+
+llmint8_status llmint8_grad_list_init(const llmint8_grad *grads_host, int64_t n,
+                                      llmint8_grad_list *list, void *stream) {
+  if (!list || !list->table_dev || (n > 0 && !grads_host)) return LLMINT8_ERR_NULL;
+  const size_t need = llmint8_grad_list_size(n);
+  if (need == 0) return LLMINT8_ERR_SHAPE;
+  if (!aligned(list->table_dev, 256)) return LLMINT8_ERR_ALIGN;
+  if (list->table_bytes < need) return LLMINT8_ERR_WORKSPACE;
+  int64_t chunks = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const llmint8_grad &g = grads_host[i];
+    if (g.type != LLMINT8_F16 && g.type != LLMINT8_F32 && g.type != LLMINT8_BF16)
+      return LLMINT8_ERR_ARG;
+    if (g.n < 0 || g.n > (int64_t)1 << 40) return LLMINT8_ERR_SHAPE;
+    if (g.n == 0) continue;
+    if (!g.grad_dev) return LLMINT8_ERR_NULL;
+    const uintptr_t size = g.type == LLMINT8_F32 ? 4 : 2;
+    if (!aligned(g.grad_dev, size) || !aligned(g.out_dev, size)) return LLMINT8_ERR_ALIGN;
+    if (g.out_dev != g.grad_dev &&
+        overlap(g.out_dev, size * (size_t)g.n, g.grad_dev, size * (size_t)g.n))
+      return LLMINT8_ERR_ARG;
+    chunks += (g.n + clip::CHUNK - 1) / clip::CHUNK;
+  }
+  Device *dev = nullptr;
+  llmint8_status rc = current_device(&dev);
+  if (rc) return rc;
+  cudaStream_t st = as_stream(stream);
+  clip::Entry *table = reinterpret_cast<clip::Entry *>(static_cast<uint8_t *>(list->table_dev) +
+                                                       clip::kPartialBytes);
+  int64_t at = 0;
+  for (int64_t i = 0; i < n; i += clip::INIT_ENTRIES) {
+    const int m = (int)std::min<int64_t>(clip::INIT_ENTRIES, n - i);
+    clip::InitBatch batch = {};
+    for (int k = 0; k < m; ++k) {
+      const llmint8_grad &g = grads_host[i + k];
+      clip::Entry &e = batch.e[k];
+      e.grad = g.grad_dev;
+      e.out = g.out_dev ? g.out_dev : const_cast<void *>(g.grad_dev);
+      e.n = g.n;
+      e.chunk0 = at;
+      e.type = g.type;
+      at += (g.n + clip::CHUNK - 1) / clip::CHUNK;
+    }
+    if (launch(clip::k_list_init, dim3(1), dim3(64), 0, st, false, table + i, batch, m) !=
+        cudaSuccess)
+      return LLMINT8_ERR_CUDA;
+  }
+  list->n = n;
+  list->chunks = chunks;
+  return last_launch();
+}
+
+llmint8_status llmint8_clip_grads(const llmint8_grad_list *list, float max_norm, float *norm_dev,
+                                  void *stream) {
+  if (!list || !list->table_dev || !norm_dev) return LLMINT8_ERR_NULL;
+  if (std::isnan(max_norm) || max_norm < 0.0f) return LLMINT8_ERR_ARG;
+  const size_t need = llmint8_grad_list_size(list->n);
+  if (need == 0 || list->chunks < 0) return LLMINT8_ERR_SHAPE;
+  if (!aligned(list->table_dev, 256) || !aligned(norm_dev, 4)) return LLMINT8_ERR_ALIGN;
+  if (list->table_bytes < need) return LLMINT8_ERR_WORKSPACE;
+  Device *dev = nullptr;
+  llmint8_status rc = current_device(&dev);
+  if (rc) return rc;
+  cudaStream_t st = as_stream(stream);
+  double *partial = static_cast<double *>(list->table_dev);
+  const clip::Entry *table = reinterpret_cast<const clip::Entry *>(
+      static_cast<const uint8_t *>(list->table_dev) + clip::kPartialBytes);
+  // as many blocks as fit the GPU at once, four per SM, and one at least
+  const int64_t blocks = std::max<int64_t>(
+      1, std::min<int64_t>({list->chunks, 4 * (int64_t)dev->sm_count, clip::MAX_BLOCKS}));
+  if (launch(clip::k_square_sums, dim3((unsigned)blocks), dim3(clip::THREADS), 0, st, false, table,
+             list->n, list->chunks, partial) != cudaSuccess)
+    return LLMINT8_ERR_CUDA;
+  if (launch(clip::k_clip_scale, dim3((unsigned)blocks), dim3(clip::THREADS), 0, st, true, table,
+             list->n, list->chunks, (const double *)partial, (int32_t)blocks, max_norm,
+             norm_dev) != cudaSuccess)
+    return LLMINT8_ERR_CUDA;
+  return last_launch();
+}
+
+}  // extern "C"

@@ -1,0 +1,203 @@
+// The global norm of the gradients of many tensors, and clipping to it:
+//
+//   norm = sqrt(sum over all tensors and elements of g^2)
+//   coef = min(1, max_norm / (norm + 1e-6))       out = g * coef
+//
+// Bound: bytes. The list of tensors is laid out once, on the device, as a
+// table of entries with the running number of chunks (CHUNK elements) before
+// each. A launch cuts the chunks of all tensors into equal contiguous ranges,
+// one per block, so thousands of small tensors and a few large ones load the
+// GPU alike. The norm kernel leaves one fp64 partial sum per block; the
+// scaling kernel's blocks each add those partial sums in the same order, so
+// the result does not depend on timing, and take their ranges from the end
+// of the list, where the norm kernel's reads are still in L2.
+//
+// Squares are fp64: the square of an fp32 or bf16 gradient above 2^64 or
+// below 2^-75 has no fp32 value.
+#pragma once
+
+#include <cstdint>
+
+#include "ptx_sm100.cuh"
+#include "rows_common.cuh"
+
+namespace llmint8 {
+namespace clip {
+
+constexpr int THREADS = 512;
+constexpr int CHUNK = 8192;        // elements
+constexpr int MAX_BLOCKS = 1024;   // partial sums a list holds
+constexpr int INIT_ENTRIES = 48;   // entries one launch of k_list_init carries
+
+struct Entry {
+  const void *grad;
+  void *out;
+  int64_t n;
+  int64_t chunk0;  // chunks of the tensors before this one
+  int32_t type;
+  int32_t pad;
+};
+
+// The table: MAX_BLOCKS partial sums, then the entries.
+constexpr size_t kPartialBytes = MAX_BLOCKS * sizeof(double);
+
+struct InitBatch {
+  Entry e[INIT_ENTRIES];
+};
+
+__global__ void k_list_init(Entry *table, const __grid_constant__ InitBatch batch, int32_t n) {
+  const int i = threadIdx.x;
+  if (i < n) table[i] = batch.e[i];
+}
+
+// The entry that holds chunk c: the last one with chunk0 <= c and n > 0
+// (entries without elements share their successor's chunk0).
+__device__ __forceinline__ int64_t find_entry(const Entry *table, int64_t n, int64_t c) {
+  int64_t lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi + 1) >> 1;
+    if (table[mid].chunk0 <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f(float &d, float v) { d = v; }
+__device__ __forceinline__ void from_f(__half &d, float v) { d = __float2half_rn(v); }
+__device__ __forceinline__ void from_f(__nv_bfloat16 &d, float v) { d = __float2bfloat16_rn(v); }
+
+template <typename T>
+struct Pack {
+  static constexpr int N = 16 / sizeof(T);
+  union {
+    uint4 q;
+    T v[N];
+  };
+  __device__ __forceinline__ Pack() {}
+};
+
+// Sum of squares of elements [0, m) of g, m <= CHUNK.
+template <typename T>
+__device__ __forceinline__ double chunk_square_sum(const T *g, int m) {
+  double acc = 0.0;
+  constexpr int N = Pack<T>::N;
+  int done = 0;
+  if ((reinterpret_cast<uintptr_t>(g) & 15) == 0) {
+    const int nv = m / N;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nv; i += THREADS) {
+      Pack<T> p;
+      p.q = reinterpret_cast<const uint4 *>(g)[i];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const double d = (double)to_f(p.v[e]);
+        acc = fma(d, d, acc);
+      }
+    }
+    done = nv * N;
+  }
+  for (int i = done + threadIdx.x; i < m; i += THREADS) {
+    const double d = (double)to_f(g[i]);
+    acc = fma(d, d, acc);
+  }
+  return acc;
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const T *g, T *out, int m, float coef) {
+  constexpr int N = Pack<T>::N;
+  int done = 0;
+  if (((reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
+    const int nv = m / N;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < nv; i += THREADS) {
+      Pack<T> p;
+      p.q = reinterpret_cast<const uint4 *>(g)[i];
+#pragma unroll
+      for (int e = 0; e < N; ++e) from_f(p.v[e], to_f(p.v[e]) * coef);
+      reinterpret_cast<uint4 *>(out)[i] = p.q;
+    }
+    done = nv * N;
+  }
+  for (int i = done + threadIdx.x; i < m; i += THREADS) from_f(out[i], to_f(g[i]) * coef);
+}
+
+__global__ void __launch_bounds__(THREADS)
+    k_square_sums(const Entry *__restrict__ table, int64_t n, int64_t chunks,
+                  double *__restrict__ partial) {
+  __shared__ double red[32];
+  const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
+  double acc = 0.0;
+  int64_t t = c0 < c1 ? find_entry(table, n, c0) : 0;
+  for (int64_t c = c0; c < c1; ++c) {
+    while (t + 1 < n && table[t + 1].chunk0 <= c) ++t;
+    const Entry e = table[t];
+    const int64_t at = (c - e.chunk0) * CHUNK;
+    const int m = (int)(e.n - at < CHUNK ? e.n - at : CHUNK);
+    if (e.type == LLMINT8_F16)
+      acc += chunk_square_sum(static_cast<const __half *>(e.grad) + at, m);
+    else if (e.type == LLMINT8_BF16)
+      acc += chunk_square_sum(static_cast<const __nv_bfloat16 *>(e.grad) + at, m);
+    else
+      acc += chunk_square_sum(static_cast<const float *>(e.grad) + at, m);
+  }
+  acc = warp_sum(acc);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = acc;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const double v = warp_sum((int)threadIdx.x < THREADS / 32 ? red[threadIdx.x] : 0.0);
+    if (threadIdx.x == 0) partial[blockIdx.x] = v;
+  }
+}
+
+__global__ void __launch_bounds__(THREADS)
+    k_clip_scale(const Entry *__restrict__ table, int64_t n, int64_t chunks,
+                 const double *__restrict__ partial, int32_t n_partial, float max_norm,
+                 float *__restrict__ norm_out) {
+  __shared__ double red[32];
+  __shared__ float s_coef;
+  grid_dependency_wait();
+  double acc = 0.0;
+  for (int i = threadIdx.x; i < n_partial; i += THREADS) acc += partial[i];
+  acc = warp_sum(acc);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = acc;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const double v = warp_sum((int)threadIdx.x < THREADS / 32 ? red[threadIdx.x] : 0.0);
+    if (threadIdx.x == 0) {
+      const double norm = sqrt(v);
+      const double c = (double)max_norm / (norm + 1e-6);
+      // max_norm = inf asks for the norm alone; a NaN norm gives a NaN coefficient
+      s_coef = c > 1.0 || isinf(max_norm) ? 1.0f : (float)c;
+      if (blockIdx.x == 0) *norm_out = (float)norm;
+    }
+  }
+  __syncthreads();
+  const float coef = s_coef;
+  const int64_t b = gridDim.x - 1 - blockIdx.x;
+  const int64_t c0 = chunks * b / gridDim.x, c1 = chunks * (b + 1) / gridDim.x;
+  if (c0 >= c1) return;
+  int64_t t = find_entry(table, n, c1 - 1);
+  for (int64_t c = c1 - 1; c >= c0; --c) {
+    while (t > 0 && table[t].chunk0 > c) --t;
+    const Entry e = table[t];
+    if (coef == 1.0f && e.out == e.grad) continue;  // nothing to change in place
+    const int64_t at = (c - e.chunk0) * CHUNK;
+    const int m = (int)(e.n - at < CHUNK ? e.n - at : CHUNK);
+    if (e.type == LLMINT8_F16)
+      chunk_scale(static_cast<const __half *>(e.grad) + at, static_cast<__half *>(e.out) + at, m,
+                  coef);
+    else if (e.type == LLMINT8_BF16)
+      chunk_scale(static_cast<const __nv_bfloat16 *>(e.grad) + at,
+                  static_cast<__nv_bfloat16 *>(e.out) + at, m, coef);
+    else
+      chunk_scale(static_cast<const float *>(e.grad) + at, static_cast<float *>(e.out) + at, m,
+                  coef);
+  }
+}
+
+}  // namespace clip
+}  // namespace llmint8

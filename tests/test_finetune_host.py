@@ -1,0 +1,185 @@
+"""Host-side checks of the operators next to the projection that need no GPU:
+workspace sizes and the refusal of invalid arguments before anything is
+enqueued. Placeholder pointers are never dereferenced; the calls are skipped
+when a GPU is visible."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from mixed_precision_int8_b200 import binding, build
+
+FAKE = ctypes.c_void_p(1 << 20)  # 256-byte aligned, never dereferenced
+ODD = ctypes.c_void_p((1 << 20) + 2)
+BIG = 1 << 40
+
+needs_no_gpu = pytest.mark.skipif(torch.cuda.is_available(),
+                                  reason="placeholder pointers: CPU box only")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return binding.load_library()
+
+
+def test_workspace_sizes(lib):
+    assert lib.llmint8_adapters_workspace_size(0, 256, 256, 1, 8) > 0
+    assert (lib.llmint8_adapters_workspace_size(4096, 256, 256, 1, 64)
+            > lib.llmint8_adapters_workspace_size(16, 256, 256, 1, 64))
+    for bad in ((-1, 256, 256, 1, 8), (2 ** 31, 256, 256, 1, 8), (4, 250, 256, 1, 8),
+                (4, 256, 8, 1, 8), (4, 256, 256, 0, 8), (4, 256, 256, 65536, 8),
+                (4, 256, 256, 1, 0), (4, 256, 256, 1, 12), (4, 256, 256, 1, 136)):
+        assert lib.llmint8_adapters_workspace_size(*bad) == 0
+    assert lib.llmint8_matmul_backward_workspace_size(128, 256, 256) > 0
+    assert lib.llmint8_matmul_backward_workspace_size(-1, 256, 256) == 0
+    assert lib.llmint8_matmul_backward_workspace_size(1, 256, 250) == 0
+    assert lib.llmint8_layernorm_workspace_size(128, 256) > 0
+    assert lib.llmint8_layernorm_workspace_size(128, 133160) == 0
+    assert lib.llmint8_grad_list_size(0) > 0
+    assert lib.llmint8_grad_list_size(-1) == 0
+    assert lib.llmint8_grad_list_size(2 ** 24 + 1) == 0
+
+
+def _adapters(h=256, o=256, n=2, r=8, a=FAKE, b=FAKE, scale=FAKE, rank=None):
+    return binding.llmint8_adapters(h, o, n, r, a, b, scale, rank)
+
+
+@needs_no_gpu
+def test_adapters_forward_refusals(lib):
+    def call(ad=None, s=4, X=FAKE, ids=FAKE, base=FAKE, out=ctypes.c_void_p(1 << 24), v=None,
+             ws=FAKE, nb=BIG):
+        ad = ad if ad is not None else _adapters()
+        return lib.llmint8_adapters_forward(X, s, ctypes.byref(ad), ids, base, out, v, ws, nb,
+                                            None)
+    assert lib.llmint8_adapters_forward(FAKE, 4, None, FAKE, None, FAKE, None, FAKE, BIG,
+                                        None) == -1
+    for kw in ("a", "b", "scale"):
+        assert call(_adapters(**{kw: None})) == -1
+    for kw in (dict(h=250), dict(o=8), dict(n=0), dict(n=65536), dict(r=4), dict(r=12),
+               dict(r=136)):
+        assert call(_adapters(**kw)) == -2
+    for kw in (dict(a=ODD), dict(b=ODD), dict(scale=ODD), dict(rank=ODD)):
+        assert call(_adapters(**kw)) == -3
+    assert call(s=-1) == -2 and call(s=2 ** 31) == -2
+    for kw in ("X", "ids", "out", "ws"):
+        assert call(**{kw: None}) == -1
+    for kw in ("X", "ids", "base", "out", "v", "ws"):
+        assert call(**{kw: ODD}) == -3
+    need = lib.llmint8_adapters_workspace_size(4, 256, 256, 2, 8)
+    assert call(nb=need - 1) == -4
+    # an output that overlaps its base without being it
+    assert call(base=ctypes.c_void_p((1 << 24) + 512)) == -7
+    assert call(X=ctypes.c_void_p(1 << 24)) == -7
+    assert call(s=0, X=None, ids=None, out=None, ws=None) == 0
+
+
+@needs_no_gpu
+def test_adapters_backward_refusals(lib):
+    far = [ctypes.c_void_p((k + 16) << 24) for k in range(3)]
+
+    def call(ad=None, s=4, X=FAKE, dY=FAKE, ids=FAKE, v=FAKE, base=FAKE, dX=far[0], dA=far[1],
+             dB=far[2], ws=FAKE, nb=BIG):
+        ad = ad if ad is not None else _adapters()
+        return lib.llmint8_adapters_backward(X, dY, s, ctypes.byref(ad), ids, v, base, dX, dA,
+                                             dB, ws, nb, None)
+    assert call(_adapters(r=12)) == -2
+    for kw in ("dY", "ids", "ws"):
+        assert call(**{kw: None}) == -1
+    assert call(X=None) == -1  # needed for dA
+    assert call(X=None, dA=None, v=None) == -1  # and for v
+    for kw in ("X", "dY", "ids", "v", "base", "dX", "dA", "dB", "ws"):
+        assert call(**{kw: ODD}) == -3
+    assert call(nb=lib.llmint8_adapters_workspace_size(4, 256, 256, 2, 8) - 1) == -4
+    assert call(dX=FAKE, base=None) == -7  # the gradient's own rows
+    assert call(base=ctypes.c_void_p((16 << 24) + 256)) == -7
+    assert call(s=-1) == -2
+
+
+@needs_no_gpu
+def test_matmul_backward_refusals(lib):
+    def call(w=None, s=4, dY=FAKE, base=None, dX=ctypes.c_void_p(1 << 24), ws=FAKE, nb=BIG):
+        w = w if w is not None else binding.llmint8_weight(256, 256, FAKE, FAKE)
+        return lib.llmint8_matmul_backward(dY, s, ctypes.byref(w), base, dX, ws, nb, None)
+    assert lib.llmint8_matmul_backward(FAKE, 4, None, None, FAKE, FAKE, BIG, None) == -1
+    assert call(binding.llmint8_weight(256, 256, None, FAKE)) == -1
+    assert call(binding.llmint8_weight(250, 256, FAKE, FAKE)) == -2
+    assert call(binding.llmint8_weight(256, 256, ODD, FAKE)) == -3
+    for kw in ("dY", "dX", "ws"):
+        assert call(**{kw: None}) == -1
+    for kw in ("dY", "base", "dX", "ws"):
+        assert call(**{kw: ODD}) == -3
+    assert call(nb=lib.llmint8_matmul_backward_workspace_size(4, 256, 256) - 1) == -4
+    assert call(dX=FAKE) == -7  # overlaps dY
+    assert call(base=ctypes.c_void_p((1 << 24) + 256)) == -7
+    assert call(s=-1) == -2
+    assert call(s=0, dY=None, dX=None, ws=None) == 0
+
+
+@needs_no_gpu
+def test_layernorm_refusals(lib):
+    def fwd(x=FAKE, xt=0, s=4, h=256, g=FAKE, b=FAKE, pt=0, eps=1e-5, y=FAKE, mean=FAKE,
+            rstd=FAKE):
+        return lib.llmint8_layernorm_forward(x, xt, s, h, g, b, pt, eps, y, mean, rstd, None)
+    assert fwd(h=250) == -2 and fwd(h=133160) == -2 and fwd(s=-1) == -2
+    assert fwd(xt=2) == -7 and fwd(pt=2) == -7 and fwd(xt=-1) == -7
+    for bad in (-1.0, math.nan, math.inf):
+        assert fwd(eps=bad) == -7
+    for kw in ("x", "g", "y"):
+        assert fwd(**{kw: None}) == -1
+    for kw in ("x", "g", "b", "y", "mean", "rstd"):
+        assert fwd(**{kw: ODD}) == -3
+    assert fwd(s=0, x=None, g=None, y=None) == 0
+
+    def bwd(dy=FAKE, x=FAKE, xt=0, s=4, h=256, g=FAKE, pt=0, mean=FAKE, rstd=FAKE, dx=FAKE,
+            dg=FAKE, db=FAKE, ws=FAKE, nb=BIG):
+        return lib.llmint8_layernorm_backward(dy, x, xt, s, h, g, pt, mean, rstd, dx, dg, db,
+                                              ws, nb, None)
+    assert bwd(h=250) == -2 and bwd(xt=2) == -7 and bwd(pt=3) == -7
+    for kw in ("dy", "x", "g", "mean", "rstd", "ws"):
+        assert bwd(**{kw: None}) == -1
+    for kw in ("dy", "x", "g", "mean", "rstd", "dx", "dg", "db", "ws"):
+        assert bwd(**{kw: ODD}) == -3
+    assert bwd(nb=lib.llmint8_layernorm_workspace_size(4, 256) - 1) == -4
+
+
+@needs_no_gpu
+def test_clip_refusals(lib):
+    lst = binding.llmint8_grad_list(FAKE, BIG, 1, 1)
+    init = lib.llmint8_grad_list_init
+    item = binding.llmint8_grad(FAKE, FAKE, 10, 1)
+
+    def one(**kw):
+        g = binding.llmint8_grad(kw.get("grad", FAKE), kw.get("out", FAKE), kw.get("n", 10),
+                                 kw.get("type", 1))
+        return init(ctypes.byref(g), 1, ctypes.byref(lst), None)
+    assert init(None, 1, ctypes.byref(lst), None) == -1
+    assert init(ctypes.byref(item), 1, None, None) == -1
+    assert init(ctypes.byref(item), -1, ctypes.byref(lst), None) == -2
+    assert one(type=3) == -7 and one(n=-1) == -2 and one(grad=None) == -1
+    assert one(grad=ODD) == -3 and one(out=ODD) == -3
+    assert one(out=ctypes.c_void_p((1 << 20) + 4)) == -7  # a shifted overlap
+    small = binding.llmint8_grad_list(FAKE, lib.llmint8_grad_list_size(1) - 1, 0, 0)
+    assert init(ctypes.byref(item), 1, ctypes.byref(small), None) == -4
+    off = binding.llmint8_grad_list(ODD, BIG, 0, 0)
+    assert init(ctypes.byref(item), 1, ctypes.byref(off), None) == -3
+    clip = lib.llmint8_clip_grads
+    assert clip(None, 1.0, FAKE, None) == -1
+    assert clip(ctypes.byref(lst), 1.0, None, None) == -1
+    for bad in (-1.0, math.nan):
+        assert clip(ctypes.byref(lst), bad, FAKE, None) == -7
+    assert clip(ctypes.byref(lst), 1.0, ctypes.c_void_p((1 << 20) + 1), None) == -3
+    assert clip(ctypes.byref(small), 1.0, FAKE, None) != 0
+
+
+def test_binding_refuses_tensors_it_cannot_take():
+    A = torch.zeros(2, 8, 32, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        binding.Adapters(A, A, torch.ones(2))  # not on a GPU
+    with pytest.raises(ValueError):
+        binding.Adapters(A[0], A, torch.ones(2))
+    with pytest.raises(ValueError):
+        binding.llmint8_layernorm_forward(torch.zeros(4, 32), torch.ones(32))
+    with pytest.raises(ValueError):
+        binding.llmint8_layernorm_forward(torch.zeros(32), torch.ones(32))

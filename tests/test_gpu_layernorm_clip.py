@@ -1,0 +1,277 @@
+"""Layer norm (forward, backward) and gradient clipping on the GPU, against
+the formulas in 64 bits.
+
+Bounds, u = 2^-24 (half a step of fp32): a block sums a row of h values in
+chains of at most h / 512 terms per thread (64 up to h = 32768) and a tree of
+ten levels, so |mean err| <= 74 u mean|x|, and the sum of squares is off by at
+most 74 u relative, rstd by half of that and three more roundings. With
+N = 80 u:
+    |xh err|  <= N (mean|x| rstd + |xh|)
+    |y err|   <= |gamma| * that + 3 u (|xh gamma| + |beta|) + one fp16 rounding
+and for the backward pass the same counts around each of its terms.
+"""
+import math
+
+import pytest
+import torch
+
+from mixed_precision_int8_b200 import binding as L, build
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+N = 80 * U
+D = torch.float64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    build.build()
+    L.load_library()
+    yield
+
+
+def rounding(ref, dtype):
+    """Half a step of the type at ref, half of its smallest subnormal at 0."""
+    tiny = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134, torch.float32: 2.0 ** -150}
+    return torch.finfo(dtype).eps / 2 * ref.abs() + tiny[dtype]
+
+
+def ln_inputs(s, h, xt, pt, kind, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + 7 * s + h)
+    X = torch.randn(s, h, generator=g, device="cuda")
+    if kind == "shifted":  # a mean far larger than the spread
+        X = X * 0.5 + 200
+    elif kind == "constant":
+        X = torch.full((s, h), 3.140625, device="cuda")
+    elif kind == "outliers":
+        X[:, :: max(1, h // 5)] *= 60
+    elif kind == "small":
+        X = X * 1e-4
+    gamma = (1 + 0.1 * torch.randn(h, generator=g, device="cuda")).to(pt)
+    beta = (0.1 * torch.randn(h, generator=g, device="cuda")).to(pt)
+    dY = (torch.randn(s, h, generator=g, device="cuda") * 0.1).half()
+    return X.to(xt), gamma, beta, dY
+
+
+SHAPES = [(1, 16), (3, 272), (8, 12288), (5, 16384), (3, 16400), (2, 49152), (700, 528),
+          (33, 4096), (1, 133136)]
+TYPES = [(torch.float16, torch.float16), (torch.float32, torch.float32),
+         (torch.float32, torch.float16), (torch.float16, torch.float32)]
+
+
+@pytest.mark.parametrize("s,h", SHAPES)
+@pytest.mark.parametrize("xt,pt", TYPES)
+def test_layernorm(s, h, xt, pt):
+    for kind in ("normal", "shifted", "constant", "outliers", "small"):
+        X, gamma, beta, dY = ln_inputs(s, h, xt, pt, kind)
+        eps = 1e-5
+        n = N if h <= 32768 else N * h / 32768
+        y, mean, rstd = L.llmint8_layernorm_forward(X, gamma, beta, eps)
+        Xd, gd, bd = X.to(D), gamma.to(D), beta.to(D)
+        rm = Xd.mean(1, keepdim=True)
+        rv = ((Xd - rm) ** 2).mean(1, keepdim=True)
+        rq = (rv + eps) ** -0.5
+        ma = Xd.abs().mean(1, keepdim=True)
+        xh = (Xd - rm) * rq
+        assert ((mean.to(D)[:, None] - rm).abs() <= n * ma).all()
+        # the mean's error e adds at most e^2 to the variance
+        assert ((rstd.to(D)[:, None] / rq - 1).abs() <= n + (n * ma * rq) ** 2).all()
+        exh = n * (ma * rq + xh.abs()) + (n * ma * rq) ** 2 * xh.abs()
+        ref = xh * gd + bd
+        lim = gd.abs() * exh + 3 * U * ((xh * gd).abs() + bd.abs()) + rounding(ref, torch.float16)
+        assert ((y.to(D) - ref).abs() <= lim * (1 + 2.0 ** -10)).all(), kind
+        # backward, from the statistics that the forward pass left
+        dX, dg, db = L.llmint8_layernorm_backward(dY, X, gamma, mean, rstd)
+        m, q = mean.to(D)[:, None], rstd.to(D)[:, None]
+        dYd = dY.to(D)
+        xh = (Xd - m) * q
+        g = dYd * gd
+        c1, c2 = g.mean(1, keepdim=True), (g * xh).mean(1, keepdim=True)
+        ref = q * (g - c1 - xh * c2)
+        a1, a2 = g.abs().mean(1, keepdim=True), (g * xh).abs().mean(1, keepdim=True)
+        lim = n * q * (g.abs() + a1 + xh.abs() * a2) + rounding(ref, xt)
+        assert dX.dtype == xt
+        assert ((dX.to(D) - ref).abs() <= lim * (1 + 2.0 ** -10)).all(), kind
+        # column sums: at most s roundings in a block's chain and 64 over the blocks
+        k = (s + 64) * U
+        rg, ag = (dYd * xh).sum(0), (dYd * xh).abs().sum(0)
+        assert ((dg.to(D) - rg).abs() <= (k + 3 * U) * ag).all(), kind
+        assert ((db.to(D) - dYd.sum(0)).abs() <= k * dYd.abs().sum(0)).all(), kind
+
+
+def test_layernorm_without_beta_and_its_rows_alone():
+    """No beta; the rows around the call's output stay; NaN of one row stays
+    in it (its column sums excepted)."""
+    X, gamma, _, dY = ln_inputs(9, 528, torch.float16, torch.float16, "normal")
+    X[4, 7] = float("nan")
+    buf = torch.full((11, 528), 5.0, dtype=torch.float16, device="cuda")
+    y, mean, rstd = L.llmint8_layernorm_forward(X, gamma, out=buf[1:-1])
+    assert (buf[0] == 5).all() and (buf[-1] == 5).all()
+    ok = [i for i in range(9) if i != 4]
+    ref, _, _ = L.llmint8_layernorm_forward(X[ok].contiguous(), gamma, torch.zeros_like(gamma))
+    assert torch.equal(y[ok], ref)
+    assert y[4].isnan().all()
+    dbuf = torch.full((11, 528), 5.0, dtype=torch.float16, device="cuda")
+    L.llmint8_layernorm_backward(dY, X, gamma, mean, rstd, dX=dbuf[1:-1])
+    assert (dbuf[0] == 5).all() and (dbuf[-1] == 5).all()
+    one, _, _ = L.llmint8_layernorm_backward(dY[ok].contiguous(), X[ok].contiguous(), gamma,
+                                             mean[ok].contiguous(), rstd[ok].contiguous())
+    assert torch.equal(dbuf[1:-1][ok], one)
+
+
+def test_layernorm_gradient_against_differences():
+    """Central differences of sum(y dY) in 64 bits, next to the kernels'
+    gradients of the same inputs."""
+    X, gamma, beta, dY = ln_inputs(4, 64, torch.float32, torch.float32, "normal")
+    _, mean, rstd = L.llmint8_layernorm_forward(X, gamma, beta, 1e-5)
+    dX, dg, db = L.llmint8_layernorm_backward(dY, X, gamma, mean, rstd)
+
+    def loss(x, g, b):
+        m = x.mean(1, keepdim=True)
+        v = ((x - m) ** 2).mean(1, keepdim=True)
+        return (((x - m) / torch.sqrt(v + 1e-5) * g + b) * dY.to(D)).sum()
+
+    args = [X.to(D), gamma.to(D), beta.to(D)]
+    for k, (grad, at) in enumerate(((dX, (2, 5)), (dg, (9,)), (db, (9,)))):
+        step = 1e-5
+        up = [t.clone() for t in args]
+        dn = [t.clone() for t in args]
+        up[k][at] += step
+        dn[k][at] -= step
+        diff = float(loss(*up) - loss(*dn)) / (2 * step)
+        # step^2 times a third derivative of order 1, plus the kernels' bounds
+        assert abs(diff - float(grad[at])) <= 1e-7 + 1e-4 * abs(diff) * 0.1
+
+
+def test_layernorm_no_rows():
+    X, gamma, beta, dY = ln_inputs(2, 64, torch.float16, torch.float16, "normal")
+    y, mean, rstd = L.llmint8_layernorm_forward(X[:0], gamma, beta)
+    assert y.shape == (0, 64) and mean.shape == (0,)
+    ws = L.LayerNormWorkspace(1, 64)
+    _, dg, db = L.llmint8_layernorm_backward(dY[:0], X[:0], gamma, mean, rstd, workspace=ws)
+    assert not dg.any() and not db.any()
+
+
+# ------------------------------------------------------------ clipping
+
+def clip_reference(grads, max_norm):
+    norm = math.sqrt(sum(float((g.to(D) ** 2).sum()) for g in grads))
+    return norm, min(1.0, max_norm / (norm + 1e-6))
+
+
+def check_clip(grads, outs, norm, before, max_norm):
+    ref, coef = clip_reference(before, max_norm)
+    # fp64 sums, one rounding of the norm and one of the coefficient
+    assert abs(float(norm) - ref) <= 2 * U * ref
+    for g, out, b in zip(grads, outs, before):
+        want = b.to(D) * coef
+        assert ((out.to(D) - want).abs() <= rounding(want, b.dtype) + 4 * U * want.abs()).all()
+
+
+@pytest.mark.parametrize("count", [1, 3, 49, 500])
+@pytest.mark.parametrize("factor", [0.5, 2.0])
+def test_clip_many_tensors(count, factor):
+    """Types mixed; sizes from nothing to several pieces; views that start at
+    any element."""
+    g = torch.Generator(device="cuda").manual_seed(count)
+    types = (torch.float16, torch.float32, torch.bfloat16)
+    sizes = (0, 1, 7, 4096, 8191, 8192, 8193, 40001, 3)
+    grads = []
+    for i in range(count):
+        m, off = sizes[(i + 3) % len(sizes)], i % 9
+        buf = torch.randn(m + off + 9, generator=g, device="cuda").to(types[i % 3])
+        grads.append(buf[off:off + m])
+    before = [x.clone() for x in grads]
+    max_norm = factor * clip_reference(before, 1.0)[0]
+    outs = [torch.full_like(x, 7.0) for x in grads]
+    norm = L.llmint8_clip_grads(L.GradList(grads, outs), max_norm)
+    check_clip(grads, outs, norm, before, max_norm)
+    assert all(torch.equal(x, y) for x, y in zip(grads, before))
+    # in place, twice from the same list
+    lst = L.GradList(grads)
+    first = L.llmint8_clip_grads(lst, max_norm)
+    check_clip(grads, grads, first, before, max_norm)
+    assert torch.equal(first, norm)
+    again = L.llmint8_clip_grads(lst, float("inf"))
+    assert float(again) <= max_norm * (1 + 2.0 ** -8)
+
+
+def test_clip_neighbours_stay():
+    buf = torch.full((40000,), 3.0, dtype=torch.float16, device="cuda")
+    L.llmint8_clip_grads(L.GradList([buf[5:20001], buf[20003:39990]]), 1.0)
+    for lo, hi in ((0, 5), (20001, 20003), (39990, 40000)):
+        assert (buf[lo:hi] == 3).all()
+    assert (buf[5:20001] < 0.1).all() and (buf[20003:39990] < 0.1).all()
+
+
+def test_clip_edges():
+    none = L.llmint8_clip_grads(L.GradList([]), 1.0)
+    assert float(none) == 0.0
+    empty = L.llmint8_clip_grads(L.GradList([torch.empty(0, device="cuda")]), 1.0)
+    assert float(empty) == 0.0
+    z = torch.zeros(1000, device="cuda")
+    assert float(L.llmint8_clip_grads(L.GradList([z]), 1.0)) == 0.0 and not z.any()
+    # max_norm 0 and inf
+    g = torch.ones(100, device="cuda")
+    assert float(L.llmint8_clip_grads(L.GradList([g]), float("inf"))) == 10.0
+    assert (g == 1).all()
+    L.llmint8_clip_grads(L.GradList([g]), 0.0)
+    assert not g.any()
+    # squares that no fp32 number holds
+    for big in (1e30, 1e-30):
+        g = torch.full((4,), big, device="cuda")
+        norm = L.llmint8_clip_grads(L.GradList([g]), float("inf"))
+        assert abs(float(norm) / (2 * big) - 1) < 1e-6
+    # a gradient that overflowed: the norm says so
+    g = torch.ones(5, device="cuda")
+    g[2] = float("inf")
+    assert math.isinf(float(L.llmint8_clip_grads(L.GradList([g]), 1.0)))
+    assert g[2].isnan() and g[0] == 0
+    g = torch.ones(5, device="cuda")
+    g[2] = float("nan")
+    assert math.isnan(float(L.llmint8_clip_grads(L.GradList([g]), 1.0)))
+    assert g.isnan().all()
+
+
+def test_clip_offsets_past_32_bits():
+    g = torch.ones(2 ** 31 + 5000, dtype=torch.float16, device="cuda")
+    g[-1] = 1000
+    norm = L.llmint8_clip_grads(L.GradList([g]), float(2 ** 20))
+    want = math.sqrt(2 ** 31 + 4999 + 1e6)
+    assert abs(float(norm) / want - 1) <= 2 * U
+    assert g[-1] == 1000 and (g[-100:-1] == 1).all()
+    L.llmint8_clip_grads(L.GradList([g]), want / 2)
+    assert g[-1] == 500 and (g[-100:-1] == 0.5).all() and (g[:100] == 0.5).all()
+
+
+def test_norm_layer_and_clip_on_a_stream_and_in_a_graph():
+    X, gamma, beta, dY = ln_inputs(300, 528, torch.float16, torch.float16, "normal")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y, mean, rstd = L.llmint8_layernorm_forward(X, gamma, beta, stream=side)
+    ws = L.LayerNormWorkspace(300, 528)
+    torch.cuda.current_stream().wait_stream(side)
+    grads = [torch.empty(528, device="cuda"), torch.empty(528, device="cuda")]
+    lst = L.GradList(grads)
+    torch.cuda.synchronize()
+
+    def step():
+        y, mean, rstd = L.llmint8_layernorm_forward(X, gamma, beta)
+        dX, dg, db = L.llmint8_layernorm_backward(dY, X, gamma, mean, rstd, workspace=ws)
+        grads[0].copy_(dg)
+        grads[1].copy_(db)
+        return y, dX, L.llmint8_clip_grads(lst, 0.5)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for k in (1, 2):
+        X.copy_(ln_inputs(300, 528, torch.float16, torch.float16, "normal", seed=k)[0])
+        graph.replay()
+        got = [t.clone() for t in held] + [g.clone() for g in grads]
+        for a, b in zip(got, list(step()) + grads):
+            assert torch.equal(a, b)
