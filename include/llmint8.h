@@ -488,10 +488,11 @@ LLMINT8_API llmint8_status llmint8_adapters_backward(
 
 /* Gradient of the projection's input through the frozen int8 weight:
  *   dX[i][k] = fp16(base[i][k] + sum_j dY[i][j] * WR[k][j])
- *   WR[k][j] = fp16(fp32(fp32(wq[j][k]) * aw[j]) / 127)
- * the fp16 weight that llmint8_matmul recovers for its outlier rows (w16_dev
- * is not used), with fp32 sums; the rounding of X to int8 counts as the
- * identity. dY_dev fp16 [s][o]; base_dev (fp16 [s][h]) another gradient to add
+ *   WR[k][j] = fp16(wq[j][k] * (aw[j] / 127))
+ * (the product of the code and an fp32 factor, rounded once: the fp16 weight
+ * that llmint8_matmul recovers for its outlier rows, but for the order of its
+ * fp32 roundings; w16_dev is not used), with fp32 sums; the rounding of X to
+ * int8 counts as the identity. dY_dev fp16 [s][o]; base_dev (fp16 [s][h]) another gradient to add
  * or NULL; dX_dev fp16 [s][h], may be base_dev itself, and overlaps no other
  * input (LLMINT8_ERR_ARG). */
 LLMINT8_API size_t llmint8_matmul_backward_workspace_size(int64_t s, int64_t h, int64_t o);

@@ -26,6 +26,7 @@ struct Device {
   bool init = false;
   bool supported = false;
   int sm_count = 0;
+  int max_pairs = 0;  // CTA pairs of k_input_grad that fit at once
 };
 Device g_device[kMaxDevices];
 std::mutex g_device_mutex;
@@ -42,6 +43,27 @@ llmint8_status current_device(Device **out) {
         cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return LLMINT8_ERR_CUDA;
     d.supported = major == 10 && minor == 0;
+    if (d.supported) {
+      if (cudaFuncSetAttribute(igrad::k_input_grad, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)igrad::SMEM_BYTES) != cudaSuccess)
+        return LLMINT8_ERR_CUDA;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(2 * (unsigned)(d.sm_count / 2));
+      cfg.blockDim = dim3(igrad::NUM_THREADS);
+      cfg.dynamicSmemBytes = igrad::SMEM_BYTES;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int clusters = 0;
+      if (cudaOccupancyMaxActiveClusters(&clusters, igrad::k_input_grad, &cfg) != cudaSuccess ||
+          clusters < 1)
+        return LLMINT8_ERR_CUDA;
+      d.max_pairs = std::min({clusters, d.sm_count / 2, igrad::MAX_PAIRS});
+    }
     d.init = true;
   }
   if (!d.supported) return LLMINT8_ERR_UNSUPPORTED;
@@ -130,6 +152,41 @@ llmint8_status enqueue_outer(const float *p, const uint16_t *Q, int64_t s, int64
              ad->rank_dev, ad->n, ad->r, d) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   return LLMINT8_OK;
+}
+
+// ---------------------------------------- gradient of the projection's input
+
+// Whole rounds of tiles first (one tile per pair); the tiles of the last,
+// partial round are cut along the reduction into as many parts as make the
+// rounds they then take shortest. A part costs an fp32 tile written and read
+// back, counted here as two stages. Planned for MAX_PAIRS pairs on any
+// device, so that the workspace size depends on the sizes alone.
+igrad::Plan input_grad_plan(int64_t s, int64_t h, int64_t o) {
+  igrad::Plan p;
+  p.num_m = (int32_t)((s + 2 * igrad::BM - 1) / (2 * igrad::BM));
+  p.num_n = (int32_t)((h + igrad::BN - 1) / igrad::BN);
+  p.num_k = (int32_t)((o + igrad::BK - 1) / igrad::BK);
+  const int64_t tiles = (int64_t)p.num_m * p.num_n;
+  p.whole = (int32_t)(tiles / igrad::MAX_PAIRS * igrad::MAX_PAIRS);
+  p.rest = (int32_t)(tiles - p.whole);
+  p.parts = 1;
+  int64_t best = INT64_MAX;
+  for (int32_t parts = 1; p.rest > 0 && parts <= p.num_k && p.rest * parts <= igrad::MAX_PARTS;
+       ++parts) {
+    const int64_t rounds = (p.rest * parts + igrad::MAX_PAIRS - 1) / igrad::MAX_PAIRS;
+    const int64_t cost = rounds * ((p.num_k + parts - 1) / parts + (parts > 1 ? 2 : 0)) +
+                         (parts > 1 ? 2 * parts : 0);
+    if (cost < best) {
+      best = cost;
+      p.parts = parts;
+    }
+  }
+  return p;
+}
+
+size_t input_grad_workspace(const igrad::Plan &p) {
+  const size_t slots = p.parts > 1 ? (size_t)p.rest * p.parts : 0;
+  return align256(kStateBytes + 4 * igrad::PART_ELEMS * slots);
 }
 
 // ----------------------------------------------------------- layer norm
@@ -276,7 +333,14 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
 
 size_t llmint8_matmul_backward_workspace_size(int64_t s, int64_t h, int64_t o) {
   if (check_hw(h, o) || check_rows(s)) return 0;
-  return kStateBytes;
+  // up to MAX_PARTS fp32 tiles: the most that any smaller number of rows needs
+  // (the plan repeats every MAX_PAIRS tiles of rows)
+  size_t bytes = 0;
+  const int64_t num_m = (s + 2 * igrad::BM - 1) / (2 * igrad::BM);
+  for (int64_t m = 0; m < std::min<int64_t>(num_m, igrad::MAX_PAIRS); ++m)
+    bytes = std::max(bytes, input_grad_workspace(
+                                input_grad_plan((num_m - m) * 2 * igrad::BM, h, o)));
+  return std::max(bytes, kStateBytes);
 }
 
 llmint8_status llmint8_matmul_backward(const uint16_t *dY_dev, int64_t s, const llmint8_weight *w,
@@ -296,14 +360,39 @@ llmint8_status llmint8_matmul_backward(const uint16_t *dY_dev, int64_t s, const 
   if (overlap(dX_dev, dx_bytes, dY_dev, 2 * (size_t)s * w->o) ||
       (base_dev != dX_dev && overlap(dX_dev, dx_bytes, base_dev, dx_bytes)))
     return LLMINT8_ERR_ARG;
-  if (ws_bytes < llmint8_matmul_backward_workspace_size(s, w->h, w->o))
-    return LLMINT8_ERR_WORKSPACE;
+  const igrad::Plan plan = input_grad_plan(s, w->h, w->o);
+  if (ws_bytes < input_grad_workspace(plan)) return LLMINT8_ERR_WORKSPACE;
   Device *dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
-  if (launch(igrad::k_input_grad_simple, dim3(blocks_for(w->h, 64), blocks_for(s, 64)), dim3(256),
-             0, as_stream(stream), false, as_half(dY_dev), s, (int32_t)w->h, (int32_t)w->o,
-             (const int8_t *)w->wq_dev, (const float *)w->aw_dev, as_half(base_dev),
-             as_half(dX_dev)) != cudaSuccess)
+  igrad::Params p;
+  p.s = (int32_t)s;
+  p.h = (int32_t)w->h;
+  p.o = (int32_t)w->o;
+  p.plan = plan;
+  p.wq = w->wq_dev;
+  p.aw = w->aw_dev;
+  p.base = as_half(base_dev);
+  p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws_dev) + kStateBytes);
+  p.status = static_cast<int32_t *>(ws_dev);
+  p.timeout_ns = kTimeoutNs;
+  CUtensorMap tmA, tmW, tmOut;
+  if (!make_tmap_i8_plain(&tmW, w->wq_dev, (uint64_t)w->h, (uint64_t)w->o, igrad::BNH,
+                          igrad::BK) ||
+      !make_tmap_f16(&tmA, const_cast<uint16_t *>(dY_dev), (uint64_t)w->o, (uint64_t)s, igrad::BK,
+                     igrad::BM) ||
+      !make_tmap_f16(&tmOut, dX_dev, (uint64_t)w->h, (uint64_t)s, 32, 32))
+    return LLMINT8_ERR_CUDA;
+  cudaStream_t st = as_stream(stream);
+  const int64_t units = p.plan.whole + (int64_t)p.plan.rest * p.plan.parts;
+  const int pairs = (int)std::min<int64_t>(units, dev->max_pairs);
+  if (launch_pairs(igrad::k_input_grad, dim3(2 * pairs), dim3(igrad::NUM_THREADS),
+                   igrad::SMEM_BYTES, st, false, tmA, tmW, tmOut, p) != cudaSuccess)
+    return LLMINT8_ERR_CUDA;
+  if (p.plan.parts > 1 &&
+      launch(igrad::k_input_grad_sum,
+             dim3(blocks_for((int64_t)p.plan.rest * 2 * igrad::BM * (igrad::BN / 8),
+                             igrad::SUM_THREADS)),
+             dim3(igrad::SUM_THREADS), 0, st, true, p, as_half(dX_dev)) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   return last_launch();
 }

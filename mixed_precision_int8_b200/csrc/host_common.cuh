@@ -40,9 +40,9 @@ EncodeTiledFn encode_fn() {
 }
 
 // 2-D int8 tensor [rows][inner] with row stride `inner` bytes, box
-// [box_rows][box_inner] landing in shared memory with the 128-byte swizzle.
-bool make_tmap_i8(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t rows,
-                  uint32_t box_inner, uint32_t box_rows) {
+// [box_rows][box_inner] landing in shared memory with the given swizzle.
+bool make_tmap_u8(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t rows,
+                  uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {inner, rows};
@@ -50,8 +50,19 @@ bool make_tmap_i8(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t ro
   cuuint32_t box[2] = {box_inner, box_rows};
   cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// With the 128-byte swizzle (operands of int8 MMAs), or as the box lies.
+bool make_tmap_i8(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t rows,
+                  uint32_t box_inner, uint32_t box_rows) {
+  return make_tmap_u8(map, ptr, inner, rows, box_inner, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+[[maybe_unused]] bool make_tmap_i8_plain(CUtensorMap *map, const void *ptr, uint64_t inner,
+                                         uint64_t rows, uint32_t box_inner, uint32_t box_rows) {
+  return make_tmap_u8(map, ptr, inner, rows, box_inner, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // 2-D fp16 tensor [rows][inner] (row stride 2*inner bytes) for TMA stores of
@@ -111,6 +122,27 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// The same for a kernel run by clusters of two CTAs along x.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pairs(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t st, bool pdl, Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 

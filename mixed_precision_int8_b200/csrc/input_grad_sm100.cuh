@@ -1,11 +1,44 @@
 // Gradient of an LLM.int8() projection's input, through the frozen int8
-// weight:
+// weight, on the tensor cores:
 //
-//   dX[i][k] = fp16(base[i][k] + sum_j dY[i][j] * W[k][j]),
-//   W[k][j]  = wq[j][k] * aw[j] / 127
+//   dX[i][k] = fp16(base[i][k] + sum_j dY[i][j] * WR[k][j])
+//   WR[k][j] = fp16(wq[j][k] * (aw[j] / 127))
+//
+// M = rows of dY, N = h, reduction over o. dY [s][o] is K-major as it lies.
+// wq [o][h] has the reduction index outside: its tiles are an MN-major
+// operand, so nothing is transposed; each int8 tile is turned into fp16 on
+// its way into shared memory.
+//
+// Bound: the fp16 tensor cores (2 s h o operations) at prefill sizes. A pair
+// of CTAs computes a 256 x 256 tile (tcgen05 cta_group::2), so that per stage
+// of 64 reduction indices a CTA stores and reads only its 128 x 64 half of
+// each operand: the converted weight costs shared memory no more than a
+// plain fp16 one would, and its global traffic is half. Two groups of eight
+// warps convert alternate stages: TMA brings the codes (and their column
+// scales) into a ring of their own, a lane takes 16 codes of it and writes 16
+// fp16 values through the 128-byte swizzle. The converters load nothing from
+// global memory themselves: the fence that makes their writes visible to the
+// tensor cores waits for all that a thread has in flight, and with register
+// loads running ahead it took as long as those (measured: 1170 us instead of
+// %%% at 4096 x 5120 x 20480).
+//
+//   warp 0      TMA producer of dY
+//   warp 1      one thread of rank 0 issues the MMAs
+//   warp 2      allocates TMEM (two 256-column accumulators); TMA producer of
+//               the codes
+//   warps 4-7   epilogue: TMEM -> + base -> fp16 -> TMA store
+//   warps 8-23  converters
+//
+// Tiles that do not fill a round of all pairs (the last ones, or all of a
+// small problem) are cut along o into equal parts, each of which leaves an
+// fp32 tile in the workspace; k_input_grad_sum adds them in order.
+//
+// Every wait is bounded; a role that gives up records a status bit, and the
+// CTA drains what it started and returns.
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "ptx_sm100.cuh"
@@ -14,49 +47,458 @@
 namespace llmint8 {
 namespace igrad {
 
-// 64 x 64 output tile per block of 256 threads, 16 output columns of W per
-// step, 4 x 4 outputs per thread.
-__global__ void __launch_bounds__(256)
-    k_input_grad_simple(const __half *dY, int64_t s, int32_t h, int32_t o, const int8_t *wq,
-                        const float *aw, const __half *base, __half *dX) {
-  __shared__ float sY[16][68];
-  __shared__ float sW[16][68];
-  const int64_t i0 = (int64_t)blockIdx.y * 64;
-  const int k0 = blockIdx.x * 64;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  float acc[4][4] = {};
-  for (int j0 = 0; j0 < o; j0 += 16) {
-    for (int e = threadIdx.x; e < 64 * 16; e += 256) {
-      const int64_t i = i0 + e / 16;
-      sY[e % 16][e / 16] = i < s ? __half2float(dY[i * o + j0 + e % 16]) : 0.0f;
-      const int j = j0 + e / 64, k = k0 + e % 64;
-      sW[e / 64][e % 64] = k < h ? (float)wq[(int64_t)j * h + k] * (aw[j] / 127.0f) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      float a[4], b[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        a[u] = sY[j][ty * 4 + u];
-        b[u] = sW[j][tx * 4 + u];
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) acc[u][w] = fmaf(a[u], b[w], acc[u][w]);
-    }
-    __syncthreads();
+constexpr int BM = 128;   // rows per CTA (256 per pair)
+constexpr int BN = 256;   // columns of h per pair
+constexpr int BNH = 128;  // columns whose weight this CTA converts
+constexpr int BK = 64;    // reduction indices per stage
+constexpr int UMMA_K = 16;
+constexpr int STAGES = 5;
+constexpr int RAW_STAGES = 5;  // stages of int8 codes in flight
+constexpr int NUM_ACC = 2;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t A_STAGE_BYTES = BM * BK * 2;
+constexpr uint32_t B_STAGE_BYTES = BNH * BK * 2;
+constexpr uint32_t B_BLOCK_BYTES = 64 * BK * 2;  // 64 columns x 64 reduction rows
+constexpr int EPI_WARP0 = 4, EPI_THREADS = 128;
+constexpr int CVT_WARP0 = 8, CVT_WARPS = 8, CVT_THREADS = 32 * CVT_WARPS;
+constexpr int CVT_GROUPS = 2;
+constexpr int NUM_THREADS = 32 * (CVT_WARP0 + CVT_GROUPS * CVT_WARPS);
+constexpr uint32_t FULL_ARRIVALS = 1 + 2 * CVT_WARPS;
+constexpr uint32_t OUT_STAGE_BYTES = 32 * 32 * 2;  // per epilogue warp
+constexpr uint32_t RAW_BYTES = BNH * BK;                 // codes of a stage
+constexpr uint32_t RAW_STAGE_BYTES = RAW_BYTES + 1024;   // + BK column scales
+constexpr uint32_t RAW_OFF = STAGES * (A_STAGE_BYTES + B_STAGE_BYTES);
+constexpr uint32_t OUT_OFF = RAW_OFF + RAW_STAGES * RAW_STAGE_BYTES;
+constexpr uint32_t BAR_OFF = OUT_OFF + 4 * OUT_STAGE_BYTES;
+constexpr size_t SMEM_BYTES = 1024 + BAR_OFF + 256;
+constexpr int MAX_PAIRS = 74;
+constexpr int MAX_PARTS = 2 * MAX_PAIRS;  // fp32 tiles the workspace holds
+constexpr size_t PART_ELEMS = 2 * BM * BN;
+
+static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+static_assert((2 * STAGES + 2 * RAW_STAGES + 2 * NUM_ACC + 1) * 8 + 8 <= 256, "barrier block size");
+
+// How the tiles are shared out: the first `whole` ones are computed whole,
+// each of the other `rest` in `parts` parts along the reduction.
+struct Plan {
+  int32_t num_m, num_n, num_k;  // tiles of 256 rows, of 256 columns, stages
+  int32_t whole, rest, parts;
+};
+
+struct Params {
+  int32_t s, h, o;
+  Plan plan;
+  const int8_t *wq;   // [o][h]
+  const float *aw;    // [o]
+  const __half *base; // [s][h] or null
+  float *part;        // [rest * parts][256][256]
+  int32_t *status;
+  uint64_t timeout_ns;
+};
+
+// One piece of work: a tile and a range of its stages.
+struct Unit {
+  int32_t m, n, k0, k1;
+  int32_t slot;  // fp32 tile it leaves, or -1 for a whole tile
+};
+
+__device__ __forceinline__ bool unit_at(const Plan &pl, int32_t idx, Unit &u) {
+  int32_t tile;
+  if (idx < pl.whole) {
+    tile = idx;
+    u.k0 = 0;
+    u.k1 = pl.num_k;
+    u.slot = -1;
+  } else {
+    const int32_t t = idx - pl.whole;
+    if (t >= pl.rest * pl.parts) return false;
+    const int32_t part = t / pl.rest;
+    tile = pl.whole + t % pl.rest;
+    u.k0 = (int32_t)((int64_t)pl.num_k * part / pl.parts);
+    u.k1 = (int32_t)((int64_t)pl.num_k * (part + 1) / pl.parts);
+    u.slot = pl.parts > 1 ? t : -1;
   }
-  for (int u = 0; u < 4; ++u)
-    for (int w = 0; w < 4; ++w) {
-      const int64_t i = i0 + ty * 4 + u;
-      const int k = k0 + tx * 4 + w;
-      if (i < s && k < h) {
-        const float b = base ? __half2float(base[i * h + k]) : 0.0f;
-        dX[i * h + k] = __float2half_rn(b + acc[u][w]);
+  u.m = tile % pl.num_m;
+  u.n = tile / pl.num_m;
+  return true;
+}
+
+// A row's factor f = aw / 127 in the form the conversion uses, all exact but
+// for lo's last bit: f = (hi + lo) * p2 with p2 a power of two, as fp16 pairs.
+// hi + lo lies in [2^-6, 2^-5) (lower only for the two smallest binary16
+// values of aw), so a code times it and, for every binary16 aw, p2 stay in
+// range; lo's error is below 2^-18 of f.
+struct Factor {
+  __half2 hi, lo, p2;
+};
+
+__device__ __forceinline__ Factor factor_of(float aw) {
+  const float f = aw * (1.0f / 127.0f);
+  const int e = max((int)((__float_as_uint(f) >> 23) & 0xff) - 127 + 6, -24);
+  const float m = f * __uint_as_float((uint32_t)(127 - e) << 23);
+  Factor r;
+  const __half hi = __float2half_rn(m);
+  r.hi = __half2half2(hi);
+  r.lo = __float2half2_rn(m - __half2float(hi));
+  r.p2 = __float2half2_rn(__uint_as_float((uint32_t)(127 + e) << 23));
+  return r;
+}
+
+// Two int8 codes q (given as q + 128 in the low bytes of fp16 numbers
+// 1024 + (q + 128)) times the factor. The subtraction is exact; q * (hi + lo)
+// is rounded once to fp16 (its q * lo term to 2^-22 of it before), and the
+// power of two only where the result is subnormal.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t h, const Factor &f) {
+  const __half2 q = __hadd2(*reinterpret_cast<const __half2 *>(&h), __float2half2_rn(-1152.0f));
+  const __half2 v = __hmul2(__hfma2(q, f.hi, __hmul2(q, f.lo)), f.p2);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ uint2 codes_to_half(uint32_t w, const Factor &f) {
+  const uint32_t x = w ^ 0x80808080u;
+  return make_uint2(scale_pair(prmt(x, 0x64646464u, 0x4140), f),
+                    scale_pair(prmt(x, 0x64646464u, 0x4342), f));
+}
+
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    k_input_grad(const __grid_constant__ CUtensorMap tmA,
+                 const __grid_constant__ CUtensorMap tmW,
+                 const __grid_constant__ CUtensorMap tmOut, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+  uint8_t *base = smem_raw + pad;
+  const uint32_t sA = smem_u32(base);
+  const uint32_t sB = sA + STAGES * A_STAGE_BYTES;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(base + BAR_OFF);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int st) { return bar0 + 8u * st; };
+  auto empty_bar = [&](int st) { return bar0 + 8u * (STAGES + st); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + NUM_ACC + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NUM_ACC);
+  auto raw_full_bar = [&](int st) { return drain_bar + 8u * (1 + st); };
+  auto raw_empty_bar = [&](int st) { return drain_bar + 8u * (1 + RAW_STAGES + st); };
+  uint32_t *tmem_holder =
+      reinterpret_cast<uint32_t *>(bars + 2 * STAGES + 2 * RAW_STAGES + 2 * NUM_ACC + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(full_bar(i), FULL_ARRIVALS);
+      mbar_init(empty_bar(i), 1);
+    }
+    for (int i = 0; i < RAW_STAGES; ++i) {
+      mbar_init(raw_full_bar(i), 1);
+      mbar_init(raw_empty_bar(i), CVT_WARPS);
+    }
+    for (int a = 0; a < NUM_ACC; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * EPI_THREADS);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmOut);
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(smem_u32(tmem_holder), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before either signals the other's
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  grid_dependency_wait();
+
+  const int32_t pair = (int32_t)blockIdx.x >> 1, npairs = (int32_t)gridDim.x >> 1;
+  Unit u;
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------- TMA producer (dY)
+    uint32_t stage = 0, phase = 0, issued = 0, last_par = 0;
+    bool ok = true;
+    for (int32_t idx = pair; ok && unit_at(p.plan, idx, u); idx += npairs) {
+      const int32_t row = u.m * (2 * BM) + (int32_t)rank * BM;
+      for (int32_t kb = u.k0; kb < u.k1; ++kb) {
+        if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * A_STAGE_BYTES);
+        tma_load_2d_pair(sA + stage * A_STAGE_BYTES, &tmA, mapa_shared(full_bar(stage), 0),
+                         kb * BK, row);
+        issued |= 1u << stage;
+        last_par = (last_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
+    if (!ok) {
+      // let every copy this CTA started land before shared memory goes: a
+      // phase whose copies came in may still miss converters, so wait a
+      // while instead of for the barriers
+      const uint64_t t0 = global_timer_ns();
+      while (issued && global_timer_ns() - t0 < 200000u) __nanosleep(1000);
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc = idesc_f16_f32_mn(2 * BM, BN, false, true);
+    uint32_t stage = 0, phase = 0;
+    bool ok = true, any = false;
+    int32_t it = 0;
+    for (int32_t idx = pair; ok && unit_at(p.plan, idx, u); idx += npairs, ++it) {
+      const uint32_t acc = it & 1, acc_par = (it >> 1) & 1;
+      if (!mbar_wait_bounded(tempty_bar(acc), acc_par ^ 1u, abort_flag, p.status,
+                                     LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + acc * BN;
+      for (int32_t kb = u.k0; kb < u.k1; ++kb) {
+        if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, p.status,
+                                       LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t a_desc = smem_desc_kmajor_sw128(sA + stage * A_STAGE_BYTES);
+        const uint64_t b_desc = smem_desc_mn_sw128(sB + stage * B_STAGE_BYTES, B_BLOCK_BYTES);
+#pragma unroll
+        for (int k = 0; k < BK / UMMA_K; ++k)
+          mma_f16_pair(d_tmem, a_desc + (uint64_t)((k * UMMA_K * 2) >> 4),
+                       b_desc + (uint64_t)((k * UMMA_K * 128) >> 4), idesc,
+                       (kb > u.k0 || k > 0) ? 1u : 0u);
+        any = true;
+        mma_commit_pair(mapa_shared(empty_bar(stage), 0));
+        mma_commit_pair(mapa_shared(empty_bar(stage), 1));
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      mma_commit_pair(mapa_shared(tfull_bar(acc), 0));
+      mma_commit_pair(mapa_shared(tfull_bar(acc), 1));
+    }
+    if (!ok && any) {
+      volatile int never = 0;
+      mma_commit_pair(mapa_shared(drain_bar, 0));
+      mbar_wait_bounded(drain_bar, 0, &never, p.status, LLMINT8_DEV_TIMEOUT_DRAIN, p.timeout_ns);
+    }
+  } else if (warp == 2 && lane == 0) {
+    // ------------------------- TMA producer of the codes and their scales
+    uint32_t stage = 0, phase = 0, issued = 0, last_par = 0;
+    bool ok = true;
+    for (int32_t idx = pair; ok && unit_at(p.plan, idx, u); idx += npairs) {
+      const int32_t col = u.n * BN + (int32_t)rank * BNH;
+      for (int32_t kb = u.k0; kb < u.k1; ++kb) {
+        if (!mbar_wait_bounded(raw_empty_bar(stage), phase ^ 1u, abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = smem_u32(base) + RAW_OFF + stage * RAW_STAGE_BYTES;
+        const uint32_t scale_bytes = 4u * (uint32_t)min(BK, p.o - kb * BK);  // o % 16 == 0
+        mbar_arrive_expect_tx(raw_full_bar(stage), RAW_BYTES + scale_bytes);
+        tma_load_2d(dst, &tmW, raw_full_bar(stage), col, kb * BK);
+        bulk_load_1d(dst + RAW_BYTES, p.aw + kb * BK, scale_bytes, raw_full_bar(stage));
+        issued |= 1u << stage;
+        last_par = (last_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == RAW_STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) {  // let every copy land before shared memory goes
+      volatile int never = 0;
+      for (int st = 0; st < RAW_STAGES; ++st)
+        if ((issued >> st) & 1u)
+          mbar_wait_bounded(raw_full_bar(st), (last_par >> st) & 1u, &never, p.status,
+                            LLMINT8_DEV_TIMEOUT_DRAIN, p.timeout_ns);
+    }
+  } else if (warp >= EPI_WARP0 && warp < CVT_WARP0) {
+    // --------------------------------------------------------- epilogue
+    const int ew = warp & 3;
+    uint8_t *sOut = base + OUT_OFF + ew * OUT_STAGE_BYTES;  // [32][64 B], 64-byte swizzle
+    const uint32_t sOut_addr = smem_u32(sOut);
+    int32_t it = 0;
+    for (int32_t idx = pair; unit_at(p.plan, idx, u); idx += npairs, ++it) {
+      const uint32_t acc = it & 1, acc_par = (it >> 1) & 1;
+      const bool ready = mbar_wait_bounded(tfull_bar(acc), acc_par, abort_flag, p.status,
+                                           LLMINT8_DEV_TIMEOUT_EPILOGUE, p.timeout_ns);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      tc_fence_after();
+      const uint32_t t_row = tmem_base + ((uint32_t)(ew * 32) << 16) + acc * BN;
+      const int32_t row0 = u.m * (2 * BM) + (int32_t)rank * BM + ew * 32;
+      const int32_t row = row0 + lane;
+      for (int c = 0; c < BN / 32; ++c) {
+        const int32_t j0 = u.n * BN + c * 32;
+        uint32_t v[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(t_row + c * 32, v);
+        if (lane == 0) bulk_wait_group_read0();
+        tmem_ld_wait();
+        __syncwarp();
+        if (c == BN / 32 - 1) {
+          tc_fence_before();
+          mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+        }
+        if (u.slot >= 0) {
+          if (row < p.s && j0 < p.h) {
+            float4 *dst = reinterpret_cast<float4 *>(
+                p.part + (size_t)u.slot * PART_ELEMS +
+                (size_t)((int)rank * BM + ew * 32 + lane) * BN + c * 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                   __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+          }
+          continue;
+        }
+#pragma unroll
+        for (int q8 = 0; q8 < 4; ++q8) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * q8 + e]);
+          // h is a multiple of 16: 8 columns are all inside or all outside
+          if (p.base && row < p.s && j0 + 8 * q8 < p.h) {
+            Vec8<__half> b;
+            b.load(p.base + (int64_t)row * p.h + j0 + 8 * q8);
+            float bf[8];
+            b.get(bf);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] += bf[e];
+          }
+          store8(reinterpret_cast<__half *>(sOut + lane * 64 + ((q8 ^ ((lane >> 1) & 3)) * 16)), f);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && j0 < p.h && row0 < p.s) {
+          tma_store_2d(&tmOut, sOut_addr, j0, row0);
+          bulk_commit_group();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group0();
+  } else if (warp >= CVT_WARP0) {
+    // ------------------------------------------------------- converters
+    // group g takes the pair's stages g, g + CVT_GROUPS, ... in order
+    const int group = (warp - CVT_WARP0) / CVT_WARPS;
+    const int ct = (threadIdx.x - CVT_WARP0 * 32) % CVT_THREADS;
+    // lane: 16 codes (16 of the CTA's columns) of reduction rows r0, r0 + 32
+    const int r0 = ct >> 3, c = ct & 7, blk = c >> 2;
+    uint32_t stage = group, phase = 0, rstage = group % RAW_STAGES, rphase = 0;
+    bool ok = true;
+    int32_t skip = group;  // stages of the sequence before this group's next one
+    for (int32_t idx = pair; ok && unit_at(p.plan, idx, u); idx += npairs) {
+      int32_t kb = u.k0 + skip;
+      for (; kb < u.k1; kb += CVT_GROUPS) {
+        ok = mbar_wait_bounded(raw_full_bar(rstage), rphase, abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const uint8_t *src = base + RAW_OFF + rstage * RAW_STAGE_BYTES;
+        uint4 raw[2];
+        float sc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int kr = r0 + 32 * i;
+          raw[i] = *reinterpret_cast<const uint4 *>(src + kr * 128 + c * 16);
+          const float aw = *reinterpret_cast<const float *>(src + RAW_BYTES + 4 * kr);
+          sc[i] = kb * BK + kr < p.o ? aw : 0.0f;
+        }
+        ok = mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        uint8_t *dst = base + STAGES * A_STAGE_BYTES + stage * B_STAGE_BYTES + blk * B_BLOCK_BYTES;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int kr = r0 + 32 * i;
+          const Factor f = factor_of(sc[i]);
+          // 16-byte chunks 2m and 2m + 1 of the row's 128 bytes; the lanes of
+          // the second block write them in the other order, so that a quarter
+          // of a warp covers all eight bank groups
+          const uint4 w = raw[i];
+          const uint2 a = codes_to_half(blk ? w.z : w.x, f), b = codes_to_half(blk ? w.w : w.y, f);
+          const uint2 d = codes_to_half(blk ? w.x : w.z, f), e = codes_to_half(blk ? w.y : w.w, f);
+          const int m0 = 2 * (c & 3) + blk;
+          *reinterpret_cast<uint4 *>(dst + kr * 128 + ((m0 ^ (kr & 7)) << 4)) =
+              make_uint4(a.x, a.y, b.x, b.y);
+          *reinterpret_cast<uint4 *>(dst + kr * 128 + (((m0 ^ 1) ^ (kr & 7)) << 4)) =
+              make_uint4(d.x, d.y, e.x, e.y);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_remote(mapa_shared(full_bar(stage), 0));
+          mbar_arrive(raw_empty_bar(rstage));
+        }
+        stage += CVT_GROUPS;
+        if (stage >= STAGES) {
+          stage -= STAGES;
+          phase ^= 1u;
+        }
+        rstage += CVT_GROUPS;
+        if (rstage >= RAW_STAGES) {
+          rstage -= RAW_STAGES;
+          rphase ^= 1u;
+        }
+      }
+      skip = kb - u.k1;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // neither CTA frees the pair's TMEM, or leaves, while the other may still
+  // use its barriers or its accumulator
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+// The tiles computed in parts: out = fp16(base + the parts in order). A
+// thread holds 8 columns of one row of a tile.
+constexpr int SUM_THREADS = 256;
+__global__ void __launch_bounds__(SUM_THREADS)
+    k_input_grad_sum(const Params p, __half *__restrict__ out) {
+  grid_dependency_wait();
+  const int32_t idx = blockIdx.x * SUM_THREADS + threadIdx.x;
+  const int32_t per_tile = 2 * BM * (BN / 8);
+  const int32_t t = idx / per_tile, e = idx % per_tile;
+  if (t >= p.plan.rest) return;
+  const int32_t tile = p.plan.whole + t;
+  const int32_t row = (tile % p.plan.num_m) * (2 * BM) + e / (BN / 8);
+  const int32_t col = (tile / p.plan.num_m) * BN + (e % (BN / 8)) * 8;
+  if (row >= p.s || col >= p.h) return;
+  float f[8] = {};
+  if (p.base) {
+    Vec8<__half> b;
+    b.load(p.base + (int64_t)row * p.h + col);
+    b.get(f);
+  }
+  float acc[8] = {};
+  for (int32_t part = 0; part < p.plan.parts; ++part) {
+    const float *src = p.part + (size_t)(part * p.plan.rest + t) * PART_ELEMS + (size_t)e * 8;
+    Vec8<float> v;
+    v.load(src);
+    float g[8];
+    v.get(g);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] += g[k];
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] += acc[k];
+  store8(out + (int64_t)row * p.h + col, f);
 }
 
 }  // namespace igrad

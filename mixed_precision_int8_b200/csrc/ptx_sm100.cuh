@@ -122,6 +122,16 @@ __device__ __forceinline__ void bulk_load_1d_hint(uint32_t dst, const void *src,
       : "memory");
 }
 
+// The same without a policy.
+__device__ __forceinline__ void bulk_load_1d(uint32_t dst, const void *src, uint32_t bytes,
+                                             uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map))
                : "memory");
@@ -376,6 +386,22 @@ __device__ __forceinline__ uint64_t smem_desc_kmajor_sw128(uint32_t saddr) {
   return d;
 }
 
+// Shared-memory matrix descriptor for an MN-major operand tile (the reduction
+// index outside, the M or N index contiguous) in 128-byte-swizzled blocks of
+// 64 fp16 columns: each block's rows are 128 bytes, one per value of the
+// reduction index, and blocks follow each other block_bytes apart. Leading
+// byte offset: from one 64-column block to the next; stride byte offset: from
+// one group of 8 reduction rows to the next (1024). Other fields as above.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t block_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+  d |= (uint64_t)(block_bytes >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
 // ----------------------------------------- CTA pairs (tcgen05 cta_group::2)
 // A cluster of two CTAs whose tensor-core ops run as one: the MMA issued by
 // rank 0 reads A rows from both CTAs' shared memory (128 each) and B
@@ -406,6 +432,14 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
+}
+
+// The same at the default scope: no wait for the thread's writes to reach the
+// cluster's point of coherence (a round trip to L2 under load). For signals
+// about shared memory of this CTA that only this SM's tensor core reads, after
+// fence.proxy.async has made the writes visible to it.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 // 2-D tiled copy into this CTA's shared memory whose bytes are counted on
@@ -478,6 +512,13 @@ __host__ __device__ constexpr uint32_t idesc_i8_s32(uint32_t M, uint32_t N) {
 // N >> 3 in bits 17-22, M >> 4 in bits 24-28.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// The same with the operands' majors chosen: bit 15 (A) and 16 (B) set for
+// MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32_mn(uint32_t M, uint32_t N, bool a_mn,
+                                                        bool b_mn) {
+  return idesc_f16_f32(M, N) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
 }
 
 }  // namespace llmint8

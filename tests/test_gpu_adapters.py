@@ -443,6 +443,30 @@ def test_input_gradient_of_a_prepared_weight(s, h, o):
     assert torch.equal(got[1:], L.llmint8_matmul_backward(dY, pw)[1:])
 
 
+def test_input_gradient_recovers_weights_of_any_size():
+    """One-hot gradients read the recovered weights themselves: within half an
+    fp16 step of code * aw / 127 (and 2^-6 of one for the factor), and, where
+    that is subnormal, two roundings of half of 2^-24; column scales from the
+    largest binary16 number to the smallest, and zero."""
+    h, scales = 272, [65504.0, 127.0, 1.0, 0.08, 6e-5, 1e-6, 2.0 ** -23, 2.0 ** -24, 0.0]
+    o = 16 * ((len(scales) + 15) // 16)
+    aw = torch.tensor(scales + [1.0] * (o - len(scales)), device="cuda").half().float()
+    g = torch.Generator(device="cuda").manual_seed(8)
+    wq = torch.randint(-127, 128, (o, h), generator=g, device="cuda").to(torch.int8)
+    wq[:, :255] = torch.arange(-127, 128, device="cuda").to(torch.int8)
+    got = L.llmint8_matmul_backward(torch.eye(o, dtype=torch.float16, device="cuda"),
+                                    L.PreparedWeight(wq, aw)).double()
+    ref = wq.double() * aw.double()[:, None] / 127
+    lim = 2.0 ** -11 * (1 + 2.0 ** -6) * ref.abs() + 2.0 ** -24
+    assert ((got - ref).abs() <= lim).all()
+    # the two smallest scales are one or two steps of 2^-24 at their largest codes
+    assert torch.equal(got[6, [0, 254]], torch.tensor([-1.0, 1.0], device="cuda").double()
+                       * 2.0 ** -23)
+    assert torch.equal(got[7, [0, 254]], torch.tensor([-1.0, 1.0], device="cuda").double()
+                       * 2.0 ** -24)
+    assert not got[8].any()
+
+
 def test_input_gradient_no_rows():
     w, dY, _, _ = backward_case(4, 272, 528)
     assert L.llmint8_matmul_backward(dY[:0], w).shape == (0, 272)
