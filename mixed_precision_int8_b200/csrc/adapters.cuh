@@ -33,93 +33,125 @@ __device__ __forceinline__ int rank_of(const int32_t *rank, int a, int r) {
   return rank ? max(0, min(rank[a], r)) : r;
 }
 
-// v[i][t] = X[i] . F[a][t] (0 where the row has no adapter or t >= rank):
-// one warp per (row, t).
-__global__ void k_shrink_simple(const __half *X, int64_t s, int32_t h, const __half *F,
-                                const int32_t *ids, const int32_t *rank, int32_t n, int32_t r,
-                                float *v) {
-  const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (w >= s * r) return;
-  const int64_t i = w / r;
-  const int t = (int)(w % r);
-  const int a = adapter_of(ids, i, n);
-  float acc = 0.0f;
-  if (a >= 0 && t < rank_of(rank, a, r)) {
-    const __half *x = X + i * h, *f = F + ((int64_t)a * r + t) * h;
-    for (int c = lane; c < h / 8; c += 32) {
-      Vec8<__half> xv, fv;
-      xv.load(x + 8 * c);
-      fv.load(f + 8 * c);
-      float xf[8], ff[8];
-      xv.get(xf);
-      fv.get(ff);
+// ------------------------------------------------- a few rows (decode steps)
+//
+// Each row reads its own adapter's factors once: the work is those bytes, so
+// it is spread over (row, slice of the features) blocks on CUDA cores, with
+// fp32 products and sums. k_rows_shrink leaves one partial sum of v per slice;
+// k_rows_expand, launched as its programmatic dependent, has its first factor
+// rows in registers before it waits for them.
+
+constexpr int RS_SLICE = 512;       // features of a k_rows_shrink block
+constexpr int RS_THREADS = 256;
+constexpr int RE_THREADS = 128;
+constexpr int RE_SLICE = 8 * RE_THREADS;  // features of a k_rows_expand block
+constexpr int RE_AHEAD = 16;        // factor rows held in registers
+
+// part[slice][i][t] = X[i] . F[a][t] over the slice. Grid (slices, s).
+__global__ void __launch_bounds__(RS_THREADS)
+    k_rows_shrink(const __half *__restrict__ X, int32_t s, int32_t h, const __half *__restrict__ F,
+                  const int32_t *__restrict__ ids, const int32_t *__restrict__ rank, int32_t n,
+                  int32_t r, float *__restrict__ part) {
+  grid_dependency_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = blockIdx.y;
+  const int a = adapter_of(ids, row, n);
+  const int rk = a >= 0 ? rank_of(rank, a, r) : 0;
+  const int c0 = blockIdx.x * RS_SLICE + lane * 8;  // and 256 features further
+  float x[2][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc = fmaf(xf[e], ff[e], acc);
+  for (int u = 0; u < 2; ++u) {
+    Vec8<__half> v;
+    v.zero();
+    if (c0 + 256 * u < h) v.load(X + row * h + c0 + 256 * u);
+    v.get(x[u]);
+  }
+  float *dst = part + ((int64_t)blockIdx.x * s + row) * r;
+  const __half *f = F + (int64_t)max(a, 0) * r * h;
+#pragma unroll 4
+  for (int t = warp; t < r; t += RS_THREADS / 32) {
+    float acc = 0.0f;
+    if (t < rk) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (c0 + 256 * u >= h) continue;
+        Vec8<__half> v;
+        v.load(f + (int64_t)t * h + c0 + 256 * u);
+        float y[8];
+        v.get(y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc = fmaf(x[u][e], y[e], acc);
+      }
     }
     acc = warp_sum(acc);
+    if (lane == 0) dst[t] = acc;
   }
-  if (lane == 0) v[w] = acc;
 }
 
-// out[i][8c..] = fp16(base + scale * sum_t v[i][t] * F[a][t][8c..])
-__global__ void k_expand_simple(const float *v, int64_t s, int32_t o, const __half *F,
-                                const int32_t *ids, const float *scale, const int32_t *rank,
-                                int32_t n, int32_t r, const __half *base, __half *out) {
-  const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int nv = o / 8;
-  if (idx >= s * nv) return;
-  const int64_t i = idx / nv;
-  const int c = (int)(idx % nv);
-  const int a = adapter_of(ids, i, n);
-  Vec8<__half> b;
+// out[i][8c..] = base + scale * sum_t v[i][t] * F[a][t][8c..]. Grid (slices, s).
+__global__ void __launch_bounds__(RE_THREADS)
+    k_rows_expand(const float *__restrict__ part, int32_t slices, int32_t s, int32_t o,
+                  const __half *__restrict__ F, const int32_t *__restrict__ ids,
+                  const float *__restrict__ scale, const int32_t *__restrict__ rank, int32_t n,
+                  int32_t r, const __half *base, __half *out, float *__restrict__ v_out) {
+  __shared__ float seg_sum[RE_THREADS];
+  __shared__ float v[MAX_R];
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.y;
+  const int col = blockIdx.x * RE_SLICE + tid * 8;
+  const int a = adapter_of(ids, row, n);
+  const int rk = a >= 0 ? rank_of(rank, a, r) : 0;
+  const __half *f = F + (int64_t)max(a, 0) * r * o + col;
+  const bool in = col < o;
+  Vec8<__half> ahead[RE_AHEAD], b;
+#pragma unroll
+  for (int t = 0; t < RE_AHEAD; ++t) {
+    ahead[t].zero();
+    if (in && t < rk) ahead[t].load(f + (int64_t)t * o);
+  }
   b.zero();
-  if (base) b.load(base + i * o + 8 * c);
-  if (a >= 0) {
-    float acc[8] = {}, f[8];
-    const int rk = rank_of(rank, a, r);
-    for (int t = 0; t < rk; ++t) {
-      Vec8<__half> fv;
-      fv.load(F + ((int64_t)a * r + t) * o + 8 * c);
-      fv.get(f);
-      const float x = v[i * r + t];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(x, f[e], acc[e]);
-    }
-    b.get(f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = fmaf(scale[a], acc[e], f[e]);
-    store8(out + i * o + 8 * c, f);
-  } else {
-    *reinterpret_cast<uint4 *>(out + i * o + 8 * c) = b.q;
+  if (in && base) b.load(base + row * o + col);
+  grid_dependency_wait();
+  // v: the slices' sums, by RE_THREADS / r threads per term in turn
+  const int segs = RE_THREADS / r, t0 = tid % r, seg = tid / r;
+  float sum = 0.0f;
+  if (seg < segs)
+    for (int q = seg; q < slices; q += segs) sum += part[((int64_t)q * s + row) * r + t0];
+  seg_sum[tid] = sum;
+  __syncthreads();
+  if (tid < r) {
+    float t = 0.0f;
+    for (int q = 0; q < segs; ++q) t += seg_sum[q * r + tid];
+    v[tid] = t;
+    if (v_out && blockIdx.x == 0) v_out[row * r + tid] = t;
   }
-}
-
-// d[a][t][8c..] = scale[a] * sum over the adapter's rows of p[i][t] * Q[i][8c..]
-__global__ void k_outer_simple(const float *p, const __half *Q, int64_t s, int32_t w,
-                               const int32_t *ids, const float *scale, const int32_t *rank,
-                               int32_t n, int32_t r, float *d) {
-  const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int nv = w / 8;
-  if (idx >= (int64_t)n * r * nv) return;
-  const int c = (int)(idx % nv);
-  const int t = (int)(idx / nv % r);
-  const int a = (int)(idx / nv / r);
-  float acc[8] = {}, f[8];
-  if (t < rank_of(rank, a, r)) {
-    for (int64_t i = 0; i < s; ++i) {
-      if (ids[i] != a) continue;
-      Vec8<__half> qv;
-      qv.load(Q + i * w + 8 * c);
-      qv.get(f);
-      const float x = p[i * r + t];
+  __syncthreads();
+  if (!in) return;
+  if (a < 0) {
+    *reinterpret_cast<uint4 *>(out + row * o + col) = b.q;
+    return;
+  }
+  float acc[8] = {}, y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(x, f[e], acc[e]);
+  for (int t = 0; t < RE_AHEAD; ++t) {
+    if (t < rk) {
+      ahead[t].get(y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(v[t], y[e], acc[e]);
     }
   }
+#pragma unroll 8
+  for (int t = RE_AHEAD; t < rk; ++t) {
+    Vec8<__half> w;
+    w.load(f + (int64_t)t * o);
+    w.get(y);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] *= scale[a];
-  store8(d + idx * 8, acc);
+    for (int e = 0; e < 8; ++e) acc[e] = fmaf(v[t], y[e], acc[e]);
+  }
+  b.get(y);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = fmaf(scale[a], acc[e], y[e]);
+  store8(out + row * o + col, y);
 }
 
 }  // namespace lora

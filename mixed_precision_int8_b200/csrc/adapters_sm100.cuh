@@ -1,0 +1,972 @@
+// The adapters' products on the tensor cores, for batches of more than a few
+// rows (formulas: adapters.cuh). Three kernels:
+//
+//   k_shrink   v = X . F^T over the features: 128 rows per cluster, the
+//              features cut over the cluster's CTAs, their partial sums added
+//              through distributed shared memory in rank order
+//   k_expand   out = base + scale * v . F: 128 rows x 64 features per step
+//   k_outer    dF = scale * P^T . Q over the rows of one adapter: 256 features
+//              per cluster, the blocks of 64 rows cut over its CTAs
+//
+// All are bound by bytes: at rank r an fp16 feature takes part in 2 r to 4 r
+// operations. What they read once (X, dY, base) streams through TMA rings;
+// the factors and the s x r arrays stay in L2.
+//
+// A tile of rows may mix adapters. tile_slots() numbers the distinct ones;
+// k_shrink and k_expand multiply the whole tile with each adapter's factor
+// into columns (or a step) of its own and keep, per row, its own adapter's,
+// so nothing of another adapter or row can reach a row. k_outer sums over
+// rows: in a block of rows that is not all one adapter's, the others' rows of
+// both operands are zeroed in shared memory.
+//
+// v, g and the sums are fp32. As tensor-core operands they are split into two
+// fp16 numbers (hi + lo, 22 bits) after an exact scaling by a power of two
+// that brings the largest of a row (k_expand) or of an adapter's rows
+// (k_outer) to [2^14, 2^15), so neither large nor small gradients leave the
+// fp16 range; sums run in several TMEM accumulators in turn, which shortens
+// the chains that the tensor cores round toward zero.
+//
+// Every wait is bounded, as in the GEMMs: a role that gives up sets a status
+// bit, the others follow, copies in flight land, TMEM is freed.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include "adapters.cuh"
+#include "ptx_sm100.cuh"
+#include "rows_common.cuh"
+
+namespace llmint8 {
+namespace lora {
+
+constexpr int TM = 128;                      // rows of a tile
+constexpr uint32_t SMEM_LIMIT = 232448;
+
+// ------------------------------------------------------------ shared parts
+
+struct TileSlots {
+  int32_t id[TM];       // adapter of each row, -1 for none
+  int32_t slot[TM];     // number of that adapter within the tile, or -1
+  int32_t adapter[TM];  // adapter of each slot, by first row
+  int32_t first[TM];    // slot of the rows that lead one
+  int32_t per_warp[4];
+  int32_t count;
+};
+
+// Whole block (at least TM threads, whole warps).
+__device__ __forceinline__ void tile_slots(const int32_t *ids, int64_t row0, int64_t s, int32_t n,
+                                           TileSlots &ts) {
+  const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+  int a = -1, lead = t;
+  unsigned leaders = 0;
+  if (t < TM) {
+    if (row0 + t < s) a = adapter_of(ids, row0 + t, n);
+    ts.id[t] = a;
+  }
+  __syncthreads();
+  if (t < TM) {
+    const unsigned same = __match_any_sync(0xffffffffu, a);
+    const int head = __ffs(same) - 1;
+    lead = (w << 5) + head;
+    if (lane == head && a >= 0) {
+      for (int j = 0; j < (w << 5); j += 4) {
+        const int4 q = *reinterpret_cast<const int4 *>(&ts.id[j]);
+        const int hit = q.x == a ? 0 : q.y == a ? 1 : q.z == a ? 2 : q.w == a ? 3 : -1;
+        if (hit >= 0) {
+          lead = j + hit;
+          break;
+        }
+      }
+    }
+    __syncwarp();
+    lead = __shfl_sync(0xffffffffu, lead, head);
+    leaders = __ballot_sync(0xffffffffu, a >= 0 && lead == t);
+    if (lane == 0) ts.per_warp[w] = __popc(leaders);
+  }
+  __syncthreads();
+  if (t < TM && a >= 0 && lead == t) {
+    int slot = __popc(leaders & ((1u << lane) - 1u));
+    for (int i = 0; i < w; ++i) slot += ts.per_warp[i];
+    ts.first[t] = slot;
+    ts.adapter[slot] = a;
+  }
+  if (t == 0) ts.count = ts.per_warp[0] + ts.per_warp[1] + ts.per_warp[2] + ts.per_warp[3];
+  __syncthreads();
+  if (t < TM) ts.slot[t] = a >= 0 ? ts.first[lead] : -1;
+  __syncthreads();
+}
+
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a <= 3.402823466e38f ? a : 0.0f;  // NaN and infinities count as 0
+}
+
+// The power of two 2^e that brings `largest` to [2^14, 2^15) as
+// largest * 2^-e; 1 for 0. e stays within what fp32 holds.
+__device__ __forceinline__ int scale_exponent(float largest) {
+  if (!(largest > 0.0f)) return 0;
+  const int e = (int)((__float_as_uint(largest) >> 23) & 0xff) - 127 - 14;
+  return max(-112, min(112, e));
+}
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// Eight fp32 values times `f` as hi + lo fp16 octets.
+__device__ __forceinline__ void split8(const float (&x)[8], float f, uint4 &hi, uint4 &lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = x[2 * i] * f, b = x[2 * i + 1] * f;
+    const __half2 hh = __floats2half2_rn(a, b);
+    const float2 back = __half22float2(hh);
+    // an infinity keeps its sign in hi; its lo is not inf - inf
+    const __half2 ll = __floats2half2_rn(isinf(back.x) ? 0.0f : a - back.x,
+                                         isinf(back.y) ? 0.0f : b - back.y);
+    h[i] = *reinterpret_cast<const uint32_t *>(&hh);
+    l[i] = *reinterpret_cast<const uint32_t *>(&ll);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Shared by the roles of a CTA.
+struct Ctl {
+  uint32_t tmem;
+  int abort;
+};
+
+// ------------------------------------------------------------------ k_shrink
+
+constexpr int SH_THREADS = 256;
+constexpr int SH_KB = 64;       // features per stage
+constexpr int SH_COLS = 128;    // columns of an accumulator: slots of a pass x r
+constexpr int SH_ACC = 4;       // accumulators, used in turn
+constexpr int SH_MAX_STAGES = 8;
+constexpr uint32_t SH_X_BYTES = TM * SH_KB * 2;
+
+struct ShrinkParams {
+  int32_t s, k, n, r;
+  int32_t split;        // CTAs of a cluster
+  int32_t slots;        // adapters of a pass: SH_COLS / r
+  int32_t stages;
+  uint32_t stage_bytes;
+  const int32_t *ids, *rank;
+  float *v, *vmax;      // [s][r]; [s] largest finite |v| of each row
+  const float *w;       // another [s][r] whose row maxima go to wmax, or null
+  float *wmax;
+  int32_t *status;
+  uint64_t timeout_ns;
+};
+
+struct ShrinkJob {
+  CUtensorMap x, f;  // X [s][k] in 64 x 128 boxes, F [n * r][k] in 64 x r boxes
+  ShrinkParams p;
+};
+
+__host__ __device__ inline uint32_t shrink_stage_bytes(int32_t r) {
+  return SH_X_BYTES + (uint32_t)((SH_COLS / r * r + 15) / 16 * 16) * 128;
+}
+// partial sums [TM][r + 1], slots, barriers, alignment
+__host__ __device__ inline uint32_t shrink_fixed_bytes(int32_t r) {
+  return (uint32_t)(TM * (r + 1) * 4 + 15) / 16 * 16 + (uint32_t)sizeof(TileSlots) + 256 + 1024;
+}
+
+// Grid: (m tiles * split, 1, jobs), clusters of `split` along x.
+__global__ void __launch_bounds__(SH_THREADS, 1)
+    k_shrink(const __grid_constant__ ShrinkJob j0, const __grid_constant__ ShrinkJob j1) {
+  const ShrinkJob &job = blockIdx.z == 0 ? j0 : j1;
+  const ShrinkParams &p = job.p;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t *base = smem_raw + pad;
+  const uint32_t ring = smem_u32(base);
+  const int ldp = p.r + 1;
+  float *part = reinterpret_cast<float *>(base + p.stages * p.stage_bytes);
+  uint8_t *after = reinterpret_cast<uint8_t *>(part) + (TM * ldp * 4 + 15) / 16 * 16;
+  TileSlots &ts = *reinterpret_cast<TileSlots *>(after);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(after + (sizeof(TileSlots) + 15) / 16 * 16);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int st) { return bar0 + 8u * st; };
+  auto empty_bar = [&](int st) { return bar0 + 8u * (SH_MAX_STAGES + st); };
+  const uint32_t tfull = bar0 + 8u * (2 * SH_MAX_STAGES), tempty = tfull + 8, drain = tfull + 16;
+  Ctl *ctl = reinterpret_cast<Ctl *>(bars + 2 * SH_MAX_STAGES + 3);
+  volatile int *abort_flag = &ctl->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t cta = p.split > 1 ? cluster_ctarank() : 0;
+  const int64_t row0 = (int64_t)(blockIdx.x / p.split) * TM;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(full_bar(i), 1);
+      mbar_init(empty_bar(i), 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, TM);
+    mbar_init(drain, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&job.x);
+    tma_prefetch_desc(&job.f);
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&ctl->tmem), SH_COLS * SH_ACC);
+    tmem_relinquish();
+  }
+  grid_dependency_trigger();
+  tc_fence_before();
+  tile_slots(p.ids, row0, p.s, p.n, ts);  // ends with a barrier
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  const int32_t nk = (p.k + SH_KB - 1) / SH_KB;
+  const int32_t k0 = (int32_t)((int64_t)nk * cta / p.split);
+  const int32_t k1 = (int32_t)((int64_t)nk * (cta + 1) / p.split);
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------ TMA producer
+    uint32_t stage = 0, phase = 0, issued = 0, last_par = 0;
+    bool ok = true;
+    for (int32_t s0 = 0; ok && s0 < ts.count; s0 += p.slots) {
+      const int32_t ns = min(p.slots, ts.count - s0);
+      for (int32_t kb = k0; kb < k1; ++kb) {
+        if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = ring + stage * p.stage_bytes;
+        mbar_arrive_expect_tx(full_bar(stage), SH_X_BYTES + (uint32_t)(ns * p.r) * 128);
+        tma_load_2d(dst, &job.x, full_bar(stage), kb * SH_KB, (int32_t)row0);
+        for (int32_t i = 0; i < ns; ++i)
+          tma_load_2d(dst + SH_X_BYTES + (uint32_t)(i * p.r) * 128, &job.f, full_bar(stage),
+                      kb * SH_KB, ts.adapter[s0 + i] * p.r);
+        issued |= 1u << stage;
+        last_par = (last_par & ~(1u << stage)) | (phase << stage);
+        if ((int)++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) {  // let every copy land before shared memory goes
+      volatile int never = 0;
+      for (int st = 0; st < p.stages; ++st)
+        if ((issued >> st) & 1u)
+          mbar_wait_bounded(full_bar(st), (last_par >> st) & 1u, &never, p.status,
+                            LLMINT8_DEV_TIMEOUT_DRAIN, p.timeout_ns);
+    }
+  } else if (warp == 1 && lane == 0) {
+    // ------------------------------------------------------- MMA issuer
+    uint32_t stage = 0, phase = 0;
+    bool ok = true, any = false;
+    int32_t pass = 0;
+    for (int32_t s0 = 0; ok && s0 < ts.count; s0 += p.slots, ++pass) {
+      const int32_t cols = (min(p.slots, ts.count - s0) * p.r + 15) / 16 * 16;
+      const uint32_t idesc = idesc_f16_f32(TM, cols);
+      if (!mbar_wait_bounded(tempty, (uint32_t)(pass & 1) ^ 1u, abort_flag, p.status,
+                             LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      for (int32_t kb = k0; kb < k1; ++kb) {
+        if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t src = ring + stage * p.stage_bytes;
+        const uint64_t a = smem_desc_kmajor_sw128(src);
+        const uint64_t b = smem_desc_kmajor_sw128(src + SH_X_BYTES);
+        const int32_t i = kb - k0;
+#pragma unroll
+        for (int k = 0; k < SH_KB / 16; ++k)
+          mma_f16(tmem + (uint32_t)(i % SH_ACC) * SH_COLS, a + (uint64_t)(2 * k),
+                  b + (uint64_t)(2 * k), idesc, (i >= SH_ACC || k > 0) ? 1u : 0u);
+        any = true;
+        mma_commit(empty_bar(stage));
+        if ((int)++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (ok) mma_commit(tfull);
+    }
+    if (!ok && any) {
+      volatile int never = 0;
+      mma_commit(drain);
+      mbar_wait_bounded(drain, 0, &never, p.status, LLMINT8_DEV_TIMEOUT_DRAIN, p.timeout_ns);
+    }
+  } else if (warp >= 4) {
+    // ----------------------------------- epilogue: this CTA's partial sums
+    const int row = threadIdx.x - 128;
+    const int slot = ts.slot[row];
+    const int rk = slot >= 0 ? rank_of(p.rank, ts.adapter[slot], p.r) : 0;
+    for (int t = rk; t < p.r; ++t) part[row * ldp + t] = 0.0f;
+    const int accs = min(SH_ACC, k1 - k0);
+    int32_t pass = 0;
+    for (int32_t s0 = 0; s0 < ts.count; s0 += p.slots, ++pass) {
+      const bool ready = mbar_wait_bounded(tfull, (uint32_t)(pass & 1), abort_flag, p.status,
+                                           LLMINT8_DEV_TIMEOUT_EPILOGUE, p.timeout_ns);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      tc_fence_after();
+      const int32_t s1 = min(s0 + p.slots, ts.count);
+      for (int32_t sl = s0; sl < s1; ++sl) {
+        if (!__any_sync(0xffffffffu, slot == sl)) continue;
+        for (int c = 0; c < p.r; c += 8) {
+          float sum[8] = {};
+          for (int q = 0; q < accs; ++q) {
+            uint32_t v[8];
+            tmem_ld_32x32b_x8(tmem + ((uint32_t)((warp & 3) * 32) << 16) +
+                                  (uint32_t)(q * SH_COLS + (sl - s0) * p.r + c), v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += __uint_as_float(v[e]);
+          }
+          if (slot == sl) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (c + e < rk) part[row * ldp + c + e] = sum[e];
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(tempty);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, SH_COLS * SH_ACC);
+  // the cluster's partial sums, in rank order; this CTA finishes TM / split rows
+  if (p.split > 1) cluster_sync();
+  const int rows = TM / p.split;
+  for (int i = warp; i < rows; i += SH_THREADS / 32) {
+    const int row = (int)cta * rows + i;
+    if (row0 + row >= p.s) continue;
+    float largest = 0.0f;
+    for (int t = lane; t < p.r; t += 32) {
+      float sum = 0.0f;
+      if (p.split > 1) {
+        const uint32_t at = smem_u32(part + row * ldp + t);
+        for (int q = 0; q < p.split; ++q) sum += ld_cluster_f32(mapa_shared(at, (uint32_t)q));
+      } else {
+        sum = part[row * ldp + t];
+      }
+      p.v[(row0 + row) * p.r + t] = sum;
+      largest = fmaxf(largest, finite_abs(sum));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+      largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
+    if (lane == 0) p.vmax[row0 + row] = largest;
+    if (p.w != nullptr) {
+      largest = 0.0f;
+      for (int t = lane; t < p.r; t += 32)
+        largest = fmaxf(largest, finite_abs(p.w[(row0 + row) * p.r + t]));
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1)
+        largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
+      if (lane == 0) p.wmax[row0 + row] = largest;
+    }
+  }
+  if (p.split > 1) cluster_sync();  // no CTA leaves while its sums are read
+}
+
+// Largest finite |w| of each row of an [s][r] array: one warp per row.
+__global__ void __launch_bounds__(256)
+    k_row_max(const float *__restrict__ w, int64_t s, int32_t r, float *__restrict__ wmax) {
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= s) return;
+  float largest = 0.0f;
+  for (int t = lane; t < r; t += 32) largest = fmaxf(largest, finite_abs(w[row * r + t]));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+    largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
+  if (lane == 0) wmax[row] = largest;
+}
+
+// ------------------------------------------------------------------ k_expand
+
+constexpr int EX_N = 64;           // features per step
+constexpr int EX_WARPS = 12, EX_THREADS = 32 * EX_WARPS;
+constexpr int EX_EPI_THREADS = 256;
+constexpr int EX_ACC = 4;          // accumulators of EX_N columns
+constexpr int EX_MAX_RING = 8, EX_MAX_F = 4;
+constexpr int EX_LOADERS = 2;      // warps 2 and 3
+constexpr uint32_t EX_TILE_BYTES = TM * EX_N * 2;
+
+struct ExpandParams {
+  int32_t s, o, n, r;
+  int32_t steps, chunks;   // feature steps, cut into chunks (one per CTA and row tile)
+  int32_t ring, fbufs;     // base / output tiles, factor tiles in shared memory
+  const float *v, *vmax, *scale;
+  const __half *f;         // [n][r][o]
+  const int32_t *ids, *rank;
+  int32_t has_base;
+  int32_t *status;
+  uint64_t timeout_ns;
+};
+
+// rows of a factor tile: r, and the first 8 again when r is an odd multiple of 8
+__host__ __device__ inline int32_t expand_f_rows(int32_t r) { return r % 16 ? r + 8 : r; }
+__host__ __device__ inline uint32_t expand_bytes(int32_t r, int32_t ring, int32_t fbufs) {
+  return (uint32_t)ring * EX_TILE_BYTES + (uint32_t)fbufs * expand_f_rows(r) * 128 +
+         (uint32_t)r * 2 * TM * 2 + (uint32_t)sizeof(TileSlots) + TM * 4 + 512 + 1024;
+}
+
+// Grid: row tiles * chunks.
+__global__ void __launch_bounds__(EX_THREADS)
+    k_expand(const __grid_constant__ CUtensorMap tm_base,
+             const __grid_constant__ CUtensorMap tm_out, const ExpandParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t *base = smem_raw + pad;
+  const uint32_t ring = smem_u32(base);
+  const int32_t frows = expand_f_rows(p.r);
+  const uint32_t fbuf = ring + (uint32_t)p.ring * EX_TILE_BYTES;
+  uint8_t *vop = base + p.ring * EX_TILE_BYTES + p.fbufs * frows * 128;  // hi, lo octets of v
+  uint8_t *after = vop + p.r * 2 * TM * 2;
+  TileSlots &ts = *reinterpret_cast<TileSlots *>(after);
+  float *factor = reinterpret_cast<float *>(after + (sizeof(TileSlots) + 15) / 16 * 16);  // [TM]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(factor + TM);
+  const uint32_t bar0 = smem_u32(bars);
+  auto bfull = [&](int i) { return bar0 + 8u * i; };                    // base tile in
+  auto bempty = [&](int i) { return bar0 + 8u * (EX_MAX_RING + i); };   // output tile out
+  auto ffull = [&](int i) { return bar0 + 8u * (2 * EX_MAX_RING + i); };
+  auto fempty = [&](int i) { return bar0 + 8u * (2 * EX_MAX_RING + EX_MAX_F + i); };
+  auto tfull = [&](int i) { return bar0 + 8u * (2 * EX_MAX_RING + 2 * EX_MAX_F + i); };
+  auto tempty = [&](int i) { return bar0 + 8u * (2 * EX_MAX_RING + 2 * EX_MAX_F + EX_ACC + i); };
+  const uint32_t drain = bar0 + 8u * (2 * EX_MAX_RING + 2 * EX_MAX_F + 2 * EX_ACC);
+  Ctl *ctl = reinterpret_cast<Ctl *>(bars + 2 * EX_MAX_RING + 2 * EX_MAX_F + 2 * EX_ACC + 1);
+  volatile int *abort_flag = &ctl->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row0 = (int64_t)(blockIdx.x / p.chunks) * TM;
+  const int32_t chunk = (int32_t)(blockIdx.x % p.chunks);
+  const int32_t n0 = (int32_t)((int64_t)p.steps * chunk / p.chunks);
+  const int32_t n1 = (int32_t)((int64_t)p.steps * (chunk + 1) / p.chunks);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.ring; ++i) {
+      mbar_init(bfull(i), 1);
+      mbar_init(bempty(i), 1);
+    }
+    for (int i = 0; i < p.fbufs; ++i) {
+      mbar_init(ffull(i), 1);
+      mbar_init(fempty(i), 1);
+    }
+    for (int i = 0; i < EX_ACC; ++i) {
+      mbar_init(tfull(i), 1);
+      mbar_init(tempty(i), EX_EPI_THREADS);
+    }
+    mbar_init(drain, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_base);
+    tma_prefetch_desc(&tm_out);
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&ctl->tmem), EX_N * EX_ACC);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  tile_slots(p.ids, row0, p.s, p.n, ts);
+  grid_dependency_wait();  // v and vmax are the preceding kernel's
+  // v of the tile as the MMA's A operand: core matrices of 8 rows x 8 terms,
+  // all of the rows' for an octet of terms one after another; r hi columns,
+  // then r lo columns
+  for (int i = threadIdx.x; i < TM * (p.r / 8); i += EX_THREADS) {
+    const int row = i % TM, oct = i / TM;
+    float x[8] = {};
+    float f = 0.0f;
+    if (ts.id[row] >= 0) {
+      const int e = scale_exponent(p.vmax[row0 + row]);
+      f = pow2(-e);
+      Vec8<float> v;
+      v.load(p.v + (row0 + row) * p.r + oct * 8);
+      v.get(x);
+      if (oct == 0) factor[row] = p.scale[ts.id[row]] * pow2(e);
+    }
+    uint4 hi, lo;
+    split8(x, f, hi, lo);
+    const int at = (row / 8) * 128 + (row % 8) * 16;
+    *reinterpret_cast<uint4 *>(vop + oct * (TM * 16) + at) = hi;
+    *reinterpret_cast<uint4 *>(vop + (p.r / 8 + oct) * (TM * 16) + at) = lo;
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  const int32_t count = ts.count;
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------ base tiles by TMA
+    int slot = 0;
+    uint32_t phase = 0;
+    uint32_t issued = 0, last_par = 0;
+    bool ok = true;
+    for (int32_t n = n0; n < n1; ++n) {
+      if (!mbar_wait_bounded(bempty(slot), phase ^ 1u, abort_flag, p.status,
+                             LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns)) {
+        ok = false;
+        break;
+      }
+      if (p.has_base) {
+        mbar_arrive_expect_tx(bfull(slot), EX_TILE_BYTES);
+        tma_load_2d(ring + slot * EX_TILE_BYTES, &tm_base, bfull(slot), n * EX_N, (int32_t)row0);
+        issued |= 1u << slot;
+        last_par = (last_par & ~(1u << slot)) | (phase << slot);
+      } else {
+        mbar_arrive(bfull(slot));
+      }
+      if (++slot == p.ring) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!ok) {
+      volatile int never = 0;
+      for (int st = 0; st < p.ring; ++st)
+        if ((issued >> st) & 1u)
+          mbar_wait_bounded(bfull(st), (last_par >> st) & 1u, &never, p.status,
+                            LLMINT8_DEV_TIMEOUT_DRAIN, p.timeout_ns);
+    }
+  } else if (warp == 1 && lane == 0) {
+    // ------------------------------------------------------- MMA issuer
+    const uint32_t idesc = idesc_f16_f32_mn(TM, EX_N, false, true);
+    const uint32_t va = smem_u32(vop);
+    int fb = 0, acc = 0;
+    uint32_t fphase = 0, tphase = 0;
+    bool ok = true, any = false;
+    for (int32_t i = 0; ok && i < (n1 - n0) * count; ++i) {
+      ok = mbar_wait_bounded(tempty(acc), tphase ^ 1u, abort_flag, p.status,
+                             LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns) &&
+           mbar_wait_bounded(ffull(fb), fphase, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
+                             p.timeout_ns);
+      if (!ok) break;
+      tc_fence_after();
+      // 16 of the 2 r columns of v at a time; column c meets factor row
+      // c mod r (a chunk that crosses from hi to lo runs on into the copy of
+      // the first 8 rows)
+      for (int c = 0; c < 2 * p.r; c += 16)
+        mma_f16(tmem + acc * EX_N, smem_desc_core(va + (c / 8) * (TM * 16), TM * 16, 128),
+                smem_desc_mn_sw128(fbuf + fb * frows * 128 + (c < p.r ? c : c - p.r) * 128, 0),
+                idesc, c > 0 ? 1u : 0u);
+      any = true;
+      mma_commit(fempty(fb));
+      mma_commit(tfull(acc));
+      if (++fb == p.fbufs) {
+        fb = 0;
+        fphase ^= 1u;
+      }
+      if (++acc == EX_ACC) {
+        acc = 0;
+        tphase ^= 1u;
+      }
+    }
+    if (!ok && any) {
+      volatile int never = 0;
+      mma_commit(drain);
+      mbar_wait_bounded(drain, 0, &never, p.status, LLMINT8_DEV_TIMEOUT_DRAIN, p.timeout_ns);
+    }
+  } else if (warp == 2 || warp == 3) {
+    // ---------------- factor tiles [rows][64], zeros past the adapter's rank
+    const int32_t jobs = (n1 - n0) * count;
+    for (int32_t i = warp - 2; i < jobs; i += EX_LOADERS) {
+      const int fb = i % p.fbufs;
+      const bool free_slot =
+          mbar_wait_bounded(fempty(fb), (uint32_t)((i / p.fbufs) & 1) ^ 1u, abort_flag, p.status,
+                            LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns);
+      if (!__all_sync(0xffffffffu, free_slot)) break;
+      const int a = ts.adapter[i % count];
+      const int rk = rank_of(p.rank, a, p.r);
+      const int32_t col = (n0 + i / count) * EX_N + (lane & 7) * 8;
+      const __half *src = p.f + (int64_t)a * p.r * p.o + col;
+      const uint32_t dst = fbuf + fb * frows * 128;
+      for (int row = lane >> 3; row < frows; row += 4) {
+        const int t = row < p.r ? row : row - p.r;
+        const bool ok = t < rk && col < p.o;
+        cp_async_16(dst + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
+                    ok ? src + (int64_t)t * p.o : p.f, ok);
+      }
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ffull(fb));
+    }
+  } else if (warp >= 4) {
+    // --------------------------------------------------------- epilogue
+    // row = TMEM lane; 32 of the step's 64 columns per warp
+    const int et = threadIdx.x - 128;
+    const int row = (warp & 3) * 32 + lane, half = (warp - 4) >> 2;
+    const int my = ts.slot[row];
+    const float f = my >= 0 ? factor[row] : 0.0f;
+    int slot = 0, acc = 0;
+    uint32_t bphase = 0, tphase = 0;
+    bool ok = true;
+    int prev = -1;  // tile whose store may still read shared memory
+    for (int32_t n = n0; ok && n < n1; ++n) {
+      ok = mbar_wait_bounded(bfull(slot), bphase, abort_flag, p.status,
+                             LLMINT8_DEV_TIMEOUT_EPILOGUE, p.timeout_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      uint8_t *tile = base + slot * EX_TILE_BYTES + row * 128;
+      if (ok && !p.has_base && my < 0) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4 *>(tile + (((half * 4 + c) ^ (row & 7)) << 4)) =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+      for (int32_t sl = 0; ok && sl < count; ++sl) {
+        ok = mbar_wait_bounded(tfull(acc), tphase, abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_EPILOGUE, p.timeout_ns);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, my == sl)) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc * EX_N + half * 32,
+                             v);
+          tmem_ld_wait();
+          if (my == sl) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint8_t *at = tile + (((half * 4 + c) ^ (row & 7)) << 4);
+              float x[8] = {};
+              if (p.has_base) {
+                Vec8<__half> b;
+                b.load(reinterpret_cast<const __half *>(at));
+                b.get(x);
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = fmaf(f, __uint_as_float(v[8 * c + e]), x[e]);
+              store8(reinterpret_cast<__half *>(at), x);
+            }
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        mbar_arrive(tempty(acc));
+        if (++acc == EX_ACC) {
+          acc = 0;
+          tphase ^= 1u;
+        }
+      }
+      fence_proxy_async_smem();
+      if (named_barrier_or(1, EX_EPI_THREADS, !ok)) break;
+      if (et == 0) {
+        tma_store_2d(&tm_out, ring + slot * EX_TILE_BYTES, n * EX_N, (int32_t)row0);
+        bulk_commit_group();
+        if (prev >= 0) {
+          bulk_wait_group_read1();
+          mbar_arrive(bempty(prev));
+        }
+        prev = slot;
+      }
+      if (++slot == p.ring) {
+        slot = 0;
+        bphase ^= 1u;
+      }
+    }
+    if (et == 0) bulk_wait_group0();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, EX_N * EX_ACC);
+}
+
+// ------------------------------------------------------------------- k_outer
+
+constexpr int OU_KB = 64;          // rows per stage
+constexpr int OU_COLS = 256;       // features per cluster: two M = 128 products
+constexpr int OU_CVT_GROUPS = 2, OU_CVT_WARPS = 4;
+constexpr int OU_THREADS = 32 * (4 + OU_CVT_GROUPS * OU_CVT_WARPS);
+constexpr int OU_MAX_STAGES = 6;
+constexpr int OU_WINDOW = 1024;    // blocks of rows looked through at a time
+constexpr uint32_t OU_Q_BYTES = OU_KB * OU_COLS * 2;
+constexpr uint32_t OU_BLOCK_BYTES = OU_KB * 128;  // 64 features x 64 rows
+
+struct OuterParams {
+  int32_t s, w, n, r;      // rows, features
+  int32_t r16;             // r rounded up to 16: columns of a product
+  int32_t split, stages, accs, tmem_cols;
+  int32_t col_tiles;
+  uint32_t stage_bytes;
+  const float *p, *pmax;   // [s][r], [s]
+  const int32_t *ids, *rank;
+  const float *scale;
+  float *out;              // [n][r][w]
+  int32_t *status;
+  uint64_t timeout_ns;
+};
+
+struct OuterJob {
+  CUtensorMap q;           // Q [s][w] in 64 x 64 boxes
+  OuterParams p;
+};
+
+__host__ __device__ inline uint32_t outer_p_bytes(int32_t r16) { return (uint32_t)r16 * OU_KB * 2; }
+// block list, masks, barriers, alignment
+constexpr uint32_t OU_FIXED_BYTES = OU_WINDOW * (8 + 4) + 512 + 1024 + 256;
+
+// Grid: (col tiles of both jobs * split, 1, n), clusters of `split` along x.
+__global__ void __launch_bounds__(OU_THREADS, 1)
+    k_outer(const __grid_constant__ OuterJob j0, const __grid_constant__ OuterJob j1) {
+  const int32_t group = (int32_t)(blockIdx.x / j0.p.split);
+  const bool second = group >= j0.p.col_tiles;
+  const OuterJob &job = second ? j1 : j0;
+  const OuterParams &p = job.p;
+  const int32_t col0 = (second ? group - j0.p.col_tiles : group) * OU_COLS;
+  const int32_t a = (int32_t)blockIdx.z;
+  const uint32_t cta = p.split > 1 ? cluster_ctarank() : 0;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t *base = smem_raw + pad;
+  const uint32_t ring = smem_u32(base);
+  uint8_t *after = base + p.stages * p.stage_bytes;
+  uint64_t *masks = reinterpret_cast<uint64_t *>(after);            // [OU_WINDOW]
+  int32_t *list = reinterpret_cast<int32_t *>(masks + OU_WINDOW);   // [OU_WINDOW]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(list + OU_WINDOW);
+  const uint32_t bar0 = smem_u32(bars);
+  auto qfull = [&](int i) { return bar0 + 8u * i; };
+  auto pfull = [&](int i) { return bar0 + 8u * (OU_MAX_STAGES + i); };
+  auto empty = [&](int i) { return bar0 + 8u * (2 * OU_MAX_STAGES + i); };
+  const uint32_t done = bar0 + 8u * (3 * OU_MAX_STAGES);
+  Ctl *ctl = reinterpret_cast<Ctl *>(bars + 3 * OU_MAX_STAGES + 1);
+  volatile int *abort_flag = &ctl->abort;
+  int32_t *listed = reinterpret_cast<int32_t *>(ctl + 1);
+  uint32_t *largest = reinterpret_cast<uint32_t *>(listed + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(qfull(i), 1);
+      mbar_init(pfull(i), OU_CVT_WARPS);
+      mbar_init(empty(i), 1);
+    }
+    mbar_init(done, 1);
+    ctl->abort = 0;
+    *largest = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&job.q);
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&ctl->tmem), p.tmem_cols);
+    tmem_relinquish();
+  }
+  // the columns between r and r16 of every P tile stay zero
+  if (p.r16 != p.r) {
+    for (int i = threadIdx.x; i < p.stages * 2 * OU_KB; i += OU_THREADS) {
+      const int st = i / (2 * OU_KB), hl = (i / OU_KB) & 1, k = i % OU_KB;
+      *reinterpret_cast<uint4 *>(base + st * p.stage_bytes + OU_Q_BYTES +
+                                 hl * outer_p_bytes(p.r16) + (p.r / 8) * (OU_KB * 16) + k * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  grid_dependency_wait();
+
+  const int64_t blocks = ((int64_t)p.s + OU_KB - 1) / OU_KB;
+  // the adapter's largest |p| (all rows), for its exact scaling
+  {
+    float m = 0.0f;
+    for (int64_t i = threadIdx.x; i < p.s; i += OU_THREADS) {
+      const float pm = p.pmax[i];
+      m = fmaxf(m, p.ids[i] == a ? pm : 0.0f);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (lane == 0 && m > 0.0f) atomicMax(largest, __float_as_uint(m));
+  }
+  // barriers and parities run on over the windows
+  uint32_t it0 = 0;  // stages this CTA has used before the window
+  bool failed = false;
+  for (int64_t w0 = 0; w0 < blocks; w0 += OU_WINDOW) {
+    const int nb = (int)min((int64_t)OU_WINDOW, blocks - w0);
+    // which rows of each block are the adapter's: two blocks per warp step
+    for (int b = 2 * warp; b < nb; b += 2 * (OU_THREADS / 32)) {
+      const int64_t r0 = (w0 + b) * OU_KB + lane * 4;
+      int bitsel = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (r0 + e < p.s && p.ids[r0 + e] == a) bitsel |= 1 << e;
+      // lanes 0-15: rows of block b, lanes 16-31: of block b + 1
+      uint64_t m = (uint64_t)bitsel << (4 * (lane & 15));
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) m |= __shfl_xor_sync(0xffffffffu, m, d);
+      if ((lane & 15) == 0 && b + (lane >> 4) < nb) masks[b + (lane >> 4)] = m;
+    }
+    __syncthreads();
+    if (warp == 0) {  // the non-empty blocks, in order
+      int cnt = 0;
+      for (int b = 0; b < nb; b += 32) {
+        const bool any = b + lane < nb && masks[b + lane] != 0;
+        const unsigned v = __ballot_sync(0xffffffffu, any);
+        if (any) list[cnt + __popc(v & ((1u << lane) - 1u))] = b + lane;
+        cnt += __popc(v);
+      }
+      if (lane == 0) *listed = cnt;
+    }
+    __syncthreads();
+    const int32_t total = *listed;
+    const int32_t mine = total > (int32_t)cta ? (total - (int32_t)cta + p.split - 1) / p.split : 0;
+    // this CTA's i-th block of the window is list[cta + i * split]
+    if (warp == 0 && lane == 0) {
+      for (int32_t i = 0; i < mine; ++i) {
+        const uint32_t it = it0 + i;
+        const int st = (int)(it % p.stages);
+        if (!mbar_wait_bounded(empty(st), ((it / p.stages) & 1u) ^ 1u, abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns))
+          break;
+        const uint32_t dst = ring + st * p.stage_bytes;
+        const int32_t row = (int32_t)((w0 + list[cta + i * p.split]) * OU_KB);
+        mbar_arrive_expect_tx(qfull(st), OU_Q_BYTES);
+#pragma unroll
+        for (int c = 0; c < OU_COLS / 64; ++c)
+          tma_load_2d(dst + c * OU_BLOCK_BYTES, &job.q, qfull(st), col0 + c * 64, row);
+      }
+    } else if (warp == 1 && lane == 0) {
+      const uint32_t idesc = idesc_f16_f32_mn(128, p.r16, true, true);
+      for (int32_t i = 0; i < mine; ++i) {
+        const uint32_t it = it0 + i;
+        const int st = (int)(it % p.stages);
+        const uint32_t par = (it / p.stages) & 1u;
+        if (!mbar_wait_bounded(qfull(st), par, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
+                               p.timeout_ns) ||
+            !mbar_wait_bounded(pfull(st), par, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
+                               p.timeout_ns))
+          break;
+        tc_fence_after();
+        const uint32_t src = ring + st * p.stage_bytes;
+        const uint32_t acc = it % p.accs;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          for (int hl = 0; hl < 2; ++hl)
+#pragma unroll
+            for (int k = 0; k < OU_KB / 16; ++k)
+              mma_f16(tmem + (acc * 2 + c) * p.r16,
+                      smem_desc_mn_sw128(src + c * 2 * OU_BLOCK_BYTES + k * 2048, OU_BLOCK_BYTES),
+                      smem_desc_core(src + OU_Q_BYTES + hl * outer_p_bytes(p.r16) + k * 256, 128,
+                                     OU_KB * 16),
+                      idesc, (it >= (uint32_t)p.accs || hl > 0 || k > 0) ? 1u : 0u);
+        mma_commit(empty(st));
+      }
+    } else if (warp >= 4) {
+      // ------------------------- P tiles: hi and lo octets of 64 rows
+      const int grp = (warp - 4) / OU_CVT_WARPS;
+      const int ct = (threadIdx.x - 128) % (32 * OU_CVT_WARPS);
+      const int k = ct & 63, o0 = ct >> 6;
+      const float f = pow2(-scale_exponent(__uint_as_float(*largest)));
+      for (int32_t i = 0; i < mine; ++i) {
+        const uint32_t it = it0 + i;
+        if ((int)(it % OU_CVT_GROUPS) != grp) continue;
+        const int st = (int)(it % p.stages);
+        const uint32_t par = (it / p.stages) & 1u;
+        const int32_t b = list[cta + i * p.split];
+        const uint64_t mask = masks[b];
+        const int64_t row = (w0 + b) * OU_KB + k;
+        const bool in = (mask >> k) & 1u;
+        bool ok = mbar_wait_bounded(empty(st), par ^ 1u, abort_flag, p.status,
+                                    LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        uint8_t *dst = base + st * p.stage_bytes + OU_Q_BYTES;
+        for (int oct = o0; oct < p.r / 8; oct += 2) {
+          float x[8] = {};
+          if (in) {
+            Vec8<float> v;
+            v.load(p.p + row * p.r + oct * 8);
+            v.get(x);
+          }
+          uint4 hi, lo;
+          split8(x, f, hi, lo);
+          *reinterpret_cast<uint4 *>(dst + oct * (OU_KB * 16) + k * 16) = hi;
+          *reinterpret_cast<uint4 *>(dst + outer_p_bytes(p.r16) + oct * (OU_KB * 16) + k * 16) = lo;
+        }
+        if (mask != ~0ull) {
+          // rows of other adapters: zeros in Q too, whatever they hold
+          ok = mbar_wait_bounded(qfull(st), par, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
+                                 p.timeout_ns);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          if (!in) {
+            uint8_t *q = base + st * p.stage_bytes + k * 128;
+            for (int c = o0; c < 8 * (OU_COLS / 64); c += 2)
+              *reinterpret_cast<uint4 *>(q + (c >> 3) * OU_BLOCK_BYTES + (c & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull(st));
+      }
+    }
+    __syncthreads();
+    it0 += (uint32_t)mine;
+    if (*abort_flag) {
+      failed = true;
+      break;
+    }
+  }
+  // all products done (commits arrive in order; the last one stands for all)
+  if (warp == 1 && lane == 0) mma_commit(done);
+  {
+    volatile int never = 0;
+    mbar_wait_bounded(done, 0, &never, p.status, LLMINT8_DEV_TIMEOUT_DRAIN, p.timeout_ns);
+  }
+  if (failed) {
+    // copies in flight land before shared memory goes
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 200000u) __nanosleep(1000);
+  }
+  tc_fence_after();
+  // partial sums [r][OU_COLS] over the ring's memory, one thread per feature
+  float *part = reinterpret_cast<float *>(base);
+  const int32_t used = (int32_t)min(it0, (uint32_t)p.accs);
+  if (warp >= 4) {
+    const int lanes = (warp & 3) * 32, c = (warp - 4) >> 2;  // two products of 128 features
+    for (int t = 0; t < p.r; t += 8) {
+      float sum[8] = {};
+      for (int q = 0; q < used; ++q) {
+        uint32_t v[8];
+        tmem_ld_32x32b_x8(tmem + ((uint32_t)lanes << 16) + (uint32_t)((q * 2 + c) * p.r16 + t), v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += __uint_as_float(v[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part[(t + e) * OU_COLS + c * 128 + lanes + lane] = sum[e];
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, p.tmem_cols);
+  if (p.split > 1) cluster_sync();
+  const float f = p.scale[a] * pow2(scale_exponent(__uint_as_float(*largest)));
+  const int rk = rank_of(p.rank, a, p.r);
+  for (int t = (int)cta; t < p.r; t += p.split) {
+    float *dst = p.out + ((int64_t)a * p.r + t) * p.w + col0;
+    for (int c = threadIdx.x; c < OU_COLS; c += OU_THREADS) {
+      if (col0 + c >= p.w) continue;
+      float sum = 0.0f;
+      const uint32_t at = smem_u32(part + t * OU_COLS + c);
+      if (p.split > 1)
+        for (int q = 0; q < p.split; ++q) sum += ld_cluster_f32(mapa_shared(at, (uint32_t)q));
+      else
+        sum = part[t * OU_COLS + c];
+      dst[c] = t < rk ? f * sum : 0.0f;
+    }
+  }
+  if (p.split > 1) cluster_sync();
+}
+
+}  // namespace lora
+}  // namespace llmint8

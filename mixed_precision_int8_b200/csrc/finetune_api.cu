@@ -14,6 +14,7 @@
 #include "llmint8.h"
 #include "host_common.cuh"
 #include "adapters.cuh"
+#include "adapters_sm100.cuh"
 #include "grad_clip.cuh"
 #include "input_grad_sm100.cuh"
 #include "layernorm.cuh"
@@ -45,7 +46,13 @@ llmint8_status current_device(Device **out) {
     d.supported = major == 10 && minor == 0;
     if (d.supported) {
       if (cudaFuncSetAttribute(igrad::k_input_grad, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)igrad::SMEM_BYTES) != cudaSuccess)
+                               (int)igrad::SMEM_BYTES) != cudaSuccess ||
+          cudaFuncSetAttribute(lora::k_shrink, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)lora::SMEM_LIMIT) != cudaSuccess ||
+          cudaFuncSetAttribute(lora::k_expand, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)lora::SMEM_LIMIT) != cudaSuccess ||
+          cudaFuncSetAttribute(lora::k_outer, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)lora::SMEM_LIMIT) != cudaSuccess)
         return LLMINT8_ERR_CUDA;
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 * (unsigned)(d.sm_count / 2));
@@ -92,15 +99,24 @@ bool overlap(const void *p, size_t pn, const void *q, size_t qn) {
 
 // ------------------------------------------------------------- adapters
 
+// Rows up to which the forward pass runs the row kernels.
+constexpr int64_t kRowKernelMaxRows = 16;
+
 struct AdapterLayout {
-  size_t v, g, end;
+  size_t v, g, vmax, gmax, part, end;
 };
 
-AdapterLayout adapter_layout(int64_t s, int32_t r) {
+int64_t row_slices(int64_t h) { return (h + lora::RS_SLICE - 1) / lora::RS_SLICE; }
+
+AdapterLayout adapter_layout(int64_t s, int64_t h, int32_t r) {
   AdapterLayout L;
+  const size_t sr = 4 * (size_t)s * r, s1 = 4 * (size_t)s;
   L.v = kStateBytes;
-  L.g = align256(L.v + 4 * (size_t)s * r);
-  L.end = align256(L.g + 4 * (size_t)s * r);
+  L.g = align256(L.v + sr);
+  L.vmax = align256(L.g + sr);
+  L.gmax = align256(L.vmax + s1);
+  L.part = align256(L.gmax + s1);
+  L.end = align256(L.part + 4 * (size_t)(row_slices(h) * std::min(s, kRowKernelMaxRows)) * r);
   return L;
 }
 
@@ -124,34 +140,156 @@ llmint8_status check_adapters(const llmint8_adapters *ad, int64_t s) {
 const __half *as_half(const uint16_t *p) { return reinterpret_cast<const __half *>(p); }
 __half *as_half(uint16_t *p) { return reinterpret_cast<__half *>(p); }
 
-llmint8_status enqueue_shrink(const uint16_t *X, int64_t s, int64_t h, const uint16_t *F,
-                              const llmint8_adapters *ad, const int32_t *ids, float *v,
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The largest power of two up to `limit` CTAs per cluster that still leaves
+// each of `tiles` clusters an SM per CTA, or 1.
+int cluster_split(int64_t tiles, int64_t limit, int sm_count) {
+  int split = 1;
+  while (2 * split <= std::min<int64_t>(limit, 8) && tiles * 2 * split <= sm_count) split *= 2;
+  return split;
+}
+
+// v = X . F^T with the row maxima; w, wmax: another [s][r] array's maxima too.
+bool shrink_job(lora::ShrinkJob *job, const uint16_t *X, int64_t s, int64_t k, const uint16_t *F,
+                const llmint8_adapters *ad, const int32_t *ids, float *v, float *vmax,
+                const float *w, float *wmax, int split, void *ws) {
+  lora::ShrinkParams &p = job->p;
+  p.s = (int32_t)s;
+  p.k = (int32_t)k;
+  p.n = ad->n;
+  p.r = ad->r;
+  p.split = split;
+  p.slots = lora::SH_COLS / ad->r;
+  p.stage_bytes = lora::shrink_stage_bytes(ad->r);
+  p.stages = (int32_t)std::min<uint32_t>(
+      lora::SH_MAX_STAGES, (lora::SMEM_LIMIT - lora::shrink_fixed_bytes(ad->r)) / p.stage_bytes);
+  p.ids = ids;
+  p.rank = ad->rank_dev;
+  p.v = v;
+  p.vmax = vmax;
+  p.w = w;
+  p.wmax = wmax;
+  p.status = static_cast<int32_t *>(ws);
+  p.timeout_ns = kTimeoutNs;
+  return make_tmap_f16(&job->x, const_cast<uint16_t *>(X), (uint64_t)k, (uint64_t)s, lora::SH_KB,
+                       lora::TM) &&
+         make_tmap_f16(&job->f, const_cast<uint16_t *>(F), (uint64_t)k,
+                       (uint64_t)ad->n * ad->r, lora::SH_KB, (uint32_t)ad->r);
+}
+
+cudaError_t launch_shrink(const lora::ShrinkJob *jobs, int n_jobs, cudaStream_t st) {
+  const lora::ShrinkParams &p = jobs[0].p;
+  const int64_t tiles = ceil_div(p.s, lora::TM);
+  const uint32_t smem = lora::shrink_fixed_bytes(p.r) + p.stages * p.stage_bytes;
+  return launch_clusters(lora::k_shrink, dim3((unsigned)(tiles * p.split), 1, n_jobs),
+                         dim3(lora::SH_THREADS), smem, st, p.split, false, jobs[0],
+                         jobs[n_jobs - 1]);
+}
+
+int shrink_split(int64_t s, int64_t k, int n_jobs, int sm_count) {
+  return cluster_split(n_jobs * ceil_div(s, lora::TM), ceil_div(k, 2 * lora::SH_KB), sm_count);
+}
+
+// out = base + scale * v . F
+llmint8_status enqueue_expand(const float *v, const float *vmax, int64_t s, int64_t o,
+                              const uint16_t *F, const llmint8_adapters *ad, const int32_t *ids,
+                              const uint16_t *base, uint16_t *out, void *ws, int sm_count,
                               cudaStream_t st) {
-  if (launch(lora::k_shrink_simple, dim3(blocks_for(s * ad->r, 8)), dim3(256), 0, st, false,
-             as_half(X), s, (int32_t)h, as_half(F), ids, ad->rank_dev, ad->n, ad->r,
-             v) != cudaSuccess)
+  lora::ExpandParams p;
+  p.s = (int32_t)s;
+  p.o = (int32_t)o;
+  p.n = ad->n;
+  p.r = ad->r;
+  p.steps = (int32_t)ceil_div(o, lora::EX_N);
+  // two CTAs per SM while v's operand leaves room for their rings
+  const int per_sm = ad->r <= 64 ? 2 : 1;
+  const uint32_t limit = per_sm == 2 ? 114 * 1024 : lora::SMEM_LIMIT;
+  p.fbufs = ad->r <= 32 ? 4 : 2;
+  p.ring = 2;
+  while (p.ring < lora::EX_MAX_RING && lora::expand_bytes(ad->r, p.ring + 1, p.fbufs) <= limit)
+    ++p.ring;
+  // chunks of steps per row tile: the fewest CTA rounds for their length (a
+  // CTA's start counted as three steps)
+  const int64_t tiles = ceil_div(s, lora::TM), room = (int64_t)per_sm * sm_count;
+  int64_t best = INT64_MAX;
+  for (int64_t c = 1; c <= std::min<int64_t>(p.steps, std::max<int64_t>(room / tiles, 16)); ++c) {
+    const int64_t cost = ceil_div(tiles * c, room) * (ceil_div(p.steps, c) + 3);
+    if (cost < best) {
+      best = cost;
+      p.chunks = (int32_t)c;
+    }
+  }
+  p.v = v;
+  p.vmax = vmax;
+  p.scale = ad->scale_dev;
+  p.f = as_half(F);
+  p.ids = ids;
+  p.rank = ad->rank_dev;
+  p.has_base = base != nullptr;
+  p.status = static_cast<int32_t *>(ws);
+  p.timeout_ns = kTimeoutNs;
+  CUtensorMap tm_base, tm_out;
+  if (!make_tmap_f16(&tm_out, out, (uint64_t)o, (uint64_t)s, lora::EX_N, lora::TM) ||
+      !make_tmap_f16(&tm_base, const_cast<uint16_t *>(base ? base : out), (uint64_t)o, (uint64_t)s,
+                     lora::EX_N, lora::TM))
+    return LLMINT8_ERR_CUDA;
+  if (launch(lora::k_expand, dim3((unsigned)(tiles * p.chunks)), dim3(lora::EX_THREADS),
+             lora::expand_bytes(ad->r, p.ring, p.fbufs), st, true, tm_base, tm_out,
+             p) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   return LLMINT8_OK;
 }
 
-llmint8_status enqueue_expand(const float *v, int64_t s, int64_t o, const uint16_t *F,
-                              const llmint8_adapters *ad, const int32_t *ids,
-                              const uint16_t *base, uint16_t *out, cudaStream_t st) {
-  if (launch(lora::k_expand_simple, dim3(blocks_for(s * (o / 8), 256)), dim3(256), 0, st, false, v,
-             s, (int32_t)o, as_half(F), ids, ad->scale_dev, ad->rank_dev, ad->n, ad->r,
-             as_half(base), as_half(out)) != cudaSuccess)
-    return LLMINT8_ERR_CUDA;
-  return LLMINT8_OK;
+// dF = scale * P^T . Q per adapter
+bool outer_job(lora::OuterJob *job, const float *pp, const float *pmax, const uint16_t *Q,
+               int64_t s, int64_t w, const llmint8_adapters *ad, const int32_t *ids, float *out,
+               void *ws) {
+  lora::OuterParams &p = job->p;
+  p.s = (int32_t)s;
+  p.w = (int32_t)w;
+  p.n = ad->n;
+  p.r = ad->r;
+  p.r16 = (ad->r + 15) / 16 * 16;
+  p.stage_bytes = lora::OU_Q_BYTES + 2 * lora::outer_p_bytes(p.r16);
+  p.stages = (int32_t)std::min<uint32_t>(
+      lora::OU_MAX_STAGES, (lora::SMEM_LIMIT - lora::OU_FIXED_BYTES) / p.stage_bytes);
+  p.accs = std::min(4, 512 / (2 * p.r16));
+  p.tmem_cols = 32;
+  while (p.tmem_cols < p.accs * 2 * p.r16) p.tmem_cols *= 2;
+  p.col_tiles = (int32_t)ceil_div(w, lora::OU_COLS);
+  p.p = pp;
+  p.pmax = pmax;
+  p.ids = ids;
+  p.rank = ad->rank_dev;
+  p.scale = ad->scale_dev;
+  p.out = out;
+  p.status = static_cast<int32_t *>(ws);
+  p.timeout_ns = kTimeoutNs;
+  return make_tmap_f16(&job->q, const_cast<uint16_t *>(Q), (uint64_t)w, (uint64_t)s, 64,
+                       lora::OU_KB);
 }
 
-llmint8_status enqueue_outer(const float *p, const uint16_t *Q, int64_t s, int64_t w,
-                             const llmint8_adapters *ad, const int32_t *ids, float *d,
-                             cudaStream_t st) {
-  if (launch(lora::k_outer_simple, dim3(blocks_for((int64_t)ad->n * ad->r * (w / 8), 256)),
-             dim3(256), 0, st, false, p, as_half(Q), s, (int32_t)w, ids, ad->scale_dev,
-             ad->rank_dev, ad->n, ad->r, d) != cudaSuccess)
-    return LLMINT8_ERR_CUDA;
-  return LLMINT8_OK;
+cudaError_t launch_outer(lora::OuterJob *jobs, int n_jobs, int sm_count, cudaStream_t st) {
+  int64_t tiles = 0;
+  for (int i = 0; i < n_jobs; ++i) tiles += jobs[i].p.col_tiles;
+  // the fewest rounds for their length (a CTA's start counted as four blocks)
+  const lora::OuterParams &p = jobs[0].p;
+  const int64_t blocks = ceil_div(p.s, lora::OU_KB);
+  int split = 1;
+  int64_t best = INT64_MAX;
+  for (int c = 1; c <= 8 && c <= blocks; c *= 2) {
+    const int64_t cost = ceil_div(tiles * p.n * c, sm_count) * (ceil_div(blocks, c) + 4);
+    if (cost < best) {
+      best = cost;
+      split = c;
+    }
+  }
+  for (int i = 0; i < n_jobs; ++i) jobs[i].p.split = split;
+  return launch_clusters(lora::k_outer, dim3((unsigned)(tiles * split), 1, (unsigned)p.n),
+                         dim3(lora::OU_THREADS),
+                         lora::OU_FIXED_BYTES + p.stages * p.stage_bytes, st, split, true, jobs[0],
+                         jobs[n_jobs - 1]);
 }
 
 // ---------------------------------------- gradient of the projection's input
@@ -259,7 +397,7 @@ extern "C" {
 
 size_t llmint8_adapters_workspace_size(int64_t s, int64_t h, int64_t o, int32_t n, int32_t r) {
   if (check_adapter_sizes(s, h, o, n, r)) return 0;
-  return adapter_layout(s, r).end;
+  return adapter_layout(s, h, r).end;
 }
 
 llmint8_status llmint8_adapters_forward(const uint16_t *X_dev, int64_t s,
@@ -277,14 +415,37 @@ llmint8_status llmint8_adapters_forward(const uint16_t *X_dev, int64_t s,
   if (overlap(out_dev, out_bytes, X_dev, in_bytes) ||
       (base_dev != out_dev && overlap(out_dev, out_bytes, base_dev, out_bytes)))
     return LLMINT8_ERR_ARG;
-  const AdapterLayout L = adapter_layout(s, ad->r);
+  const AdapterLayout L = adapter_layout(s, ad->h, ad->r);
   if (ws_bytes < L.end) return LLMINT8_ERR_WORKSPACE;
   Device *dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   cudaStream_t st = as_stream(stream);
-  float *v = v_dev ? v_dev : reinterpret_cast<float *>(static_cast<uint8_t *>(ws_dev) + L.v);
-  if ((rc = enqueue_shrink(X_dev, s, ad->h, ad->a_dev, ad, ids_dev, v, st))) return rc;
-  if ((rc = enqueue_expand(v, s, ad->o, ad->b_dev, ad, ids_dev, base_dev, out_dev, st))) return rc;
+  uint8_t *wsb = static_cast<uint8_t *>(ws_dev);
+  if (s <= kRowKernelMaxRows) {
+    float *part = reinterpret_cast<float *>(wsb + L.part);
+    const int64_t slices = row_slices(ad->h);
+    if (launch(lora::k_rows_shrink, dim3((unsigned)slices, (unsigned)s), dim3(lora::RS_THREADS), 0,
+               st, false, as_half(X_dev), (int32_t)s, (int32_t)ad->h, as_half(ad->a_dev), ids_dev,
+               ad->rank_dev, ad->n, ad->r, part) != cudaSuccess ||
+        launch(lora::k_rows_expand,
+               dim3((unsigned)ceil_div(ad->o, lora::RE_SLICE), (unsigned)s),
+               dim3(lora::RE_THREADS), 0, st, true, (const float *)part, (int32_t)slices,
+               (int32_t)s, (int32_t)ad->o, as_half(ad->b_dev), ids_dev, ad->scale_dev,
+               ad->rank_dev, ad->n, ad->r, as_half(base_dev), as_half(out_dev),
+               v_dev) != cudaSuccess)
+      return LLMINT8_ERR_CUDA;
+    return last_launch();
+  }
+  float *v = v_dev ? v_dev : reinterpret_cast<float *>(wsb + L.v);
+  float *vmax = reinterpret_cast<float *>(wsb + L.vmax);
+  lora::ShrinkJob job;
+  if (!shrink_job(&job, X_dev, s, ad->h, ad->a_dev, ad, ids_dev, v, vmax, nullptr, nullptr,
+                  shrink_split(s, ad->h, 1, dev->sm_count), ws_dev) ||
+      launch_shrink(&job, 1, st) != cudaSuccess)
+    return LLMINT8_ERR_CUDA;
+  if ((rc = enqueue_expand(v, vmax, s, ad->o, ad->b_dev, ad, ids_dev, base_dev, out_dev, ws_dev,
+                           dev->sm_count, st)))
+    return rc;
   return last_launch();
 }
 
@@ -306,7 +467,7 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
   if (overlap(dX_dev, in_bytes, X_dev, in_bytes) || overlap(dX_dev, in_bytes, dY_dev, out_bytes) ||
       (base_dev != dX_dev && overlap(dX_dev, in_bytes, base_dev, in_bytes)))
     return LLMINT8_ERR_ARG;
-  const AdapterLayout L = adapter_layout(s, ad->r);
+  const AdapterLayout L = adapter_layout(s, ad->h, ad->r);
   if (s > 0 && ws_bytes < L.end) return LLMINT8_ERR_WORKSPACE;
   Device *dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
@@ -320,14 +481,39 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
   }
   uint8_t *wsb = static_cast<uint8_t *>(ws_dev);
   float *v = reinterpret_cast<float *>(wsb + L.v), *g = reinterpret_cast<float *>(wsb + L.g);
-  const float *vp = v_dev ? v_dev : v;
-  if (need_v && (rc = enqueue_shrink(X_dev, s, ad->h, ad->a_dev, ad, ids_dev, v, st))) return rc;
-  if ((dX_dev || dA_dev) && (rc = enqueue_shrink(dY_dev, s, ad->o, ad->b_dev, ad, ids_dev, g, st)))
+  float *vmax = reinterpret_cast<float *>(wsb + L.vmax);
+  float *gmax = reinterpret_cast<float *>(wsb + L.gmax);
+  const bool need_g = dX_dev || dA_dev;
+  const bool own_v = dB_dev && v_dev;  // v as the caller kept it: only its row maxima
+  lora::ShrinkJob shrink[2];
+  lora::OuterJob outer[2];
+  int n_shrink = 0, n_outer = 0;
+  const int want = (need_g ? 1 : 0) + (need_v ? 1 : 0);
+  const int split = std::min(shrink_split(s, ad->h, want, dev->sm_count),
+                             shrink_split(s, ad->o, want, dev->sm_count));
+  if (need_g && !shrink_job(&shrink[n_shrink++], dY_dev, s, ad->o, ad->b_dev, ad, ids_dev, g, gmax,
+                            own_v ? v_dev : nullptr, vmax, split, ws_dev))
+    return LLMINT8_ERR_CUDA;
+  if (need_v && !shrink_job(&shrink[n_shrink++], X_dev, s, ad->h, ad->a_dev, ad, ids_dev, v, vmax,
+                            nullptr, nullptr, split, ws_dev))
+    return LLMINT8_ERR_CUDA;
+  if (dB_dev && !outer_job(&outer[n_outer++], v_dev ? v_dev : v, vmax, dY_dev, s, ad->o, ad,
+                           ids_dev, dB_dev, ws_dev))
+    return LLMINT8_ERR_CUDA;
+  if (dA_dev &&
+      !outer_job(&outer[n_outer++], g, gmax, X_dev, s, ad->h, ad, ids_dev, dA_dev, ws_dev))
+    return LLMINT8_ERR_CUDA;
+  if (n_shrink > 0) {
+    if (launch_shrink(shrink, n_shrink, st) != cudaSuccess) return LLMINT8_ERR_CUDA;
+  } else if (own_v && launch(lora::k_row_max, dim3((unsigned)ceil_div(s, 8)), dim3(256), 0, st,
+                             false, v_dev, s, ad->r, vmax) != cudaSuccess) {
+    return LLMINT8_ERR_CUDA;
+  }
+  if (dX_dev && (rc = enqueue_expand(g, gmax, s, ad->h, ad->a_dev, ad, ids_dev, base_dev, dX_dev,
+                                     ws_dev, dev->sm_count, st)))
     return rc;
-  if (dX_dev && (rc = enqueue_expand(g, s, ad->h, ad->a_dev, ad, ids_dev, base_dev, dX_dev, st)))
-    return rc;
-  if (dA_dev && (rc = enqueue_outer(g, X_dev, s, ad->h, ad, ids_dev, dA_dev, st))) return rc;
-  if (dB_dev && (rc = enqueue_outer(vp, dY_dev, s, ad->o, ad, ids_dev, dB_dev, st))) return rc;
+  if (n_outer > 0 && launch_outer(outer, n_outer, dev->sm_count, st) != cudaSuccess)
+    return LLMINT8_ERR_CUDA;
   return last_launch();
 }
 
