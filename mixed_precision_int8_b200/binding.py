@@ -474,39 +474,44 @@ class _Launch:
     __slots__ = ("device", "stream", "_prev", "_ctx")
 
     def __init__(self, device: torch.device, stream=None):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
         self.device = device
         self.stream = stream
 
     def __enter__(self):
-        self._ctx = None
-        self._prev = torch.cuda.current_device()
-        if self._prev != self.device.index:
-            torch.cuda.set_device(self.device)
-        if self.stream is not None:
-            self._ctx = torch.cuda.stream(self.stream)
-            self._ctx.__enter__()
-            return _vp(self.stream.cuda_stream)
-        return _vp(torch.cuda.current_stream().cuda_stream)
+        index, stream = self.device.index, self.stream
+        self._prev = self._ctx = None
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {self.device}")
+        prev = torch.cuda.current_device()
+        if prev != index:
+            torch.cuda.set_device(index)
+            self._prev = prev
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(index)
+        self._ctx = torch.cuda.stream(stream)
+        self._ctx.__enter__()
+        return stream.cuda_stream
 
     def __exit__(self, *exc):
         if self._ctx is not None:
             self._ctx.__exit__(*exc)
-        if self._prev != self.device.index:
+        if self._prev is not None:
             torch.cuda.set_device(self._prev)
         return False
 
 
 def _tensor(t: torch.Tensor, name: str, dtype, shape, device=None):
-    """t must be a contiguous CUDA tensor of this dtype (or one of these) and
-    shape, on `device` when given."""
-    ok = t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype
-    if not ok or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype} and shape "
-                         f"{tuple(shape)}, not {t.dtype} {tuple(t.shape)} on {t.device}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    """t must be a contiguous CUDA tensor of this dtype and shape (a tuple),
+    on `device` when given. Returns its address."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not (
+            t.is_cuda if device is None else t.device == device):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on "
+                         f"{device or 'a CUDA device'}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _optional(t, name: str, dtype, shape, device):
+    return None if t is None else _tensor(t, name, dtype, shape, device)
 
 
 def _matrix(t: torch.Tensor, name: str):
@@ -552,10 +557,12 @@ class LayerNormWorkspace(_OpWorkspace):
         super().__init__(load_library().llmint8_layernorm_workspace_size(s, h), (s, h), device)
 
 
-def _ws_on(workspace: _OpWorkspace, device):
-    if workspace.buf.device != device:
-        raise ValueError(f"workspace is on {workspace.buf.device}, not on {device}")
-    return workspace
+def _ws(workspace, device):
+    """(address, bytes) of a workspace on this device."""
+    buf = workspace.buf
+    if buf.device != device:
+        raise ValueError(f"workspace is on {buf.device}, not on {device}")
+    return buf.data_ptr(), workspace.nbytes
 
 
 class Adapters:
@@ -580,6 +587,7 @@ class Adapters:
         self.n, self.r, self.h, self.o, self.device = n, r, h, o, dev
         self.c = llmint8_adapters(h, o, n, r, A.data_ptr(), B.data_ptr(), scale.data_ptr(),
                                   ranks.data_ptr() if ranks is not None else None)
+        self.ref = ctypes.byref(self.c)
 
 
 def llmint8_adapters_forward(X: torch.Tensor, adapters: Adapters, ids: torch.Tensor,
@@ -593,24 +601,20 @@ def llmint8_adapters_forward(X: torch.Tensor, adapters: Adapters, ids: torch.Ten
 
     base (fp16 [s,o], default zeros) is the projection's output; out may be
     base itself. v (float32 [s,r]) receives X . A for the backward pass."""
-    ad = adapters
-    s, h = _matrix(X, "X")
-    _tensor(X, "X", torch.float16, (s, ad.h), ad.device)
-    _tensor(ids, "ids", torch.int32, (s,), ad.device)
-    if base is not None:
-        _tensor(base, "base", torch.float16, (s, ad.o), ad.device)
-    if out is not None:
-        _tensor(out, "out", torch.float16, (s, ad.o), ad.device)
-    if v is not None:
-        _tensor(v, "v", torch.float32, (s, ad.r), ad.device)
-    with _Launch(ad.device, stream) as st:
+    ad, dev = adapters, adapters.device
+    s = _matrix(X, "X")[0]
+    f16 = torch.float16
+    args = (_tensor(X, "X", f16, (s, ad.h), dev), s, ad.ref,
+            _tensor(ids, "ids", torch.int32, (s,), dev),
+            _optional(base, "base", f16, (s, ad.o), dev))
+    pv = _optional(v, "v", torch.float32, (s, ad.r), dev)
+    with _Launch(dev, stream) as st:
         if out is None:
-            out = torch.empty((s, ad.o), dtype=torch.float16, device=ad.device)
+            out = torch.empty((s, ad.o), dtype=f16, device=dev)
         if workspace is None:
-            workspace = AdapterWorkspace(s, ad.h, ad.o, ad.n, ad.r, ad.device)
+            workspace = AdapterWorkspace(s, ad.h, ad.o, ad.n, ad.r, dev)
         _check("llmint8_adapters_forward", load_library().llmint8_adapters_forward(
-            _ptr(X), s, ctypes.byref(ad.c), _ptr(ids), _ptr(base), _ptr(out), _ptr(v),
-            _ptr(_ws_on(workspace, ad.device).buf), workspace.nbytes, st))
+            *args, _tensor(out, "out", f16, (s, ad.o), dev), pv, *_ws(workspace, dev), st))
     return out
 
 
@@ -629,34 +633,28 @@ def llmint8_adapters_backward(X: Optional[torch.Tensor], dY: torch.Tensor, adapt
     (fp16 [s,h], default zeros) is the gradient that reaches X through the
     projection and is added into dX, which may be base itself. want = (dX, dA,
     dB) leaves out what is not wanted (None is returned in its place)."""
-    ad = adapters
-    s, o = _matrix(dY, "dY")
-    dev = ad.device
-    _tensor(dY, "dY", torch.float16, (s, ad.o), dev)
-    _tensor(ids, "ids", torch.int32, (s,), dev)
-    want = [w or t is not None for w, t in zip(want, (dX, dA, dB))]
-    if X is None and (want[1] or (want[2] and v is None)):
+    ad, dev = adapters, adapters.device
+    s = _matrix(dY, "dY")[0]
+    f16, f32 = torch.float16, torch.float32
+    want_x, want_a, want_b = (w or t is not None for w, t in zip(want, (dX, dA, dB)))
+    if X is None and (want_a or (want_b and v is None)):
         raise ValueError("X is needed for dA, and for dB without v")
-    for t, name, dtype, shape in ((X, "X", torch.float16, (s, ad.h)),
-                                  (v, "v", torch.float32, (s, ad.r)),
-                                  (base, "base", torch.float16, (s, ad.h)),
-                                  (dX, "dX", torch.float16, (s, ad.h)),
-                                  (dA, "dA", torch.float32, (ad.n, ad.r, ad.h)),
-                                  (dB, "dB", torch.float32, (ad.n, ad.r, ad.o))):
-        if t is not None:
-            _tensor(t, name, dtype, shape, dev)
+    args = (_optional(X, "X", f16, (s, ad.h), dev), _tensor(dY, "dY", f16, (s, ad.o), dev), s,
+            ad.ref, _tensor(ids, "ids", torch.int32, (s,), dev),
+            _optional(v, "v", f32, (s, ad.r), dev), _optional(base, "base", f16, (s, ad.h), dev))
     with _Launch(dev, stream) as st:
-        if dX is None and want[0]:
-            dX = torch.empty((s, ad.h), dtype=torch.float16, device=dev)
-        if dA is None and want[1]:
-            dA = torch.empty((ad.n, ad.r, ad.h), dtype=torch.float32, device=dev)
-        if dB is None and want[2]:
-            dB = torch.empty((ad.n, ad.r, ad.o), dtype=torch.float32, device=dev)
+        if dX is None and want_x:
+            dX = torch.empty((s, ad.h), dtype=f16, device=dev)
+        if dA is None and want_a:
+            dA = torch.empty((ad.n, ad.r, ad.h), dtype=f32, device=dev)
+        if dB is None and want_b:
+            dB = torch.empty((ad.n, ad.r, ad.o), dtype=f32, device=dev)
         if workspace is None:
             workspace = AdapterWorkspace(s, ad.h, ad.o, ad.n, ad.r, dev)
         _check("llmint8_adapters_backward", load_library().llmint8_adapters_backward(
-            _ptr(X), _ptr(dY), s, ctypes.byref(ad.c), _ptr(ids), _ptr(v), _ptr(base), _ptr(dX),
-            _ptr(dA), _ptr(dB), _ptr(_ws_on(workspace, dev).buf), workspace.nbytes, st))
+            *args, _optional(dX, "dX", f16, (s, ad.h), dev),
+            _optional(dA, "dA", f32, (ad.n, ad.r, ad.h), dev),
+            _optional(dB, "dB", f32, (ad.n, ad.r, ad.o), dev), *_ws(workspace, dev), st))
     return dX, dA, dB
 
 
@@ -667,25 +665,25 @@ def llmint8_matmul_backward(dY: torch.Tensor, w: PreparedWeight,
                             stream=None) -> torch.Tensor:
     """dX = dY . W^T through the frozen int8 weight (+ base): dY fp16 [s,o]
     -> fp16 [s,h]. out may be base itself."""
-    s, o = _matrix(dY, "dY")
-    dev = w.wq.device
-    _tensor(dY, "dY", torch.float16, (s, w.o), dev)
-    if base is not None:
-        _tensor(base, "base", torch.float16, (s, w.h), dev)
-    if out is not None:
-        _tensor(out, "out", torch.float16, (s, w.h), dev)
+    s = _matrix(dY, "dY")[0]
+    dev, f16 = w.wq.device, torch.float16
+    py, pb = _tensor(dY, "dY", f16, (s, w.o), dev), _optional(base, "base", f16, (s, w.h), dev)
     with _Launch(dev, stream) as st:
         if out is None:
-            out = torch.empty((s, w.h), dtype=torch.float16, device=dev)
+            out = torch.empty((s, w.h), dtype=f16, device=dev)
         if workspace is None:
             workspace = BackwardWorkspace(s, w.h, w.o, dev)
         _check("llmint8_matmul_backward", load_library().llmint8_matmul_backward(
-            _ptr(dY), s, ctypes.byref(w.c), _ptr(base), _ptr(out),
-            _ptr(_ws_on(workspace, dev).buf), workspace.nbytes, st))
+            py, s, ctypes.byref(w.c), pb, _tensor(out, "out", f16, (s, w.h), dev),
+            *_ws(workspace, dev), st))
     return out
 
 
-_LN_TYPES = (torch.float16, torch.float32)
+def _ln_type(t: torch.Tensor, name: str) -> int:
+    code = _TYPES.get(t.dtype, 2)
+    if code == 2:
+        raise ValueError(f"{name} must be float16 or float32, not {t.dtype}")
+    return code
 
 
 def llmint8_layernorm_forward(X: torch.Tensor, gamma: torch.Tensor,
@@ -694,20 +692,18 @@ def llmint8_layernorm_forward(X: torch.Tensor, gamma: torch.Tensor,
     """(Y fp16 [s,h], mean float32 [s], rstd float32 [s]) = layer norm of the
     rows of X (fp16 or fp32 [s,h]); gamma and beta [h] are fp16 or fp32 alike."""
     s, h = _matrix(X, "X")
-    dev = X.device
-    _tensor(X, "X", _LN_TYPES, (s, h))
-    _tensor(gamma, "gamma", _LN_TYPES, (h,), dev)
-    if beta is not None:
-        _tensor(beta, "beta", gamma.dtype, (h,), dev)
-    if out is not None:
-        _tensor(out, "out", torch.float16, (s, h), dev)
+    dev, ptype = X.device, gamma.dtype
+    tx, tp = _ln_type(X, "X"), _ln_type(gamma, "gamma")
+    args = (_tensor(X, "X", X.dtype, (s, h)), tx, s, h, _tensor(gamma, "gamma", ptype, (h,), dev),
+            _optional(beta, "beta", ptype, (h,), dev), tp, eps)
     with _Launch(dev, stream) as st:
         if out is None:
             out = torch.empty((s, h), dtype=torch.float16, device=dev)
-        mean, rstd = torch.empty((2, s), dtype=torch.float32, device=dev).unbind(0)
+        mean = torch.empty((s,), dtype=torch.float32, device=dev)
+        rstd = torch.empty((s,), dtype=torch.float32, device=dev)
         _check("llmint8_layernorm_forward", load_library().llmint8_layernorm_forward(
-            _ptr(X), _TYPES[X.dtype], s, h, _ptr(gamma), _ptr(beta), _TYPES[gamma.dtype],
-            float(eps), _ptr(out), _ptr(mean), _ptr(rstd), st))
+            *args, _tensor(out, "out", torch.float16, (s, h), dev), mean.data_ptr(),
+            rstd.data_ptr(), st))
     return out, mean, rstd
 
 
@@ -718,24 +714,21 @@ def llmint8_layernorm_backward(dY: torch.Tensor, X: torch.Tensor, gamma: torch.T
     """(dX in X's type, dgamma float32 [h], dbeta float32 [h]) for dY fp16
     [s,h], with the forward call's mean and rstd."""
     s, h = _matrix(X, "X")
-    dev = X.device
-    _tensor(X, "X", _LN_TYPES, (s, h))
-    _tensor(dY, "dY", torch.float16, (s, h), dev)
-    _tensor(gamma, "gamma", _LN_TYPES, (h,), dev)
-    _tensor(mean, "mean", torch.float32, (s,), dev)
-    _tensor(rstd, "rstd", torch.float32, (s,), dev)
-    if dX is not None:
-        _tensor(dX, "dX", X.dtype, (s, h), dev)
+    dev, f32 = X.device, torch.float32
+    tx, tp = _ln_type(X, "X"), _ln_type(gamma, "gamma")
+    args = (_tensor(dY, "dY", torch.float16, (s, h), dev), _tensor(X, "X", X.dtype, (s, h)), tx,
+            s, h, _tensor(gamma, "gamma", gamma.dtype, (h,), dev), tp,
+            _tensor(mean, "mean", f32, (s,), dev), _tensor(rstd, "rstd", f32, (s,), dev))
     with _Launch(dev, stream) as st:
         if dX is None:
             dX = torch.empty_like(X)
-        dgamma, dbeta = torch.empty((2, h), dtype=torch.float32, device=dev).unbind(0)
+        dgamma = torch.empty((h,), dtype=f32, device=dev)
+        dbeta = torch.empty((h,), dtype=f32, device=dev)
         if workspace is None:
             workspace = LayerNormWorkspace(s, h, dev)
         _check("llmint8_layernorm_backward", load_library().llmint8_layernorm_backward(
-            _ptr(dY), _ptr(X), _TYPES[X.dtype], s, h, _ptr(gamma), _TYPES[gamma.dtype],
-            _ptr(mean), _ptr(rstd), _ptr(dX), _ptr(dgamma), _ptr(dbeta),
-            _ptr(_ws_on(workspace, dev).buf), workspace.nbytes, st))
+            *args, _tensor(dX, "dX", X.dtype, (s, h), dev), dgamma.data_ptr(), dbeta.data_ptr(),
+            *_ws(workspace, dev), st))
     return dX, dgamma, dbeta
 
 
@@ -754,9 +747,11 @@ class GradList:
         n = len(self.grads)
         items = (llmint8_grad * max(n, 1))()
         for i, (g, out) in enumerate(zip(self.grads, self.outs)):
-            _tensor(g, f"grads[{i}]", tuple(_TYPES), g.shape, device)
-            _tensor(out, f"outs[{i}]", g.dtype, g.shape, device)
-            items[i] = llmint8_grad(g.data_ptr(), out.data_ptr(), g.numel(), _TYPES[g.dtype])
+            if g.dtype not in _TYPES:
+                raise ValueError(f"grads[{i}] must be float16, bfloat16 or float32")
+            items[i] = llmint8_grad(_tensor(g, f"grads[{i}]", g.dtype, g.shape, device),
+                                    _tensor(out, f"outs[{i}]", g.dtype, g.shape, device),
+                                    g.numel(), _TYPES[g.dtype])
         self.device = device
         lib = load_library()
         nbytes = int(lib.llmint8_grad_list_size(n))
@@ -771,13 +766,12 @@ def llmint8_clip_grads(grads: GradList, max_norm: float, norm: Optional[torch.Te
                        stream=None) -> torch.Tensor:
     """The global norm of a list's gradients (float32 [1]); they are scaled so
     that it does not exceed max_norm (inf: the norm alone)."""
-    if norm is not None:
-        _tensor(norm, "norm", torch.float32, (1,), grads.device)
-    with _Launch(grads.device, stream) as st:
+    dev = grads.device
+    with _Launch(dev, stream) as st:
         if norm is None:
-            norm = torch.empty((1,), dtype=torch.float32, device=grads.device)
+            norm = torch.empty((1,), dtype=torch.float32, device=dev)
         _check("llmint8_clip_grads", load_library().llmint8_clip_grads(
-            ctypes.byref(grads.c), float(max_norm), _ptr(norm), st))
+            ctypes.byref(grads.c), max_norm, _tensor(norm, "norm", torch.float32, (1,), dev), st))
     return norm
 
 

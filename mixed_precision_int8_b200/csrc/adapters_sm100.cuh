@@ -5,6 +5,7 @@
 //              features cut over the cluster's CTAs, their partial sums added
 //              through distributed shared memory in rank order
 //   k_expand   out = base + scale * v . F: 128 rows x 64 features per step
+//   k_pack     g or v as the operand of the next kernel
 //   k_outer    dF = scale * P^T . Q over the rows of one adapter: 256 features
 //              per cluster, the blocks of 64 rows cut over its CTAs
 //
@@ -23,8 +24,10 @@
 // fp16 numbers (hi + lo, 22 bits) after an exact scaling by a power of two
 // that brings the largest of a row (k_expand) or of an adapter's rows
 // (k_outer) to [2^14, 2^15), so neither large nor small gradients leave the
-// fp16 range; sums run in several TMEM accumulators in turn, which shortens
-// the chains that the tensor cores round toward zero.
+// fp16 range. The tensor cores round each accumulation toward zero, a bias
+// that grows with the number of MMAs into one accumulator (1.3e-6 of the
+// result, rms, after 52 of them; 0.4e-6 after 16); so k_shrink and k_outer
+// move on to a fresh one every 16 and add them up in fp32.
 //
 // Every wait is bounded, as in the GEMMs: a role that gives up sets a status
 // bit, the others follow, copies in flight land, TMEM is freed.
@@ -141,21 +144,24 @@ struct Ctl {
 
 constexpr int SH_THREADS = 256;
 constexpr int SH_KB = 64;       // features per stage
-constexpr int SH_COLS = 128;    // columns of an accumulator: slots of a pass x r
-constexpr int SH_ACC = 4;       // accumulators, used in turn
+constexpr int SH_DRAIN = 4;     // stages (of 4 MMAs) that one accumulator sums
 constexpr int SH_MAX_STAGES = 8;
+constexpr int SH_MAX_ACC = 8;
 constexpr uint32_t SH_X_BYTES = TM * SH_KB * 2;
 
 struct ShrinkParams {
   int32_t s, k, n, r;
   int32_t split;        // CTAs of a cluster
-  int32_t slots;        // adapters of a pass: SH_COLS / r
-  int32_t stages;
+  int32_t slots;        // adapters of a pass over the features
+  int32_t stages, accs; // accumulators of `cols` TMEM columns
+  int32_t cols, tmem_cols;
   uint32_t stage_bytes;
   const int32_t *ids, *rank;
-  float *v, *vmax;      // [s][r]; [s] largest finite |v| of each row
-  const float *w;       // another [s][r] whose row maxima go to wmax, or null
-  float *wmax;
+  float *v;             // [s][r]
+  float *vmax;          // [s] largest finite |v| of each row
+  uint32_t *amax;       // [n] of each adapter's rows (bits; zero before), or null
+  const float *w;       // another [s][r] whose adapters' maxima go to w_amax, or null
+  uint32_t *w_amax;
   int32_t *status;
   uint64_t timeout_ns;
 };
@@ -165,16 +171,30 @@ struct ShrinkJob {
   ShrinkParams p;
 };
 
+// Adapters of a pass: 64 columns' worth, one at least.
+__host__ __device__ inline int32_t shrink_slots(int32_t r) { return r < 64 ? 64 / r : 1; }
+__host__ __device__ inline int32_t shrink_cols(int32_t r) {
+  return (shrink_slots(r) * r + 15) / 16 * 16;
+}
 __host__ __device__ inline uint32_t shrink_stage_bytes(int32_t r) {
-  return SH_X_BYTES + (uint32_t)((SH_COLS / r * r + 15) / 16 * 16) * 128;
+  return SH_X_BYTES + (uint32_t)shrink_cols(r) * 128;
 }
 // partial sums [TM][r + 1], slots, barriers, alignment
 __host__ __device__ inline uint32_t shrink_fixed_bytes(int32_t r) {
-  return (uint32_t)(TM * (r + 1) * 4 + 15) / 16 * 16 + (uint32_t)sizeof(TileSlots) + 256 + 1024;
+  return (uint32_t)(TM * (r + 1) * 4 + 15) / 16 * 16 + (uint32_t)sizeof(TileSlots) + 384 + 1024;
+}
+
+// Largest finite |x[t]|, t < r, over a warp.
+__device__ __forceinline__ float warp_row_max(const float *x, int r) {
+  float m = 0.0f;
+  for (int t = threadIdx.x & 31; t < r; t += 32) m = fmaxf(m, finite_abs(x[t]));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  return m;
 }
 
 // Grid: (m tiles * split, 1, jobs), clusters of `split` along x.
-__global__ void __launch_bounds__(SH_THREADS, 1)
+__global__ void __launch_bounds__(SH_THREADS, 2)
     k_shrink(const __grid_constant__ ShrinkJob j0, const __grid_constant__ ShrinkJob j1) {
   const ShrinkJob &job = blockIdx.z == 0 ? j0 : j1;
   const ShrinkParams &p = job.p;
@@ -190,8 +210,10 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int st) { return bar0 + 8u * st; };
   auto empty_bar = [&](int st) { return bar0 + 8u * (SH_MAX_STAGES + st); };
-  const uint32_t tfull = bar0 + 8u * (2 * SH_MAX_STAGES), tempty = tfull + 8, drain = tfull + 16;
-  Ctl *ctl = reinterpret_cast<Ctl *>(bars + 2 * SH_MAX_STAGES + 3);
+  auto tfull = [&](int a) { return bar0 + 8u * (2 * SH_MAX_STAGES + a); };
+  auto tempty = [&](int a) { return bar0 + 8u * (2 * SH_MAX_STAGES + SH_MAX_ACC + a); };
+  const uint32_t drain = bar0 + 8u * (2 * SH_MAX_STAGES + 2 * SH_MAX_ACC);
+  Ctl *ctl = reinterpret_cast<Ctl *>(bars + 2 * SH_MAX_STAGES + 2 * SH_MAX_ACC + 1);
   volatile int *abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t cta = p.split > 1 ? cluster_ctarank() : 0;
@@ -202,8 +224,10 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
       mbar_init(full_bar(i), 1);
       mbar_init(empty_bar(i), 1);
     }
-    mbar_init(tfull, 1);
-    mbar_init(tempty, TM);
+    for (int a = 0; a < p.accs; ++a) {
+      mbar_init(tfull(a), 1);
+      mbar_init(tempty(a), TM);
+    }
     mbar_init(drain, 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -211,7 +235,7 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     tma_prefetch_desc(&job.f);
   }
   if (warp == 2) {
-    tmem_alloc(smem_u32(&ctl->tmem), SH_COLS * SH_ACC);
+    tmem_alloc(smem_u32(&ctl->tmem), p.tmem_cols);
     tmem_relinquish();
   }
   grid_dependency_trigger();
@@ -258,41 +282,41 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     }
   } else if (warp == 1 && lane == 0) {
     // ------------------------------------------------------- MMA issuer
-    uint32_t stage = 0, phase = 0;
+    uint32_t stage = 0, phase = 0, aphase = 0;
+    int acc = 0;
     bool ok = true, any = false;
-    int32_t pass = 0;
-    for (int32_t s0 = 0; ok && s0 < ts.count; s0 += p.slots, ++pass) {
-      const int32_t cols = (min(p.slots, ts.count - s0) * p.r + 15) / 16 * 16;
-      const uint32_t idesc = idesc_f16_f32(TM, cols);
-      if (!mbar_wait_bounded(tempty, (uint32_t)(pass & 1) ^ 1u, abort_flag, p.status,
-                             LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
+    for (int32_t s0 = 0; ok && s0 < ts.count; s0 += p.slots) {
+      const uint32_t idesc =
+          idesc_f16_f32(TM, (min(p.slots, ts.count - s0) * p.r + 15) / 16 * 16);
       for (int32_t kb = k0; kb < k1; ++kb) {
-        if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, p.status,
-                               LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
-          ok = false;
-          break;
-        }
+        const int32_t i = (kb - k0) % SH_DRAIN;
+        ok = (i > 0 || mbar_wait_bounded(tempty(acc), aphase ^ 1u, abort_flag, p.status,
+                                         LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) &&
+             mbar_wait_bounded(full_bar(stage), phase, abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t src = ring + stage * p.stage_bytes;
         const uint64_t a = smem_desc_kmajor_sw128(src);
         const uint64_t b = smem_desc_kmajor_sw128(src + SH_X_BYTES);
-        const int32_t i = kb - k0;
 #pragma unroll
         for (int k = 0; k < SH_KB / 16; ++k)
-          mma_f16(tmem + (uint32_t)(i % SH_ACC) * SH_COLS, a + (uint64_t)(2 * k),
-                  b + (uint64_t)(2 * k), idesc, (i >= SH_ACC || k > 0) ? 1u : 0u);
+          mma_f16(tmem + acc * p.cols, a + (uint64_t)(2 * k), b + (uint64_t)(2 * k), idesc,
+                  (i > 0 || k > 0) ? 1u : 0u);
         any = true;
         mma_commit(empty_bar(stage));
         if ((int)++stage == p.stages) {
           stage = 0;
           phase ^= 1u;
         }
+        if (i == SH_DRAIN - 1 || kb + 1 == k1) {
+          mma_commit(tfull(acc));
+          if (++acc == p.accs) {
+            acc = 0;
+            aphase ^= 1u;
+          }
+        }
       }
-      if (ok) mma_commit(tfull);
     }
     if (!ok && any) {
       volatile int never = 0;
@@ -304,44 +328,47 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
     const int row = threadIdx.x - 128;
     const int slot = ts.slot[row];
     const int rk = slot >= 0 ? rank_of(p.rank, ts.adapter[slot], p.r) : 0;
-    for (int t = rk; t < p.r; ++t) part[row * ldp + t] = 0.0f;
-    const int accs = min(SH_ACC, k1 - k0);
-    int32_t pass = 0;
-    for (int32_t s0 = 0; s0 < ts.count; s0 += p.slots, ++pass) {
-      const bool ready = mbar_wait_bounded(tfull, (uint32_t)(pass & 1), abort_flag, p.status,
-                                           LLMINT8_DEV_TIMEOUT_EPILOGUE, p.timeout_ns);
-      if (!__all_sync(0xffffffffu, ready)) break;
-      tc_fence_after();
+    float *mine = part + row * ldp;
+    for (int t = 0; t < p.r; ++t) mine[t] = 0.0f;
+    int acc = 0;
+    uint32_t aphase = 0;
+    bool ok = true;
+    for (int32_t s0 = 0; ok && s0 < ts.count; s0 += p.slots) {
       const int32_t s1 = min(s0 + p.slots, ts.count);
-      for (int32_t sl = s0; sl < s1; ++sl) {
-        if (!__any_sync(0xffffffffu, slot == sl)) continue;
-        for (int c = 0; c < p.r; c += 8) {
-          float sum[8] = {};
-          for (int q = 0; q < accs; ++q) {
+      for (int32_t kb = k0; kb < k1; kb += SH_DRAIN) {
+        ok = mbar_wait_bounded(tfull(acc), aphase, abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_EPILOGUE, p.timeout_ns);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc * p.cols;
+        for (int32_t sl = s0; sl < s1; ++sl) {
+          if (!__any_sync(0xffffffffu, slot == sl)) continue;
+          for (int c = 0; c < p.r; c += 8) {
             uint32_t v[8];
-            tmem_ld_32x32b_x8(tmem + ((uint32_t)((warp & 3) * 32) << 16) +
-                                  (uint32_t)(q * SH_COLS + (sl - s0) * p.r + c), v);
+            tmem_ld_32x32b_x8(src + (uint32_t)((sl - s0) * p.r + c), v);
             tmem_ld_wait();
+            if (slot == sl) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += __uint_as_float(v[e]);
+              for (int e = 0; e < 8; ++e)
+                if (c + e < rk) mine[c + e] += __uint_as_float(v[e]);
+            }
+            __syncwarp();
           }
-          if (slot == sl) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (c + e < rk) part[row * ldp + c + e] = sum[e];
-          }
-          __syncwarp();
+        }
+        tc_fence_before();
+        mbar_arrive(tempty(acc));
+        if (++acc == p.accs) {
+          acc = 0;
+          aphase ^= 1u;
         }
       }
-      tc_fence_before();
-      mbar_arrive(tempty);
     }
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 2) tmem_dealloc(tmem, SH_COLS * SH_ACC);
+  if (warp == 2) tmem_dealloc(tmem, p.tmem_cols);
   // the cluster's partial sums, in rank order; this CTA finishes TM / split rows
   if (p.split > 1) cluster_sync();
   const int rows = TM / p.split;
@@ -363,32 +390,30 @@ __global__ void __launch_bounds__(SH_THREADS, 1)
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
       largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
-    if (lane == 0) p.vmax[row0 + row] = largest;
-    if (p.w != nullptr) {
-      largest = 0.0f;
-      for (int t = lane; t < p.r; t += 32)
-        largest = fmaxf(largest, finite_abs(p.w[(row0 + row) * p.r + t]));
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1)
-        largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
-      if (lane == 0) p.wmax[row0 + row] = largest;
+    const int a = ts.id[row];
+    if (lane == 0) {
+      p.vmax[row0 + row] = largest;
+      if (p.amax != nullptr && a >= 0) atomicMax(p.amax + a, __float_as_uint(largest));
+    }
+    if (p.w != nullptr && a >= 0) {
+      const float wm = warp_row_max(p.w + (row0 + row) * p.r, p.r);
+      if (lane == 0) atomicMax(p.w_amax + a, __float_as_uint(wm));
     }
   }
   if (p.split > 1) cluster_sync();  // no CTA leaves while its sums are read
 }
 
-// Largest finite |w| of each row of an [s][r] array: one warp per row.
+// amax[a] = largest finite |w| of adapter a's rows of an [s][r] array (zero
+// before): one warp per row.
 __global__ void __launch_bounds__(256)
-    k_row_max(const float *__restrict__ w, int64_t s, int32_t r, float *__restrict__ wmax) {
+    k_adapter_max(const float *__restrict__ w, int64_t s, int32_t n, int32_t r,
+                  const int32_t *__restrict__ ids, uint32_t *__restrict__ amax) {
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
   if (row >= s) return;
-  float largest = 0.0f;
-  for (int t = lane; t < r; t += 32) largest = fmaxf(largest, finite_abs(w[row * r + t]));
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1)
-    largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
-  if (lane == 0) wmax[row] = largest;
+  const int a = adapter_of(ids, row, n);
+  if (a < 0) return;
+  const float m = warp_row_max(w + row * r, r);
+  if ((threadIdx.x & 31) == 0) atomicMax(amax + a, __float_as_uint(m));
 }
 
 // ------------------------------------------------------------------ k_expand
@@ -467,8 +492,14 @@ __global__ void __launch_bounds__(EX_THREADS)
     mbar_init(drain, 1);
     ctl->abort = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_base);
     tma_prefetch_desc(&tm_out);
+    // the first base tiles (no product of the preceding kernel) come in while
+    // the rows' slots and v are set up
+    if (p.has_base)
+      for (int i = 0; i < min(p.ring, n1 - n0); ++i) {
+        mbar_arrive_expect_tx(bfull(i), EX_TILE_BYTES);
+        tma_load_2d(ring + i * EX_TILE_BYTES, &tm_base, bfull(i), (n0 + i) * EX_N, (int32_t)row0);
+      }
   }
   if (warp == 2) {
     tmem_alloc(smem_u32(&ctl->tmem), EX_N * EX_ACC);
@@ -508,9 +539,12 @@ __global__ void __launch_bounds__(EX_THREADS)
     // ------------------------------------------------ base tiles by TMA
     int slot = 0;
     uint32_t phase = 0;
-    uint32_t issued = 0, last_par = 0;
     bool ok = true;
-    for (int32_t n = n0; n < n1; ++n) {
+    const int32_t early = p.has_base ? min(p.ring, n1 - n0) : 0;
+    uint32_t issued = (1u << early) - 1u, last_par = 0;
+    if (early == p.ring) phase = 1;
+    else slot = early;
+    for (int32_t n = n0 + early; n < n1; ++n) {
       if (!mbar_wait_bounded(bempty(slot), phase ^ 1u, abort_flag, p.status,
                              LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns)) {
         ok = false;
@@ -680,24 +714,82 @@ __global__ void __launch_bounds__(EX_THREADS)
   if (warp == 2) tmem_dealloc(tmem, EX_N * EX_ACC);
 }
 
-// ------------------------------------------------------------------- k_outer
+// ------------------------------------------------------------ k_pack, k_outer
 
 constexpr int OU_KB = 64;          // rows per stage
 constexpr int OU_COLS = 256;       // features per cluster: two M = 128 products
-constexpr int OU_CVT_GROUPS = 2, OU_CVT_WARPS = 4;
-constexpr int OU_THREADS = 32 * (4 + OU_CVT_GROUPS * OU_CVT_WARPS);
+constexpr int OU_SUM_WARPS = 8;
+constexpr int OU_THREADS = 32 * (2 + OU_SUM_WARPS);
+constexpr int OU_DRAIN = 2;        // blocks (of 8 MMAs per product) that one accumulator sums
 constexpr int OU_MAX_STAGES = 6;
-constexpr int OU_WINDOW = 1024;    // blocks of rows looked through at a time
+constexpr int OU_WINDOW = 512;     // blocks of rows looked through at a time
 constexpr uint32_t OU_Q_BYTES = OU_KB * OU_COLS * 2;
 constexpr uint32_t OU_BLOCK_BYTES = OU_KB * 128;  // 64 features x 64 rows
+constexpr uint32_t OU_CORE = OU_KB * 16;          // 8 terms of 64 rows
+
+// r rounded up to 16: columns of a product
+__host__ __device__ inline int32_t outer_r16(int32_t r) { return (r + 15) / 16 * 16; }
+// P of a block of 64 rows: hi octets, then lo octets, each as 8 core matrices
+// of 8 rows x 8 terms
+__host__ __device__ inline uint32_t outer_p_bytes(int32_t r) {
+  return 2 * (uint32_t)(outer_r16(r) / 8) * OU_CORE;
+}
+
+// What k_pack notes about a block of rows: their adapter when all 64 have the
+// same one, or
+constexpr int32_t OU_NONE = -1, OU_MIXED = -2;
+
+struct PackJob {
+  const float *p;        // [s][r]
+  const uint32_t *amax;  // [n]
+  uint8_t *out;          // [blocks of 64 rows][outer_p_bytes]
+};
+
+// Each row scaled for its own adapter; zeros for rows without one, rows past
+// s and terms past r. One block of threads per block of rows; grid (blocks,
+// jobs).
+constexpr int PK_THREADS = 256;
+__global__ void __launch_bounds__(PK_THREADS)
+    k_pack(const PackJob j0, const PackJob j1, int32_t s, int32_t n, int32_t r,
+           const int32_t *__restrict__ ids, int32_t *__restrict__ info) {
+  const PackJob &job = blockIdx.y == 0 ? j0 : j1;
+  grid_dependency_trigger();
+  const int k = threadIdx.x % OU_KB;
+  const int64_t row = (int64_t)blockIdx.x * OU_KB + k;
+  const int a = row < s ? adapter_of(ids, row, n) : -1;
+  grid_dependency_wait();
+  if (blockIdx.y == 0) {
+    const int64_t row0 = (int64_t)blockIdx.x * OU_KB;
+    const int lead = adapter_of(ids, row0, n);
+    const bool same = __syncthreads_and(a == lead);
+    const bool none = __syncthreads_and(a < 0);
+    if (threadIdx.x == 0) info[blockIdx.x] = none ? OU_NONE : same ? lead : OU_MIXED;
+  }
+  const float f = a >= 0 ? pow2(-scale_exponent(__uint_as_float(job.amax[a]))) : 0.0f;
+  uint8_t *dst = job.out + (size_t)blockIdx.x * outer_p_bytes(r) + k * 16;
+  const int octs = outer_r16(r) / 8;
+  for (int oct = threadIdx.x / OU_KB; oct < octs; oct += PK_THREADS / OU_KB) {
+    float x[8] = {};
+    if (a >= 0 && oct < r / 8) {
+      Vec8<float> v;
+      v.load(job.p + row * r + oct * 8);
+      v.get(x);
+    }
+    uint4 hi, lo;
+    split8(x, f, hi, lo);
+    *reinterpret_cast<uint4 *>(dst + oct * OU_CORE) = hi;
+    *reinterpret_cast<uint4 *>(dst + (octs + oct) * OU_CORE) = lo;
+  }
+}
 
 struct OuterParams {
   int32_t s, w, n, r;      // rows, features
-  int32_t r16;             // r rounded up to 16: columns of a product
-  int32_t split, stages, accs, tmem_cols;
+  int32_t split, stages, tmem_cols;
   int32_t col_tiles;
   uint32_t stage_bytes;
-  const float *p, *pmax;   // [s][r], [s]
+  const uint8_t *p;        // k_pack's output
+  const int32_t *info;
+  const uint32_t *amax;    // [n]
   const int32_t *ids, *rank;
   const float *scale;
   float *out;              // [n][r][w]
@@ -710,12 +802,19 @@ struct OuterJob {
   OuterParams p;
 };
 
-__host__ __device__ inline uint32_t outer_p_bytes(int32_t r16) { return (uint32_t)r16 * OU_KB * 2; }
 // block list, masks, barriers, alignment
-constexpr uint32_t OU_FIXED_BYTES = OU_WINDOW * (8 + 4) + 512 + 1024 + 256;
+constexpr uint32_t OU_FIXED_BYTES = OU_WINDOW * (8 + 4) + 512 + 1024;
 
-// Grid: (col tiles of both jobs * split, 1, n), clusters of `split` along x.
-__global__ void __launch_bounds__(OU_THREADS, 1)
+// NC: octets of terms that a thread sums in registers (r <= 8 NC). Grid: (col
+// tiles of both jobs * split, 1, n), clusters of `split` along x.
+//   warp 0     TMA producer: 64 rows x 256 features of Q, and their P
+//   warp 1     TMEM, MMA issuer
+//   warps 2-9  zero the rows of other adapters in mixed blocks (both
+//              operands, whatever they hold) before the MMAs; add each
+//              accumulator to the sums in their registers (one product and a
+//              quarter of its features each); add up the cluster's and store
+template <int NC>
+__global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
     k_outer(const __grid_constant__ OuterJob j0, const __grid_constant__ OuterJob j1) {
   const int32_t group = (int32_t)(blockIdx.x / j0.p.split);
   const bool second = group >= j0.p.col_tiles;
@@ -724,6 +823,8 @@ __global__ void __launch_bounds__(OU_THREADS, 1)
   const int32_t col0 = (second ? group - j0.p.col_tiles : group) * OU_COLS;
   const int32_t a = (int32_t)blockIdx.z;
   const uint32_t cta = p.split > 1 ? cluster_ctarank() : 0;
+  const int32_t r16 = outer_r16(p.r);
+  const uint32_t p_bytes = outer_p_bytes(p.r);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t *base = smem_raw + pad;
@@ -733,77 +834,67 @@ __global__ void __launch_bounds__(OU_THREADS, 1)
   int32_t *list = reinterpret_cast<int32_t *>(masks + OU_WINDOW);   // [OU_WINDOW]
   uint64_t *bars = reinterpret_cast<uint64_t *>(list + OU_WINDOW);
   const uint32_t bar0 = smem_u32(bars);
-  auto qfull = [&](int i) { return bar0 + 8u * i; };
-  auto pfull = [&](int i) { return bar0 + 8u * (OU_MAX_STAGES + i); };
+  auto full = [&](int i) { return bar0 + 8u * i; };
+  auto clean = [&](int i) { return bar0 + 8u * (OU_MAX_STAGES + i); };
   auto empty = [&](int i) { return bar0 + 8u * (2 * OU_MAX_STAGES + i); };
-  const uint32_t done = bar0 + 8u * (3 * OU_MAX_STAGES);
-  Ctl *ctl = reinterpret_cast<Ctl *>(bars + 3 * OU_MAX_STAGES + 1);
+  auto tfull = [&](uint32_t i) { return bar0 + 8u * (3 * OU_MAX_STAGES + i); };
+  auto tempty = [&](uint32_t i) { return bar0 + 8u * (3 * OU_MAX_STAGES + 2 + i); };
+  const uint32_t drain = bar0 + 8u * (3 * OU_MAX_STAGES + 4);
+  Ctl *ctl = reinterpret_cast<Ctl *>(bars + 3 * OU_MAX_STAGES + 5);
   volatile int *abort_flag = &ctl->abort;
   int32_t *listed = reinterpret_cast<int32_t *>(ctl + 1);
-  uint32_t *largest = reinterpret_cast<uint32_t *>(listed + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(qfull(i), 1);
-      mbar_init(pfull(i), OU_CVT_WARPS);
+      mbar_init(full(i), 1);
+      mbar_init(clean(i), OU_SUM_WARPS);
       mbar_init(empty(i), 1);
     }
-    mbar_init(done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tfull(i), 1);
+      mbar_init(tempty(i), 32 * OU_SUM_WARPS);
+    }
+    mbar_init(drain, 1);
     ctl->abort = 0;
-    *largest = 0;
     fence_mbar_init();
     tma_prefetch_desc(&job.q);
   }
-  if (warp == 2) {
+  if (warp == 1) {
     tmem_alloc(smem_u32(&ctl->tmem), p.tmem_cols);
     tmem_relinquish();
-  }
-  // the columns between r and r16 of every P tile stay zero
-  if (p.r16 != p.r) {
-    for (int i = threadIdx.x; i < p.stages * 2 * OU_KB; i += OU_THREADS) {
-      const int st = i / (2 * OU_KB), hl = (i / OU_KB) & 1, k = i % OU_KB;
-      *reinterpret_cast<uint4 *>(base + st * p.stage_bytes + OU_Q_BYTES +
-                                 hl * outer_p_bytes(p.r16) + (p.r / 8) * (OU_KB * 16) + k * 16) =
-          make_uint4(0u, 0u, 0u, 0u);
-    }
-    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-  grid_dependency_wait();
+  grid_dependency_wait();  // P, info and amax are the preceding kernels'
+
+  // sums of a thread's feature: product `prod`, TMEM lane quarter (warp & 3)
+  const int prod = (warp - 2) >> 2;
+  float acc[NC * 8];
+#pragma unroll
+  for (int t = 0; t < NC * 8; ++t) acc[t] = 0.0f;
 
   const int64_t blocks = ((int64_t)p.s + OU_KB - 1) / OU_KB;
-  // the adapter's largest |p| (all rows), for its exact scaling
-  {
-    float m = 0.0f;
-    for (int64_t i = threadIdx.x; i < p.s; i += OU_THREADS) {
-      const float pm = p.pmax[i];
-      m = fmaxf(m, p.ids[i] == a ? pm : 0.0f);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (lane == 0 && m > 0.0f) atomicMax(largest, __float_as_uint(m));
-  }
-  // barriers and parities run on over the windows
-  uint32_t it0 = 0;  // stages this CTA has used before the window
+  uint32_t it0 = 0;  // blocks this CTA has used before the window (a multiple
+                     // of OU_DRAIN: a window's last accumulator may sum fewer)
   bool failed = false;
   for (int64_t w0 = 0; w0 < blocks; w0 += OU_WINDOW) {
     const int nb = (int)min((int64_t)OU_WINDOW, blocks - w0);
-    // which rows of each block are the adapter's: two blocks per warp step
-    for (int b = 2 * warp; b < nb; b += 2 * (OU_THREADS / 32)) {
-      const int64_t r0 = (w0 + b) * OU_KB + lane * 4;
-      int bitsel = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (r0 + e < p.s && p.ids[r0 + e] == a) bitsel |= 1 << e;
-      // lanes 0-15: rows of block b, lanes 16-31: of block b + 1
-      uint64_t m = (uint64_t)bitsel << (4 * (lane & 15));
-#pragma unroll
-      for (int d = 8; d > 0; d >>= 1) m |= __shfl_xor_sync(0xffffffffu, m, d);
-      if ((lane & 15) == 0 && b + (lane >> 4) < nb) masks[b + (lane >> 4)] = m;
+    // which rows of each block are the adapter's
+    for (int b = 32 * warp; b < nb; b += OU_THREADS) {
+      const int32_t what = b + lane < nb ? p.info[w0 + b + lane] : OU_NONE;
+      if (b + lane < nb && what != OU_MIXED) masks[b + lane] = what == a ? ~0ull : 0ull;
+      unsigned mixed = __ballot_sync(0xffffffffu, what == OU_MIXED);
+      while (mixed) {
+        const int e = __ffs(mixed) - 1;
+        mixed &= mixed - 1;
+        const int64_t r0 = (w0 + b + e) * OU_KB + lane;
+        const unsigned lo = __ballot_sync(0xffffffffu, r0 < p.s && p.ids[r0] == a);
+        const unsigned hi = __ballot_sync(0xffffffffu, r0 + 32 < p.s && p.ids[r0 + 32] == a);
+        if (lane == 0) masks[b + e] = (uint64_t)hi << 32 | lo;
+      }
     }
     __syncthreads();
     if (warp == 0) {  // the non-empty blocks, in order
@@ -818,9 +909,10 @@ __global__ void __launch_bounds__(OU_THREADS, 1)
     }
     __syncthreads();
     const int32_t total = *listed;
-    const int32_t mine = total > (int32_t)cta ? (total - (int32_t)cta + p.split - 1) / p.split : 0;
     // this CTA's i-th block of the window is list[cta + i * split]
+    const int32_t mine = total > (int32_t)cta ? (total - (int32_t)cta + p.split - 1) / p.split : 0;
     if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------- TMA producer
       for (int32_t i = 0; i < mine; ++i) {
         const uint32_t it = it0 + i;
         const int st = (int)(it % p.stages);
@@ -828,129 +920,127 @@ __global__ void __launch_bounds__(OU_THREADS, 1)
                                LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns))
           break;
         const uint32_t dst = ring + st * p.stage_bytes;
-        const int32_t row = (int32_t)((w0 + list[cta + i * p.split]) * OU_KB);
-        mbar_arrive_expect_tx(qfull(st), OU_Q_BYTES);
+        const int64_t b = w0 + list[cta + i * p.split];
+        mbar_arrive_expect_tx(full(st), OU_Q_BYTES + p_bytes);
 #pragma unroll
         for (int c = 0; c < OU_COLS / 64; ++c)
-          tma_load_2d(dst + c * OU_BLOCK_BYTES, &job.q, qfull(st), col0 + c * 64, row);
+          tma_load_2d(dst + c * OU_BLOCK_BYTES, &job.q, full(st), col0 + c * 64,
+                      (int32_t)(b * OU_KB));
+        bulk_load_1d(dst + OU_Q_BYTES, p.p + (size_t)b * p_bytes, p_bytes, full(st));
       }
     } else if (warp == 1 && lane == 0) {
-      const uint32_t idesc = idesc_f16_f32_mn(128, p.r16, true, true);
+      // ----------------------------------------------------- MMA issuer
+      const uint32_t idesc = idesc_f16_f32_mn(128, r16, true, true);
       for (int32_t i = 0; i < mine; ++i) {
-        const uint32_t it = it0 + i;
+        const uint32_t it = it0 + i, use = it / OU_DRAIN, buf = use & 1u;
         const int st = (int)(it % p.stages);
         const uint32_t par = (it / p.stages) & 1u;
-        if (!mbar_wait_bounded(qfull(st), par, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
+        const bool fresh = it % OU_DRAIN == 0;
+        if ((fresh && !mbar_wait_bounded(tempty(buf), ((use >> 1) & 1u) ^ 1u, abort_flag, p.status,
+                                         LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) ||
+            !mbar_wait_bounded(full(st), par, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
                                p.timeout_ns) ||
-            !mbar_wait_bounded(pfull(st), par, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
+            !mbar_wait_bounded(clean(st), par, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
                                p.timeout_ns))
           break;
         tc_fence_after();
         const uint32_t src = ring + st * p.stage_bytes;
-        const uint32_t acc = it % p.accs;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
           for (int hl = 0; hl < 2; ++hl)
 #pragma unroll
             for (int k = 0; k < OU_KB / 16; ++k)
-              mma_f16(tmem + (acc * 2 + c) * p.r16,
+              mma_f16(tmem + (buf * 2 + c) * r16,
                       smem_desc_mn_sw128(src + c * 2 * OU_BLOCK_BYTES + k * 2048, OU_BLOCK_BYTES),
-                      smem_desc_core(src + OU_Q_BYTES + hl * outer_p_bytes(p.r16) + k * 256, 128,
-                                     OU_KB * 16),
-                      idesc, (it >= (uint32_t)p.accs || hl > 0 || k > 0) ? 1u : 0u);
+                      smem_desc_core(src + OU_Q_BYTES + hl * (p_bytes / 2) + k * 256, 128,
+                                     OU_CORE),
+                      idesc, (!fresh || hl > 0 || k > 0) ? 1u : 0u);
         mma_commit(empty(st));
+        if (it % OU_DRAIN == OU_DRAIN - 1 || i + 1 == mine) mma_commit(tfull(buf));
       }
-    } else if (warp >= 4) {
-      // ------------------------- P tiles: hi and lo octets of 64 rows
-      const int grp = (warp - 4) / OU_CVT_WARPS;
-      const int ct = (threadIdx.x - 128) % (32 * OU_CVT_WARPS);
+    } else if (warp >= 2) {
+      const int ct = threadIdx.x - 64;
       const int k = ct & 63, o0 = ct >> 6;
-      const float f = pow2(-scale_exponent(__uint_as_float(*largest)));
-      for (int32_t i = 0; i < mine; ++i) {
-        const uint32_t it = it0 + i;
-        if ((int)(it % OU_CVT_GROUPS) != grp) continue;
-        const int st = (int)(it % p.stages);
-        const uint32_t par = (it / p.stages) & 1u;
-        const int32_t b = list[cta + i * p.split];
-        const uint64_t mask = masks[b];
-        const int64_t row = (w0 + b) * OU_KB + k;
-        const bool in = (mask >> k) & 1u;
-        bool ok = mbar_wait_bounded(empty(st), par ^ 1u, abort_flag, p.status,
-                                    LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        uint8_t *dst = base + st * p.stage_bytes + OU_Q_BYTES;
-        for (int oct = o0; oct < p.r / 8; oct += 2) {
-          float x[8] = {};
-          if (in) {
-            Vec8<float> v;
-            v.load(p.p + row * p.r + oct * 8);
-            v.get(x);
+      bool ok = true;
+      // group j of OU_DRAIN blocks is cleaned while group j - 1 is multiplied
+      for (int32_t j = 0; ok && j <= (mine + OU_DRAIN - 1) / OU_DRAIN; ++j) {
+        for (int32_t i = j * OU_DRAIN; ok && i < min(mine, (j + 1) * OU_DRAIN); ++i) {
+          const uint32_t it = it0 + i;
+          const int st = (int)(it % p.stages);
+          const uint64_t mask = masks[list[cta + i * p.split]];
+          // (awaited before a block without such rows too: the barrier takes
+          // one round of arrivals per use of its slot)
+          ok = mbar_wait_bounded(full(st), (it / p.stages) & 1u, abort_flag, p.status,
+                                 LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (mask != ~0ull) {
+            if (!((mask >> k) & 1u)) {
+              uint8_t *q = base + st * p.stage_bytes;
+              const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+              for (int c = o0; c < 8 * (OU_COLS / 64); c += 4)
+                *reinterpret_cast<uint4 *>(q + (c >> 3) * OU_BLOCK_BYTES + k * 128 +
+                                           (c & 7) * 16) = zero;
+              for (int oct = o0; oct < 2 * (r16 / 8); oct += 4)
+                *reinterpret_cast<uint4 *>(q + OU_Q_BYTES + oct * OU_CORE + k * 16) = zero;
+            }
+            fence_proxy_async_smem();
           }
-          uint4 hi, lo;
-          split8(x, f, hi, lo);
-          *reinterpret_cast<uint4 *>(dst + oct * (OU_KB * 16) + k * 16) = hi;
-          *reinterpret_cast<uint4 *>(dst + outer_p_bytes(p.r16) + oct * (OU_KB * 16) + k * 16) = lo;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(clean(st));
         }
-        if (mask != ~0ull) {
-          // rows of other adapters: zeros in Q too, whatever they hold
-          ok = mbar_wait_bounded(qfull(st), par, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
-                                 p.timeout_ns);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          if (!in) {
-            uint8_t *q = base + st * p.stage_bytes + k * 128;
-            for (int c = o0; c < 8 * (OU_COLS / 64); c += 2)
-              *reinterpret_cast<uint4 *>(q + (c >> 3) * OU_BLOCK_BYTES + (c & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-          }
+        if (!ok || j == 0) continue;
+        const uint32_t use = it0 / OU_DRAIN + j - 1, buf = use & 1u;
+        ok = mbar_wait_bounded(tfull(buf), (use >> 1) & 1u, abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_EPILOGUE, p.timeout_ns);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        const uint32_t src =
+            tmem + ((uint32_t)((warp & 3) * 32) << 16) + (buf * 2 + prod) * r16;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          if (c * 8 >= p.r) break;
+          uint32_t v[8];
+          tmem_ld_32x32b_x8(src + c * 8, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[c * 8 + e] += __uint_as_float(v[e]);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pfull(st));
+        tc_fence_before();
+        mbar_arrive(tempty(buf));
       }
     }
     __syncthreads();
-    it0 += (uint32_t)mine;
+    it0 += (uint32_t)((mine + OU_DRAIN - 1) / OU_DRAIN * OU_DRAIN);
     if (*abort_flag) {
       failed = true;
       break;
     }
   }
-  // all products done (commits arrive in order; the last one stands for all)
-  if (warp == 1 && lane == 0) mma_commit(done);
-  {
-    volatile int never = 0;
-    mbar_wait_bounded(done, 0, &never, p.status, LLMINT8_DEV_TIMEOUT_DRAIN, p.timeout_ns);
-  }
-  if (failed) {
-    // copies in flight land before shared memory goes
+  if (failed) {  // MMAs and copies in flight end before shared memory goes
+    if (warp == 1 && lane == 0) {
+      volatile int never = 0;
+      mma_commit(drain);
+      mbar_wait_bounded(drain, 0, &never, p.status, LLMINT8_DEV_TIMEOUT_DRAIN, p.timeout_ns);
+    }
     const uint64_t t0 = global_timer_ns();
     while (global_timer_ns() - t0 < 200000u) __nanosleep(1000);
+    __syncthreads();
   }
-  tc_fence_after();
-  // partial sums [r][OU_COLS] over the ring's memory, one thread per feature
+  // partial sums [r][OU_COLS] over the ring's memory (every product has been
+  // read, so every copy has landed)
   float *part = reinterpret_cast<float *>(base);
-  const int32_t used = (int32_t)min(it0, (uint32_t)p.accs);
-  if (warp >= 4) {
-    const int lanes = (warp & 3) * 32, c = (warp - 4) >> 2;  // two products of 128 features
-    for (int t = 0; t < p.r; t += 8) {
-      float sum[8] = {};
-      for (int q = 0; q < used; ++q) {
-        uint32_t v[8];
-        tmem_ld_32x32b_x8(tmem + ((uint32_t)lanes << 16) + (uint32_t)((q * 2 + c) * p.r16 + t), v);
-        tmem_ld_wait();
+  if (warp >= 2) {
+    const int feature = prod * 128 + (warp & 3) * 32 + lane;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += __uint_as_float(v[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) part[(t + e) * OU_COLS + c * 128 + lanes + lane] = sum[e];
-    }
+    for (int t = 0; t < NC * 8; ++t)
+      if (t < p.r) part[t * OU_COLS + feature] = acc[t];
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 2) tmem_dealloc(tmem, p.tmem_cols);
+  if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
   if (p.split > 1) cluster_sync();
-  const float f = p.scale[a] * pow2(scale_exponent(__uint_as_float(*largest)));
+  const float f = p.scale[a] * pow2(scale_exponent(__uint_as_float(p.amax[a])));
   const int rk = rank_of(p.rank, a, p.r);
   for (int t = (int)cta; t < p.r; t += p.split) {
     float *dst = p.out + ((int64_t)a * p.r + t) * p.w + col0;

@@ -51,7 +51,13 @@ llmint8_status current_device(Device **out) {
                                (int)lora::SMEM_LIMIT) != cudaSuccess ||
           cudaFuncSetAttribute(lora::k_expand, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)lora::SMEM_LIMIT) != cudaSuccess ||
-          cudaFuncSetAttribute(lora::k_outer, cudaFuncAttributeMaxDynamicSharedMemorySize,
+          cudaFuncSetAttribute(lora::k_outer<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)lora::SMEM_LIMIT) != cudaSuccess ||
+          cudaFuncSetAttribute(lora::k_outer<4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)lora::SMEM_LIMIT) != cudaSuccess ||
+          cudaFuncSetAttribute(lora::k_outer<8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)lora::SMEM_LIMIT) != cudaSuccess ||
+          cudaFuncSetAttribute(lora::k_outer<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)lora::SMEM_LIMIT) != cudaSuccess)
         return LLMINT8_ERR_CUDA;
       cudaLaunchConfig_t cfg = {};
@@ -103,20 +109,27 @@ bool overlap(const void *p, size_t pn, const void *q, size_t qn) {
 constexpr int64_t kRowKernelMaxRows = 16;
 
 struct AdapterLayout {
-  size_t v, g, vmax, gmax, part, end;
+  size_t v, g, vmax, gmax, amax, part, info, vpack, gpack, end;
 };
 
 int64_t row_slices(int64_t h) { return (h + lora::RS_SLICE - 1) / lora::RS_SLICE; }
 
-AdapterLayout adapter_layout(int64_t s, int64_t h, int32_t r) {
+AdapterLayout adapter_layout(int64_t s, int64_t h, int32_t n, int32_t r) {
   AdapterLayout L;
   const size_t sr = 4 * (size_t)s * r, s1 = 4 * (size_t)s;
+  const size_t blocks = (size_t)((s + lora::OU_KB - 1) / lora::OU_KB);
+  const size_t packed = blocks * lora::outer_p_bytes(r);
   L.v = kStateBytes;
   L.g = align256(L.v + sr);
   L.vmax = align256(L.g + sr);
   L.gmax = align256(L.vmax + s1);
-  L.part = align256(L.gmax + s1);
-  L.end = align256(L.part + 4 * (size_t)(row_slices(h) * std::min(s, kRowKernelMaxRows)) * r);
+  L.amax = align256(L.gmax + s1);  // [2][n]: v's, g's
+  L.part = align256(L.amax + 8 * (size_t)n);
+  L.info = align256(L.part +
+                    4 * (size_t)(row_slices(h) * std::min(s, kRowKernelMaxRows)) * r);
+  L.vpack = align256(L.info + 4 * blocks);
+  L.gpack = align256(L.vpack + packed);
+  L.end = align256(L.gpack + packed);
   return L;
 }
 
@@ -150,26 +163,37 @@ int cluster_split(int64_t tiles, int64_t limit, int sm_count) {
   return split;
 }
 
-// v = X . F^T with the row maxima; w, wmax: another [s][r] array's maxima too.
+// Shared memory of a CTA when an SM holds two.
+constexpr uint32_t kHalfSmem = 113 * 1024;
+
+// v = X . F^T with the largest values per row and per adapter (amax, or
+// null); w, w_amax: another [s][r] array's per adapter.
 bool shrink_job(lora::ShrinkJob *job, const uint16_t *X, int64_t s, int64_t k, const uint16_t *F,
                 const llmint8_adapters *ad, const int32_t *ids, float *v, float *vmax,
-                const float *w, float *wmax, int split, void *ws) {
+                uint32_t *amax, const float *w, uint32_t *w_amax, int split, void *ws) {
   lora::ShrinkParams &p = job->p;
   p.s = (int32_t)s;
   p.k = (int32_t)k;
   p.n = ad->n;
   p.r = ad->r;
   p.split = split;
-  p.slots = lora::SH_COLS / ad->r;
+  p.slots = lora::shrink_slots(ad->r);
   p.stage_bytes = lora::shrink_stage_bytes(ad->r);
+  // two CTAs per SM (three stages at least in half of its shared memory) up
+  // to r = 64, one above
+  const uint32_t limit = ad->r <= 64 ? kHalfSmem : lora::SMEM_LIMIT;
   p.stages = (int32_t)std::min<uint32_t>(
-      lora::SH_MAX_STAGES, (lora::SMEM_LIMIT - lora::shrink_fixed_bytes(ad->r)) / p.stage_bytes);
+      lora::SH_MAX_STAGES, (limit - lora::shrink_fixed_bytes(ad->r)) / p.stage_bytes);
+  p.cols = lora::shrink_cols(ad->r);
+  p.tmem_cols = 256;
+  p.accs = std::min(lora::SH_MAX_ACC, p.tmem_cols / p.cols);
   p.ids = ids;
   p.rank = ad->rank_dev;
   p.v = v;
   p.vmax = vmax;
+  p.amax = amax;
   p.w = w;
-  p.wmax = wmax;
+  p.w_amax = w_amax;
   p.status = static_cast<int32_t *>(ws);
   p.timeout_ns = kTimeoutNs;
   return make_tmap_f16(&job->x, const_cast<uint16_t *>(X), (uint64_t)k, (uint64_t)s, lora::SH_KB,
@@ -187,8 +211,9 @@ cudaError_t launch_shrink(const lora::ShrinkJob *jobs, int n_jobs, cudaStream_t 
                          jobs[n_jobs - 1]);
 }
 
-int shrink_split(int64_t s, int64_t k, int n_jobs, int sm_count) {
-  return cluster_split(n_jobs * ceil_div(s, lora::TM), ceil_div(k, 2 * lora::SH_KB), sm_count);
+int shrink_split(int64_t s, int64_t k, int32_t r, int n_jobs, int sm_count) {
+  return cluster_split(n_jobs * ceil_div(s, lora::TM), ceil_div(k, 2 * lora::SH_KB),
+                       r <= 64 ? 2 * sm_count : sm_count);
 }
 
 // out = base + scale * v . F
@@ -204,7 +229,7 @@ llmint8_status enqueue_expand(const float *v, const float *vmax, int64_t s, int6
   p.steps = (int32_t)ceil_div(o, lora::EX_N);
   // two CTAs per SM while v's operand leaves room for their rings
   const int per_sm = ad->r <= 64 ? 2 : 1;
-  const uint32_t limit = per_sm == 2 ? 114 * 1024 : lora::SMEM_LIMIT;
+  const uint32_t limit = per_sm == 2 ? kHalfSmem : lora::SMEM_LIMIT;
   p.fbufs = ad->r <= 32 ? 4 : 2;
   p.ring = 2;
   while (p.ring < lora::EX_MAX_RING && lora::expand_bytes(ad->r, p.ring + 1, p.fbufs) <= limit)
@@ -242,24 +267,27 @@ llmint8_status enqueue_expand(const float *v, const float *vmax, int64_t s, int6
 }
 
 // dF = scale * P^T . Q per adapter
-bool outer_job(lora::OuterJob *job, const float *pp, const float *pmax, const uint16_t *Q,
-               int64_t s, int64_t w, const llmint8_adapters *ad, const int32_t *ids, float *out,
-               void *ws) {
+bool outer_job(lora::OuterJob *job, const uint8_t *packed, const int32_t *info,
+               const uint32_t *amax, const uint16_t *Q, int64_t s, int64_t w,
+               const llmint8_adapters *ad, const int32_t *ids, float *out, void *ws) {
   lora::OuterParams &p = job->p;
   p.s = (int32_t)s;
   p.w = (int32_t)w;
   p.n = ad->n;
   p.r = ad->r;
-  p.r16 = (ad->r + 15) / 16 * 16;
-  p.stage_bytes = lora::OU_Q_BYTES + 2 * lora::outer_p_bytes(p.r16);
+  const int32_t r16 = lora::outer_r16(ad->r);
+  p.stage_bytes = lora::OU_Q_BYTES + lora::outer_p_bytes(ad->r);
+  // two CTAs per SM up to r = 64, one above
+  const bool half = ad->r <= 64;
   p.stages = (int32_t)std::min<uint32_t>(
-      lora::OU_MAX_STAGES, (lora::SMEM_LIMIT - lora::OU_FIXED_BYTES) / p.stage_bytes);
-  p.accs = std::min(4, 512 / (2 * p.r16));
-  p.tmem_cols = 32;
-  while (p.tmem_cols < p.accs * 2 * p.r16) p.tmem_cols *= 2;
+      lora::OU_MAX_STAGES,
+      ((half ? kHalfSmem : lora::SMEM_LIMIT) - lora::OU_FIXED_BYTES) / p.stage_bytes);
+  p.tmem_cols = 32;  // two accumulators for each of the two products
+  while (p.tmem_cols < 4 * r16) p.tmem_cols *= 2;
   p.col_tiles = (int32_t)ceil_div(w, lora::OU_COLS);
-  p.p = pp;
-  p.pmax = pmax;
+  p.p = packed;
+  p.info = info;
+  p.amax = amax;
   p.ids = ids;
   p.rank = ad->rank_dev;
   p.scale = ad->scale_dev;
@@ -276,17 +304,22 @@ cudaError_t launch_outer(lora::OuterJob *jobs, int n_jobs, int sm_count, cudaStr
   // the fewest rounds for their length (a CTA's start counted as four blocks)
   const lora::OuterParams &p = jobs[0].p;
   const int64_t blocks = ceil_div(p.s, lora::OU_KB);
+  const int64_t room = p.r <= 64 ? 2 * sm_count : sm_count;
   int split = 1;
   int64_t best = INT64_MAX;
-  for (int c = 1; c <= 8 && c <= blocks; c *= 2) {
-    const int64_t cost = ceil_div(tiles * p.n * c, sm_count) * (ceil_div(blocks, c) + 4);
+  for (int c = 1; c <= 8 && c <= blocks; ++c) {
+    const int64_t cost = ceil_div(tiles * p.n * c, room) * (ceil_div(blocks, c) + 4);
     if (cost < best) {
       best = cost;
       split = c;
     }
   }
   for (int i = 0; i < n_jobs; ++i) jobs[i].p.split = split;
-  return launch_clusters(lora::k_outer, dim3((unsigned)(tiles * split), 1, (unsigned)p.n),
+  auto *k = p.r <= 16   ? lora::k_outer<2>
+            : p.r <= 32 ? lora::k_outer<4>
+            : p.r <= 64 ? lora::k_outer<8>
+                        : lora::k_outer<16>;
+  return launch_clusters(k, dim3((unsigned)(tiles * split), 1, (unsigned)p.n),
                          dim3(lora::OU_THREADS),
                          lora::OU_FIXED_BYTES + p.stages * p.stage_bytes, st, split, true, jobs[0],
                          jobs[n_jobs - 1]);
@@ -397,7 +430,7 @@ extern "C" {
 
 size_t llmint8_adapters_workspace_size(int64_t s, int64_t h, int64_t o, int32_t n, int32_t r) {
   if (check_adapter_sizes(s, h, o, n, r)) return 0;
-  return adapter_layout(s, h, r).end;
+  return adapter_layout(s, h, n, r).end;
 }
 
 llmint8_status llmint8_adapters_forward(const uint16_t *X_dev, int64_t s,
@@ -415,7 +448,7 @@ llmint8_status llmint8_adapters_forward(const uint16_t *X_dev, int64_t s,
   if (overlap(out_dev, out_bytes, X_dev, in_bytes) ||
       (base_dev != out_dev && overlap(out_dev, out_bytes, base_dev, out_bytes)))
     return LLMINT8_ERR_ARG;
-  const AdapterLayout L = adapter_layout(s, ad->h, ad->r);
+  const AdapterLayout L = adapter_layout(s, ad->h, ad->n, ad->r);
   if (ws_bytes < L.end) return LLMINT8_ERR_WORKSPACE;
   Device *dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
@@ -440,7 +473,7 @@ llmint8_status llmint8_adapters_forward(const uint16_t *X_dev, int64_t s,
   float *vmax = reinterpret_cast<float *>(wsb + L.vmax);
   lora::ShrinkJob job;
   if (!shrink_job(&job, X_dev, s, ad->h, ad->a_dev, ad, ids_dev, v, vmax, nullptr, nullptr,
-                  shrink_split(s, ad->h, 1, dev->sm_count), ws_dev) ||
+                  nullptr, shrink_split(s, ad->h, ad->r, 1, dev->sm_count), ws_dev) ||
       launch_shrink(&job, 1, st) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   if ((rc = enqueue_expand(v, vmax, s, ad->o, ad->b_dev, ad, ids_dev, base_dev, out_dev, ws_dev,
@@ -467,7 +500,7 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
   if (overlap(dX_dev, in_bytes, X_dev, in_bytes) || overlap(dX_dev, in_bytes, dY_dev, out_bytes) ||
       (base_dev != dX_dev && overlap(dX_dev, in_bytes, base_dev, in_bytes)))
     return LLMINT8_ERR_ARG;
-  const AdapterLayout L = adapter_layout(s, ad->h, ad->r);
+  const AdapterLayout L = adapter_layout(s, ad->h, ad->n, ad->r);
   if (s > 0 && ws_bytes < L.end) return LLMINT8_ERR_WORKSPACE;
   Device *dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
@@ -483,36 +516,53 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
   float *v = reinterpret_cast<float *>(wsb + L.v), *g = reinterpret_cast<float *>(wsb + L.g);
   float *vmax = reinterpret_cast<float *>(wsb + L.vmax);
   float *gmax = reinterpret_cast<float *>(wsb + L.gmax);
+  uint32_t *v_amax = reinterpret_cast<uint32_t *>(wsb + L.amax), *g_amax = v_amax + ad->n;
   const bool need_g = dX_dev || dA_dev;
-  const bool own_v = dB_dev && v_dev;  // v as the caller kept it: only its row maxima
+  const bool own_v = dB_dev && v_dev;  // v as the caller kept it: only its maxima
+  const bool sums = dA_dev || dB_dev;
+  int32_t *info = reinterpret_cast<int32_t *>(wsb + L.info);
   lora::ShrinkJob shrink[2];
   lora::OuterJob outer[2];
+  lora::PackJob pack[2];
   int n_shrink = 0, n_outer = 0;
   const int want = (need_g ? 1 : 0) + (need_v ? 1 : 0);
-  const int split = std::min(shrink_split(s, ad->h, want, dev->sm_count),
-                             shrink_split(s, ad->o, want, dev->sm_count));
+  const int split = std::min(shrink_split(s, ad->h, ad->r, want, dev->sm_count),
+                             shrink_split(s, ad->o, ad->r, want, dev->sm_count));
   if (need_g && !shrink_job(&shrink[n_shrink++], dY_dev, s, ad->o, ad->b_dev, ad, ids_dev, g, gmax,
-                            own_v ? v_dev : nullptr, vmax, split, ws_dev))
+                            dA_dev ? g_amax : nullptr, own_v ? v_dev : nullptr, v_amax, split,
+                            ws_dev))
     return LLMINT8_ERR_CUDA;
   if (need_v && !shrink_job(&shrink[n_shrink++], X_dev, s, ad->h, ad->a_dev, ad, ids_dev, v, vmax,
-                            nullptr, nullptr, split, ws_dev))
+                            v_amax, nullptr, nullptr, split, ws_dev))
     return LLMINT8_ERR_CUDA;
-  if (dB_dev && !outer_job(&outer[n_outer++], v_dev ? v_dev : v, vmax, dY_dev, s, ad->o, ad,
-                           ids_dev, dB_dev, ws_dev))
-    return LLMINT8_ERR_CUDA;
-  if (dA_dev &&
-      !outer_job(&outer[n_outer++], g, gmax, X_dev, s, ad->h, ad, ids_dev, dA_dev, ws_dev))
+  if (dB_dev) {
+    pack[n_outer] = {v_dev ? v_dev : v, v_amax, wsb + L.vpack};
+    if (!outer_job(&outer[n_outer++], wsb + L.vpack, info, v_amax, dY_dev, s, ad->o, ad, ids_dev, dB_dev,
+                   ws_dev))
+      return LLMINT8_ERR_CUDA;
+  }
+  if (dA_dev) {
+    pack[n_outer] = {g, g_amax, wsb + L.gpack};
+    if (!outer_job(&outer[n_outer++], wsb + L.gpack, info, g_amax, X_dev, s, ad->h, ad, ids_dev, dA_dev,
+                   ws_dev))
+      return LLMINT8_ERR_CUDA;
+  }
+  if (sums && cudaMemsetAsync(v_amax, 0, 8 * (size_t)ad->n, st) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   if (n_shrink > 0) {
     if (launch_shrink(shrink, n_shrink, st) != cudaSuccess) return LLMINT8_ERR_CUDA;
-  } else if (own_v && launch(lora::k_row_max, dim3((unsigned)ceil_div(s, 8)), dim3(256), 0, st,
-                             false, v_dev, s, ad->r, vmax) != cudaSuccess) {
+  } else if (own_v && launch(lora::k_adapter_max, dim3((unsigned)ceil_div(s, 8)), dim3(256), 0, st,
+                             false, v_dev, s, ad->n, ad->r, ids_dev, v_amax) != cudaSuccess) {
     return LLMINT8_ERR_CUDA;
   }
   if (dX_dev && (rc = enqueue_expand(g, gmax, s, ad->h, ad->a_dev, ad, ids_dev, base_dev, dX_dev,
                                      ws_dev, dev->sm_count, st)))
     return rc;
-  if (n_outer > 0 && launch_outer(outer, n_outer, dev->sm_count, st) != cudaSuccess)
+  if (n_outer > 0 &&
+      (launch(lora::k_pack, dim3((unsigned)ceil_div(s, lora::OU_KB), (unsigned)n_outer),
+              dim3(lora::PK_THREADS), 0, st, true, pack[0], pack[n_outer - 1], (int32_t)s, ad->n,
+              ad->r, ids_dev, info) != cudaSuccess ||
+       launch_outer(outer, n_outer, dev->sm_count, st) != cudaSuccess))
     return LLMINT8_ERR_CUDA;
   return last_launch();
 }
