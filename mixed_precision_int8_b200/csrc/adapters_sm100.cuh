@@ -879,6 +879,8 @@ __global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
   const int64_t blocks = ((int64_t)p.s + OU_KB - 1) / OU_KB;
   uint32_t it0 = 0;  // blocks this CTA has used before the window (a multiple
                      // of OU_DRAIN: a window's last accumulator may sum fewer)
+  uint32_t cleaned = 0;  // phase of each slot's clean barrier, which only
+                         // mixed blocks use
   bool failed = false;
   for (int64_t w0 = 0; w0 < blocks; w0 += OU_WINDOW) {
     const int nb = (int)min((int64_t)OU_WINDOW, blocks - w0);
@@ -940,9 +942,11 @@ __global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
                                          LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) ||
             !mbar_wait_bounded(full(st), par, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
                                p.timeout_ns) ||
-            !mbar_wait_bounded(clean(st), par, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
-                               p.timeout_ns))
+            (masks[list[cta + i * p.split]] != ~0ull &&
+             !mbar_wait_bounded(clean(st), (cleaned >> st) & 1u, abort_flag, p.status,
+                                LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)))
           break;
+        if (masks[list[cta + i * p.split]] != ~0ull) cleaned ^= 1u << st;
         tc_fence_after();
         const uint32_t src = ring + st * p.stage_bytes;
 #pragma unroll
@@ -968,23 +972,20 @@ __global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
           const uint32_t it = it0 + i;
           const int st = (int)(it % p.stages);
           const uint64_t mask = masks[list[cta + i * p.split]];
-          // (awaited before a block without such rows too: the barrier takes
-          // one round of arrivals per use of its slot)
+          if (mask == ~0ull) continue;
           ok = mbar_wait_bounded(full(st), (it / p.stages) & 1u, abort_flag, p.status,
                                  LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          if (mask != ~0ull) {
-            if (!((mask >> k) & 1u)) {
-              uint8_t *q = base + st * p.stage_bytes;
-              const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-              for (int c = o0; c < 8 * (OU_COLS / 64); c += 4)
-                *reinterpret_cast<uint4 *>(q + (c >> 3) * OU_BLOCK_BYTES + k * 128 +
-                                           (c & 7) * 16) = zero;
-              for (int oct = o0; oct < 2 * (r16 / 8); oct += 4)
-                *reinterpret_cast<uint4 *>(q + OU_Q_BYTES + oct * OU_CORE + k * 16) = zero;
-            }
-            fence_proxy_async_smem();
+          if (!((mask >> k) & 1u)) {
+            uint8_t *q = base + st * p.stage_bytes;
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = o0; c < 8 * (OU_COLS / 64); c += 4)
+              *reinterpret_cast<uint4 *>(q + (c >> 3) * OU_BLOCK_BYTES + k * 128 + (c & 7) * 16) =
+                  zero;
+            for (int oct = o0; oct < 2 * (r16 / 8); oct += 4)
+              *reinterpret_cast<uint4 *>(q + OU_Q_BYTES + oct * OU_CORE + k * 16) = zero;
           }
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(clean(st));
         }

@@ -23,6 +23,9 @@ namespace {
 
 using namespace llmint8;
 
+template <typename TX, typename TP>
+bool ln_backward_setup();
+
 struct Device {
   bool init = false;
   bool supported = false;
@@ -58,7 +61,9 @@ llmint8_status current_device(Device **out) {
           cudaFuncSetAttribute(lora::k_outer<8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)lora::SMEM_LIMIT) != cudaSuccess ||
           cudaFuncSetAttribute(lora::k_outer<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)lora::SMEM_LIMIT) != cudaSuccess)
+                               (int)lora::SMEM_LIMIT) != cudaSuccess ||
+          !ln_backward_setup<__half, __half>() || !ln_backward_setup<__half, float>() ||
+          !ln_backward_setup<float, __half>() || !ln_backward_setup<float, float>())
         return LLMINT8_ERR_CUDA;
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 * (unsigned)(d.sm_count / 2));
@@ -389,19 +394,51 @@ cudaError_t ln_forward(const void *x, int64_t s, int64_t h, const void *gamma, c
                 mean, rstd);
 }
 
-// Blocks of the backward kernel: up to kLnBlocksPerSm per SM, never more
-// than rows.
-constexpr int kLnBlocksPerSm = 2;
+// Blocks of the backward kernel, which keeps one partial sum of each column
+// per block: as many as run at once (two or three per SM for the narrower
+// rows), never more than rows.
 constexpr int kLnMaxBlocks = 512;
-int64_t ln_blocks(int64_t s, int sm_count) {
-  return std::max<int64_t>(
-      1, std::min<int64_t>({s, (int64_t)kLnBlocksPerSm * sm_count, (int64_t)kLnMaxBlocks}));
+
+int ln_blocks_per_sm(int64_t h) {
+  if (h > ln::MAX_ROW) return 2;
+  int threads, nv;
+  ln_shape(h, &threads, &nv);
+  return nv > 1 ? 1 : std::min(3, 1024 / threads);
+}
+
+int64_t ln_blocks(int64_t s, int64_t h, int sm_count) {
+  return std::max<int64_t>(1, std::min<int64_t>({s, (int64_t)ln_blocks_per_sm(h) * sm_count,
+                                                 (int64_t)kLnMaxBlocks}));
+}
+
+// nv vectors of 8 columns per thread; two rows at a time or one.
+template <typename TX, typename TP>
+auto ln_backward_kernel(int nv, bool two) {
+  constexpr int U = (int)sizeof(TX) / 2;  // units of 16 bytes in 8 columns
+  return nv == 1   ? (two ? ln::k_ln_backward<TX, TP, U, 2> : ln::k_ln_backward<TX, TP, U, 1>)
+         : nv == 2 ? (two ? ln::k_ln_backward<TX, TP, 2 * U, 2>
+                          : ln::k_ln_backward<TX, TP, 2 * U, 1>)
+         : nv == 3 ? ln::k_ln_backward<TX, TP, 3 * U, 1>
+                   : ln::k_ln_backward<TX, TP, 4 * U, 1>;
+}
+
+constexpr uint32_t kLnSmemPerSm = 224 * 1024;
+
+template <typename TX, typename TP>
+bool ln_backward_setup() {
+  for (int nv = 1; nv <= ln::MAX_VEC; ++nv)
+    for (int two = 0; two < 2; ++two)
+      if (cudaFuncSetAttribute(ln_backward_kernel<TX, TP>(nv, two != 0),
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)kLnSmemPerSm) != cudaSuccess)
+        return false;
+  return true;
 }
 
 template <typename TX, typename TP>
 cudaError_t ln_backward(const uint16_t *dy, const void *x, int64_t s, int64_t h, const void *gamma,
                         const float *mean, const float *rstd, void *dx, float *part,
-                        int64_t blocks, cudaStream_t st) {
+                        int64_t blocks, void *ws, cudaStream_t st) {
   const TX *xp = static_cast<const TX *>(x);
   const TP *gp = static_cast<const TP *>(gamma);
   TX *dxp = static_cast<TX *>(dx);
@@ -411,12 +448,15 @@ cudaError_t ln_backward(const uint16_t *dy, const void *x, int64_t s, int64_t h,
                   as_half(dy), xp, s, (int32_t)h, gp, mean, rstd, dxp, part);
   int threads, nv;
   ln_shape(h, &threads, &nv);
-  auto *k = nv == 1   ? ln::k_ln_backward<TX, TP, 1>
-            : nv == 2 ? ln::k_ln_backward<TX, TP, 2>
-            : nv == 3 ? ln::k_ln_backward<TX, TP, 3>
-                      : ln::k_ln_backward<TX, TP, 4>;
-  return launch(k, grid, dim3(threads), 0, st, false, as_half(dy), xp, s, (int32_t)h, gp, mean,
-                rstd, dxp, part);
+  uint32_t stage = (uint32_t)h * (sizeof(TX) + 2);
+  const uint32_t limit = kLnSmemPerSm / ln_blocks_per_sm(h) - 2048;
+  // two rows at a time where every block has them and three such stages fit
+  const bool two = nv <= 2 && 3 * 2 * stage <= limit && s >= 2 * blocks;
+  if (two) stage *= 2;
+  const int stages = (int)std::min<uint32_t>(ln::BW_MAX_STAGES, limit / stage);
+  return launch(ln_backward_kernel<TX, TP>(nv, two), grid, dim3(threads), stages * stage, st,
+                false, as_half(dy), xp, s, (int32_t)h, stages, gp, mean, rstd, dxp, part,
+                static_cast<int32_t *>(ws), kTimeoutNs);
 }
 
 bool ln_types_ok(int32_t x_type, int32_t p_type) {
@@ -689,18 +729,18 @@ llmint8_status llmint8_layernorm_backward(const uint16_t *dy_dev, const void *x_
       return LLMINT8_ERR_CUDA;
     return LLMINT8_OK;
   }
-  const int64_t blocks = ln_blocks(s, dev->sm_count);
+  const int64_t blocks = ln_blocks(s, h, dev->sm_count);
   float *part = dgamma_dev || dbeta_dev
                     ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws_dev) + kStateBytes)
                     : nullptr;
   auto *f = x_type == LLMINT8_F16
                 ? (p_type == LLMINT8_F16 ? ln_backward<__half, __half> : ln_backward<__half, float>)
                 : (p_type == LLMINT8_F16 ? ln_backward<float, __half> : ln_backward<float, float>);
-  if (f(dy_dev, x_dev, s, h, gamma_dev, mean_dev, rstd_dev, dx_dev, part, blocks, st) !=
+  if (f(dy_dev, x_dev, s, h, gamma_dev, mean_dev, rstd_dev, dx_dev, part, blocks, ws_dev, st) !=
       cudaSuccess)
     return LLMINT8_ERR_CUDA;
   if (part && launch(ln::k_ln_reduce, dim3(blocks_for(2 * h, ln::RED_COLS)),
-                     dim3(ln::RED_COLS * ln::RED_LANES), 0, st, true, (const float *)part,
+                     dim3(ln::RED_COLS / 4 * ln::RED_LANES), 0, st, true, (const float *)part,
                      (int32_t)blocks, (int32_t)h, dgamma_dev, dbeta_dev) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   return last_launch();

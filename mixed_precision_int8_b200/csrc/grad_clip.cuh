@@ -12,8 +12,11 @@
 // the result does not depend on timing, and take their ranges from the end
 // of the list, where the norm kernel's reads are still in L2.
 //
-// Squares are fp64: the square of an fp32 or bf16 gradient above 2^64 or
-// below 2^-75 has no fp32 value.
+// Sums are fp64. The squares of a 16-byte vector are added in fp32 first
+// (converting every element to fp64 took twice as long as its bytes), unless
+// that sum shows that fp32 does not hold them: the square of an fp32 or bf16
+// gradient above 2^64 or below 2^-75 has no fp32 value, and such vectors are
+// squared in fp64.
 #pragma once
 
 #include <cstdint>
@@ -25,7 +28,7 @@ namespace llmint8 {
 namespace clip {
 
 constexpr int THREADS = 512;
-constexpr int CHUNK = 8192;        // elements
+constexpr int CHUNK = 8192;        // elements (one to two vectors of 16 bytes per thread)
 constexpr int MAX_BLOCKS = 1024;   // partial sums a list holds
 constexpr int INIT_ENTRIES = 48;   // entries one launch of k_list_init carries
 
@@ -79,22 +82,48 @@ struct Pack {
   __device__ __forceinline__ Pack() {}
 };
 
+// Sum of squares of one 16-byte vector. A sum between 2^-80 and 2^120 has lost
+// at most its last bits: every square that matters to it is a normal number
+// (one below 2^-126 is below 2^-46 of it), and none overflowed.
+template <typename T>
+__device__ __forceinline__ double vector_square_sum(const Pack<T> &p) {
+  constexpr int N = Pack<T>::N;
+  float f = 0.0f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) f = fmaf(to_f(p.v[e]), to_f(p.v[e]), f);
+  if (f > 8.2718061e-25f && f < 1.329228e36f) return (double)f;
+  double acc = 0.0;
+  if ((p.q.x | p.q.y | p.q.z | p.q.w) != 0) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const double d = (double)to_f(p.v[e]);
+      acc = fma(d, d, acc);
+    }
+  }
+  return acc;
+}
+
 // Sum of squares of elements [0, m) of g, m <= CHUNK.
 template <typename T>
 __device__ __forceinline__ double chunk_square_sum(const T *g, int m) {
   double acc = 0.0;
   constexpr int N = Pack<T>::N;
+  constexpr int PER = CHUNK / N / THREADS;  // vectors per thread in a full chunk
   int done = 0;
   if ((reinterpret_cast<uintptr_t>(g) & 15) == 0) {
     const int nv = m / N;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < nv; i += THREADS) {
-      Pack<T> p;
-      p.q = reinterpret_cast<const uint4 *>(g)[i];
+    if (nv == PER * THREADS) {
+      Pack<T> p[PER];
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const double d = (double)to_f(p.v[e]);
-        acc = fma(d, d, acc);
+      for (int i = 0; i < PER; ++i)
+        p[i].q = __ldg(reinterpret_cast<const uint4 *>(g) + threadIdx.x + i * THREADS);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc += vector_square_sum(p[i]);
+    } else {
+      for (int i = threadIdx.x; i < nv; i += THREADS) {
+        Pack<T> p;
+        p.q = __ldg(reinterpret_cast<const uint4 *>(g) + i);
+        acc += vector_square_sum(p);
       }
     }
     done = nv * N;
@@ -111,14 +140,27 @@ __device__ __forceinline__ void chunk_scale(const T *g, T *out, int m, float coe
   constexpr int N = Pack<T>::N;
   int done = 0;
   if (((reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
+    constexpr int PER = CHUNK / N / THREADS;
     const int nv = m / N;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < nv; i += THREADS) {
-      Pack<T> p;
-      p.q = reinterpret_cast<const uint4 *>(g)[i];
+    if (nv == PER * THREADS) {
+      Pack<T> p[PER];
 #pragma unroll
-      for (int e = 0; e < N; ++e) from_f(p.v[e], to_f(p.v[e]) * coef);
-      reinterpret_cast<uint4 *>(out)[i] = p.q;
+      for (int i = 0; i < PER; ++i)
+        p[i].q = reinterpret_cast<const uint4 *>(g)[threadIdx.x + i * THREADS];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) from_f(p[i].v[e], to_f(p[i].v[e]) * coef);
+        reinterpret_cast<uint4 *>(out)[threadIdx.x + i * THREADS] = p[i].q;
+      }
+    } else {
+      for (int i = threadIdx.x; i < nv; i += THREADS) {
+        Pack<T> p;
+        p.q = reinterpret_cast<const uint4 *>(g)[i];
+#pragma unroll
+        for (int e = 0; e < N; ++e) from_f(p.v[e], to_f(p.v[e]) * coef);
+        reinterpret_cast<uint4 *>(out)[i] = p.q;
+      }
     }
     done = nv * N;
   }
@@ -129,6 +171,7 @@ __global__ void __launch_bounds__(THREADS)
     k_square_sums(const Entry *__restrict__ table, int64_t n, int64_t chunks,
                   double *__restrict__ partial) {
   __shared__ double red[32];
+  grid_dependency_trigger();
   const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
   double acc = 0.0;
   int64_t t = c0 < c1 ? find_entry(table, n, c0) : 0;

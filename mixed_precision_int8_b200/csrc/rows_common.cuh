@@ -81,15 +81,20 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
   return warp_sum(t);
 }
 
-// Two sums at once.
-__device__ __forceinline__ float2 block_sum2(float a, float b, float2 *red) {
+// Two sums at once, and whether `pred` holds in any thread.
+__device__ __forceinline__ float2 block_sum2(float a, float b, float2 *red, bool pred, bool *any) {
   a = warp_sum(a);
   b = warp_sum(b);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
+  *any = __syncthreads_or(pred);
   const int nw = blockDim.x >> 5;
   const float2 t = (int)(threadIdx.x & 31) < nw ? red[threadIdx.x & 31] : make_float2(0.f, 0.f);
   return make_float2(warp_sum(t.x), warp_sum(t.y));
+}
+
+__device__ __forceinline__ float2 block_sum2(float a, float b, float2 *red) {
+  bool any;
+  return block_sum2(a, b, red, false, &any);
 }
 
 }  // namespace llmint8
