@@ -53,6 +53,7 @@ struct TileSlots {
   int32_t id[TM];       // adapter of each row, -1 for none
   int32_t slot[TM];     // number of that adapter within the tile, or -1
   int32_t adapter[TM];  // adapter of each slot, by first row
+  int32_t rank[TM];     // terms that adapter uses
   int32_t first[TM];    // slot of the rows that lead one
   int32_t per_warp[4];
   int32_t count;
@@ -60,7 +61,7 @@ struct TileSlots {
 
 // Whole block (at least TM threads, whole warps).
 __device__ __forceinline__ void tile_slots(const int32_t *ids, int64_t row0, int64_t s, int32_t n,
-                                           TileSlots &ts) {
+                                           const int32_t *rank, int32_t r, TileSlots &ts) {
   const int t = threadIdx.x, w = t >> 5, lane = t & 31;
   int a = -1, lead = t;
   unsigned leaders = 0;
@@ -68,7 +69,18 @@ __device__ __forceinline__ void tile_slots(const int32_t *ids, int64_t row0, int
     if (row0 + t < s) a = adapter_of(ids, row0 + t, n);
     ts.id[t] = a;
   }
-  __syncthreads();
+  // one adapter's rows, perhaps with rows without one
+  const int32_t one = row0 < s ? adapter_of(ids, row0, n) : -1;
+  if (__syncthreads_and(t >= TM || a == one || a < 0)) {
+    if (t < TM) ts.slot[t] = a >= 0 ? 0 : -1;
+    if (t == 0) {
+      ts.adapter[0] = one;
+      ts.rank[0] = one >= 0 ? rank_of(rank, one, r) : 0;
+      ts.count = one >= 0 ? 1 : 0;
+    }
+    __syncthreads();
+    return;
+  }
   if (t < TM) {
     const unsigned same = __match_any_sync(0xffffffffu, a);
     const int head = __ffs(same) - 1;
@@ -94,6 +106,7 @@ __device__ __forceinline__ void tile_slots(const int32_t *ids, int64_t row0, int
     for (int i = 0; i < w; ++i) slot += ts.per_warp[i];
     ts.first[t] = slot;
     ts.adapter[slot] = a;
+    ts.rank[slot] = rank_of(rank, a, r);
   }
   if (t == 0) ts.count = ts.per_warp[0] + ts.per_warp[1] + ts.per_warp[2] + ts.per_warp[3];
   __syncthreads();
@@ -218,10 +231,15 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t cta = p.split > 1 ? cluster_ctarank() : 0;
   const int64_t row0 = (int64_t)(blockIdx.x / p.split) * TM;
+  const int32_t nk = (p.k + SH_KB - 1) / SH_KB;
+  // this CTA's blocks of features are cta, cta + split, ...: the cluster reads
+  // neighbouring parts of a row at a time
+  const int32_t blocks = (nk - (int32_t)cta + p.split - 1) / p.split;
+  const int early = min(p.stages, blocks);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(full_bar(i), 1);
+      mbar_init(full_bar(i), 2);  // X, F
       mbar_init(empty_bar(i), 1);
     }
     for (int a = 0; a < p.accs; ++a) {
@@ -233,6 +251,12 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
     fence_mbar_init();
     tma_prefetch_desc(&job.x);
     tma_prefetch_desc(&job.f);
+    // the first X tiles come in while the rows' adapters are sorted out
+    for (int i = 0; i < early; ++i) {
+      mbar_arrive_expect_tx(full_bar(i), SH_X_BYTES);
+      tma_load_2d(ring + i * p.stage_bytes, &job.x, full_bar(i),
+                  ((int32_t)cta + i * p.split) * SH_KB, (int32_t)row0);
+    }
   }
   if (warp == 2) {
     tmem_alloc(smem_u32(&ctl->tmem), p.tmem_cols);
@@ -240,31 +264,33 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
   }
   grid_dependency_trigger();
   tc_fence_before();
-  tile_slots(p.ids, row0, p.s, p.n, ts);  // ends with a barrier
+  tile_slots(p.ids, row0, p.s, p.n, p.rank, p.r, ts);  // ends with a barrier
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-  const int32_t nk = (p.k + SH_KB - 1) / SH_KB;
-  const int32_t k0 = (int32_t)((int64_t)nk * cta / p.split);
-  const int32_t k1 = (int32_t)((int64_t)nk * (cta + 1) / p.split);
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------ TMA producer
-    uint32_t stage = 0, phase = 0, issued = 0, last_par = 0;
+    uint32_t stage = 0, phase = 0, issued = (1u << early) - 1u, last_par = 0;
     bool ok = true;
+    int32_t ahead = early;  // stages whose X is under way
     for (int32_t s0 = 0; ok && s0 < ts.count; s0 += p.slots) {
       const int32_t ns = min(p.slots, ts.count - s0);
-      for (int32_t kb = k0; kb < k1; ++kb) {
+      for (int32_t i = 0; i < blocks; ++i, --ahead) {
+        const int32_t kb = (int32_t)cta + i * p.split;
         if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.status,
                                LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns)) {
           ok = false;
           break;
         }
         const uint32_t dst = ring + stage * p.stage_bytes;
-        mbar_arrive_expect_tx(full_bar(stage), SH_X_BYTES + (uint32_t)(ns * p.r) * 128);
-        tma_load_2d(dst, &job.x, full_bar(stage), kb * SH_KB, (int32_t)row0);
-        for (int32_t i = 0; i < ns; ++i)
-          tma_load_2d(dst + SH_X_BYTES + (uint32_t)(i * p.r) * 128, &job.f, full_bar(stage),
-                      kb * SH_KB, ts.adapter[s0 + i] * p.r);
+        if (ahead <= 0) {
+          mbar_arrive_expect_tx(full_bar(stage), SH_X_BYTES);
+          tma_load_2d(dst, &job.x, full_bar(stage), kb * SH_KB, (int32_t)row0);
+        }
+        mbar_arrive_expect_tx(full_bar(stage), (uint32_t)(ns * p.r) * 128);
+        for (int32_t q = 0; q < ns; ++q)
+          tma_load_2d(dst + SH_X_BYTES + (uint32_t)(q * p.r) * 128, &job.f, full_bar(stage),
+                      kb * SH_KB, ts.adapter[s0 + q] * p.r);
         issued |= 1u << stage;
         last_par = (last_par & ~(1u << stage)) | (phase << stage);
         if ((int)++stage == p.stages) {
@@ -273,12 +299,15 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
         }
       }
     }
-    if (!ok) {  // let every copy land before shared memory goes
+    if (!ok || ts.count == 0) {  // let every copy land before shared memory goes
       volatile int never = 0;
-      for (int st = 0; st < p.stages; ++st)
-        if ((issued >> st) & 1u)
-          mbar_wait_bounded(full_bar(st), (last_par >> st) & 1u, &never, p.status,
-                            LLMINT8_DEV_TIMEOUT_DRAIN, p.timeout_ns);
+      for (int st = 0; st < p.stages; ++st) {
+        if (!((issued >> st) & 1u)) continue;
+        // an early X tile that never got its F
+        if (ahead > 0 && st >= early - ahead) mbar_arrive(full_bar(st));
+        mbar_wait_bounded(full_bar(st), (last_par >> st) & 1u, &never, p.status,
+                          LLMINT8_DEV_TIMEOUT_DRAIN, p.timeout_ns);
+      }
     }
   } else if (warp == 1 && lane == 0) {
     // ------------------------------------------------------- MMA issuer
@@ -288,8 +317,8 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
     for (int32_t s0 = 0; ok && s0 < ts.count; s0 += p.slots) {
       const uint32_t idesc =
           idesc_f16_f32(TM, (min(p.slots, ts.count - s0) * p.r + 15) / 16 * 16);
-      for (int32_t kb = k0; kb < k1; ++kb) {
-        const int32_t i = (kb - k0) % SH_DRAIN;
+      for (int32_t kb = 0; kb < blocks; ++kb) {
+        const int32_t i = kb % SH_DRAIN;
         ok = (i > 0 || mbar_wait_bounded(tempty(acc), aphase ^ 1u, abort_flag, p.status,
                                          LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) &&
              mbar_wait_bounded(full_bar(stage), phase, abort_flag, p.status,
@@ -309,7 +338,7 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
           stage = 0;
           phase ^= 1u;
         }
-        if (i == SH_DRAIN - 1 || kb + 1 == k1) {
+        if (i == SH_DRAIN - 1 || kb + 1 == blocks) {
           mma_commit(tfull(acc));
           if (++acc == p.accs) {
             acc = 0;
@@ -327,7 +356,7 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
     // ----------------------------------- epilogue: this CTA's partial sums
     const int row = threadIdx.x - 128;
     const int slot = ts.slot[row];
-    const int rk = slot >= 0 ? rank_of(p.rank, ts.adapter[slot], p.r) : 0;
+    const int rk = slot >= 0 ? ts.rank[slot] : 0;
     float *mine = part + row * ldp;
     for (int t = 0; t < p.r; ++t) mine[t] = 0.0f;
     int acc = 0;
@@ -335,7 +364,7 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
     bool ok = true;
     for (int32_t s0 = 0; ok && s0 < ts.count; s0 += p.slots) {
       const int32_t s1 = min(s0 + p.slots, ts.count);
-      for (int32_t kb = k0; kb < k1; kb += SH_DRAIN) {
+      for (int32_t kb = 0; kb < blocks; kb += SH_DRAIN) {
         ok = mbar_wait_bounded(tfull(acc), aphase, abort_flag, p.status,
                                LLMINT8_DEV_TIMEOUT_EPILOGUE, p.timeout_ns);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -419,7 +448,7 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ k_expand
 
 constexpr int EX_N = 64;           // features per step
-constexpr int EX_WARPS = 12, EX_THREADS = 32 * EX_WARPS;
+constexpr int EX_WARPS = 13, EX_THREADS = 32 * EX_WARPS;
 constexpr int EX_EPI_THREADS = 256;
 constexpr int EX_ACC = 4;          // accumulators of EX_N columns
 constexpr int EX_MAX_RING = 8, EX_MAX_F = 4;
@@ -463,23 +492,27 @@ __global__ void __launch_bounds__(EX_THREADS)
   const uint32_t bar0 = smem_u32(bars);
   auto bfull = [&](int i) { return bar0 + 8u * i; };                    // base tile in
   auto bempty = [&](int i) { return bar0 + 8u * (EX_MAX_RING + i); };   // output tile out
-  auto ffull = [&](int i) { return bar0 + 8u * (2 * EX_MAX_RING + i); };
-  auto fempty = [&](int i) { return bar0 + 8u * (2 * EX_MAX_RING + EX_MAX_F + i); };
-  auto tfull = [&](int i) { return bar0 + 8u * (2 * EX_MAX_RING + 2 * EX_MAX_F + i); };
-  auto tempty = [&](int i) { return bar0 + 8u * (2 * EX_MAX_RING + 2 * EX_MAX_F + EX_ACC + i); };
-  const uint32_t drain = bar0 + 8u * (2 * EX_MAX_RING + 2 * EX_MAX_F + 2 * EX_ACC);
-  Ctl *ctl = reinterpret_cast<Ctl *>(bars + 2 * EX_MAX_RING + 2 * EX_MAX_F + 2 * EX_ACC + 1);
+  auto ready = [&](int i) { return bar0 + 8u * (2 * EX_MAX_RING + i); };  // output tile done
+  auto ffull = [&](int i) { return bar0 + 8u * (3 * EX_MAX_RING + i); };
+  auto fempty = [&](int i) { return bar0 + 8u * (3 * EX_MAX_RING + EX_MAX_F + i); };
+  auto tfull = [&](int i) { return bar0 + 8u * (3 * EX_MAX_RING + 2 * EX_MAX_F + i); };
+  auto tempty = [&](int i) { return bar0 + 8u * (3 * EX_MAX_RING + 2 * EX_MAX_F + EX_ACC + i); };
+  const uint32_t drain = bar0 + 8u * (3 * EX_MAX_RING + 2 * EX_MAX_F + 2 * EX_ACC);
+  Ctl *ctl = reinterpret_cast<Ctl *>(bars + 3 * EX_MAX_RING + 2 * EX_MAX_F + 2 * EX_ACC + 1);
   volatile int *abort_flag = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row0 = (int64_t)(blockIdx.x / p.chunks) * TM;
   const int32_t chunk = (int32_t)(blockIdx.x % p.chunks);
-  const int32_t n0 = (int32_t)((int64_t)p.steps * chunk / p.chunks);
-  const int32_t n1 = (int32_t)((int64_t)p.steps * (chunk + 1) / p.chunks);
+  // this CTA's i-th step is chunk + i * chunks: the CTAs of a row tile read
+  // and write neighbouring parts of a row at a time
+  const int32_t mine = (p.steps - chunk + p.chunks - 1) / p.chunks;
+  auto col_of = [&](int32_t i) { return (chunk + i * p.chunks) * EX_N; };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.ring; ++i) {
       mbar_init(bfull(i), 1);
       mbar_init(bempty(i), 1);
+      mbar_init(ready(i), EX_EPI_THREADS);
     }
     for (int i = 0; i < p.fbufs; ++i) {
       mbar_init(ffull(i), 1);
@@ -496,9 +529,9 @@ __global__ void __launch_bounds__(EX_THREADS)
     // the first base tiles (no product of the preceding kernel) come in while
     // the rows' slots and v are set up
     if (p.has_base)
-      for (int i = 0; i < min(p.ring, n1 - n0); ++i) {
+      for (int i = 0; i < min(p.ring, mine); ++i) {
         mbar_arrive_expect_tx(bfull(i), EX_TILE_BYTES);
-        tma_load_2d(ring + i * EX_TILE_BYTES, &tm_base, bfull(i), (n0 + i) * EX_N, (int32_t)row0);
+        tma_load_2d(ring + i * EX_TILE_BYTES, &tm_base, bfull(i), col_of(i), (int32_t)row0);
       }
   }
   if (warp == 2) {
@@ -506,7 +539,7 @@ __global__ void __launch_bounds__(EX_THREADS)
     tmem_relinquish();
   }
   tc_fence_before();
-  tile_slots(p.ids, row0, p.s, p.n, ts);
+  tile_slots(p.ids, row0, p.s, p.n, p.rank, p.r, ts);
   grid_dependency_wait();  // v and vmax are the preceding kernel's
   // v of the tile as the MMA's A operand: core matrices of 8 rows x 8 terms,
   // all of the rows' for an octet of terms one after another; r hi columns,
@@ -540,11 +573,11 @@ __global__ void __launch_bounds__(EX_THREADS)
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
-    const int32_t early = p.has_base ? min(p.ring, n1 - n0) : 0;
+    const int32_t early = p.has_base ? min(p.ring, mine) : 0;
     uint32_t issued = (1u << early) - 1u, last_par = 0;
     if (early == p.ring) phase = 1;
     else slot = early;
-    for (int32_t n = n0 + early; n < n1; ++n) {
+    for (int32_t n = early; n < mine; ++n) {
       if (!mbar_wait_bounded(bempty(slot), phase ^ 1u, abort_flag, p.status,
                              LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns)) {
         ok = false;
@@ -552,7 +585,7 @@ __global__ void __launch_bounds__(EX_THREADS)
       }
       if (p.has_base) {
         mbar_arrive_expect_tx(bfull(slot), EX_TILE_BYTES);
-        tma_load_2d(ring + slot * EX_TILE_BYTES, &tm_base, bfull(slot), n * EX_N, (int32_t)row0);
+        tma_load_2d(ring + slot * EX_TILE_BYTES, &tm_base, bfull(slot), col_of(n), (int32_t)row0);
         issued |= 1u << slot;
         last_par = (last_par & ~(1u << slot)) | (phase << slot);
       } else {
@@ -577,7 +610,7 @@ __global__ void __launch_bounds__(EX_THREADS)
     int fb = 0, acc = 0;
     uint32_t fphase = 0, tphase = 0;
     bool ok = true, any = false;
-    for (int32_t i = 0; ok && i < (n1 - n0) * count; ++i) {
+    for (int32_t i = 0; ok && i < mine * count; ++i) {
       ok = mbar_wait_bounded(tempty(acc), tphase ^ 1u, abort_flag, p.status,
                              LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns) &&
            mbar_wait_bounded(ffull(fb), fphase, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
@@ -609,42 +642,78 @@ __global__ void __launch_bounds__(EX_THREADS)
       mbar_wait_bounded(drain, 0, &never, p.status, LLMINT8_DEV_TIMEOUT_DRAIN, p.timeout_ns);
     }
   } else if (warp == 2 || warp == 3) {
-    // ---------------- factor tiles [rows][64], zeros past the adapter's rank
-    const int32_t jobs = (n1 - n0) * count;
+    // ---------------- factor tiles [rows][64], zeros past the adapter's rank;
+    // a tile's copies are under way while the warp's previous one completes.
+    // fbufs is even, so each buffer is one warp's.
+    const int32_t jobs = mine * count;
+    int32_t pending = -1;  // buffer whose copies were issued last
+    auto publish = [&](int fb) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ffull(fb));
+    };
+    bool ok = true;
     for (int32_t i = warp - 2; i < jobs; i += EX_LOADERS) {
       const int fb = i % p.fbufs;
-      const bool free_slot =
-          mbar_wait_bounded(fempty(fb), (uint32_t)((i / p.fbufs) & 1) ^ 1u, abort_flag, p.status,
-                            LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns);
-      if (!__all_sync(0xffffffffu, free_slot)) break;
-      const int a = ts.adapter[i % count];
-      const int rk = rank_of(p.rank, a, p.r);
-      const int32_t col = (n0 + i / count) * EX_N + (lane & 7) * 8;
+      const uint32_t par = (uint32_t)((i / p.fbufs) & 1) ^ 1u;
+      if (pending >= 0 && !__all_sync(0xffffffffu, mbar_test(fempty(fb), par))) {
+        // no buffer free yet: the previous tile need not wait for one
+        cp_async_wait<0>();
+        publish(pending);
+        pending = -1;
+      }
+      ok = mbar_wait_bounded(fempty(fb), par, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_PRODUCER,
+                             p.timeout_ns);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const int sl = i % count;
+      const int a = ts.adapter[sl], rk = ts.rank[sl];
+      const int32_t col = col_of(i / count) + (lane & 7) * 8;
       const __half *src = p.f + (int64_t)a * p.r * p.o + col;
       const uint32_t dst = fbuf + fb * frows * 128;
       for (int row = lane >> 3; row < frows; row += 4) {
         const int t = row < p.r ? row : row - p.r;
-        const bool ok = t < rk && col < p.o;
+        const bool in = t < rk && col < p.o;
         cp_async_16(dst + row * 128 + (((lane & 7) ^ (row & 7)) << 4),
-                    ok ? src + (int64_t)t * p.o : p.f, ok);
+                    in ? src + (int64_t)t * p.o : p.f, in);
       }
-      cp_async_wait_all();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ffull(fb));
+      cp_async_commit();
+      if (pending >= 0) {
+        cp_async_wait<1>();
+        publish(pending);
+      }
+      pending = fb;
     }
-  } else if (warp >= 4) {
+    cp_async_wait<0>();
+    if (ok && pending >= 0) publish(pending);
+  } else if (warp == EX_WARPS - 1 && lane == 0) {
+    // ---------------------------------------------- output tiles by TMA
+    int prev = -1;  // tile whose store may still read shared memory
+    for (int32_t n = 0; n < mine; ++n) {
+      const int slot = n % p.ring;
+      if (!mbar_wait_bounded(ready(slot), (uint32_t)((n / p.ring) & 1), abort_flag, p.status,
+                             LLMINT8_DEV_TIMEOUT_EPILOGUE, p.timeout_ns))
+        break;
+      tma_store_2d(&tm_out, ring + slot * EX_TILE_BYTES, col_of(n), (int32_t)row0);
+      bulk_commit_group();
+      if (prev >= 0) {
+        bulk_wait_group_read1();
+        mbar_arrive(bempty(prev));
+      }
+      prev = slot;
+    }
+    bulk_wait_group0();
+  } else if (warp >= 4 && warp < EX_WARPS - 1) {
     // --------------------------------------------------------- epilogue
-    // row = TMEM lane; 32 of the step's 64 columns per warp
-    const int et = threadIdx.x - 128;
+    // row = TMEM lane; 32 of the step's 64 columns per warp. All eight warps
+    // take every step: a parity wait tells only neighbouring phases apart, so
+    // no barrier of these rings may have waiters that skip phases.
     const int row = (warp & 3) * 32 + lane, half = (warp - 4) >> 2;
     const int my = ts.slot[row];
     const float f = my >= 0 ? factor[row] : 0.0f;
     int slot = 0, acc = 0;
     uint32_t bphase = 0, tphase = 0;
     bool ok = true;
-    int prev = -1;  // tile whose store may still read shared memory
-    for (int32_t n = n0; ok && n < n1; ++n) {
+    for (int32_t n = 0; ok && n < mine; ++n) {
       ok = mbar_wait_bounded(bfull(slot), bphase, abort_flag, p.status,
                              LLMINT8_DEV_TIMEOUT_EPILOGUE, p.timeout_ns);
       ok = __all_sync(0xffffffffu, ok);
@@ -689,23 +758,14 @@ __global__ void __launch_bounds__(EX_THREADS)
           tphase ^= 1u;
         }
       }
+      if (!ok) break;
       fence_proxy_async_smem();
-      if (named_barrier_or(1, EX_EPI_THREADS, !ok)) break;
-      if (et == 0) {
-        tma_store_2d(&tm_out, ring + slot * EX_TILE_BYTES, n * EX_N, (int32_t)row0);
-        bulk_commit_group();
-        if (prev >= 0) {
-          bulk_wait_group_read1();
-          mbar_arrive(bempty(prev));
-        }
-        prev = slot;
-      }
+      mbar_arrive(ready(slot));
       if (++slot == p.ring) {
         slot = 0;
         bphase ^= 1u;
       }
     }
-    if (et == 0) bulk_wait_group0();
   }
 
   tc_fence_before();
@@ -973,8 +1033,16 @@ __global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
           const int st = (int)(it % p.stages);
           const uint64_t mask = masks[list[cta + i * p.split]];
           if (mask == ~0ull) continue;
-          ok = mbar_wait_bounded(full(st), (it / p.stages) & 1u, abort_flag, p.status,
-                                 LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns);
+          // the slot's previous block multiplied, then this one's copy landed
+          // (its full barrier alone would not do: these warps skip the blocks
+          // that need no cleaning, and a parity wait tells only neighbouring
+          // phases apart. The empty barrier is safe: the group before last is
+          // summed, so at most one of its phases is open.)
+          const uint32_t par = (it / p.stages) & 1u;
+          ok = mbar_wait_bounded(empty(st), par ^ 1u, abort_flag, p.status,
+                                 LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns) &&
+               mbar_wait_bounded(full(st), par, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
+                                 p.timeout_ns);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           if (!((mask >> k) & 1u)) {
             uint8_t *q = base + st * p.stage_bytes;

@@ -4,7 +4,7 @@
 //   coef = min(1, max_norm / (norm + 1e-6))       out = g * coef
 //
 // Bound: bytes. The list of tensors is laid out once, on the device, as a
-// table of entries with the running number of chunks (CHUNK elements) before
+// table of entries with the running number of chunks (CHUNK_BYTES) before
 // each. A launch cuts the chunks of all tensors into equal contiguous ranges,
 // one per block, so thousands of small tensors and a few large ones load the
 // GPU alike. The norm kernel leaves one fp64 partial sum per block; the
@@ -28,7 +28,7 @@ namespace llmint8 {
 namespace clip {
 
 constexpr int THREADS = 512;
-constexpr int CHUNK = 8192;        // elements (one to two vectors of 16 bytes per thread)
+constexpr int CHUNK_BYTES = 16384;  // two vectors of 16 bytes per thread
 constexpr int MAX_BLOCKS = 1024;   // partial sums a list holds
 constexpr int INIT_ENTRIES = 48;   // entries one launch of k_list_init carries
 
@@ -63,6 +63,11 @@ __device__ __forceinline__ int64_t find_entry(const Entry *table, int64_t n, int
     else hi = mid - 1;
   }
   return lo;
+}
+
+// Elements of a chunk of a type.
+__host__ __device__ inline int chunk_elements(int32_t type) {
+  return CHUNK_BYTES / (type == LLMINT8_F32 ? 4 : 2);
 }
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -103,12 +108,12 @@ __device__ __forceinline__ double vector_square_sum(const Pack<T> &p) {
   return acc;
 }
 
-// Sum of squares of elements [0, m) of g, m <= CHUNK.
+// Sum of squares of elements [0, m) of g, at most a chunk.
 template <typename T>
 __device__ __forceinline__ double chunk_square_sum(const T *g, int m) {
   double acc = 0.0;
   constexpr int N = Pack<T>::N;
-  constexpr int PER = CHUNK / N / THREADS;  // vectors per thread in a full chunk
+  constexpr int PER = CHUNK_BYTES / 16 / THREADS;  // vectors per thread in a full chunk
   int done = 0;
   if ((reinterpret_cast<uintptr_t>(g) & 15) == 0) {
     const int nv = m / N;
@@ -140,7 +145,7 @@ __device__ __forceinline__ void chunk_scale(const T *g, T *out, int m, float coe
   constexpr int N = Pack<T>::N;
   int done = 0;
   if (((reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
-    constexpr int PER = CHUNK / N / THREADS;
+    constexpr int PER = CHUNK_BYTES / 16 / THREADS;
     const int nv = m / N;
     if (nv == PER * THREADS) {
       Pack<T> p[PER];
@@ -178,8 +183,9 @@ __global__ void __launch_bounds__(THREADS)
   for (int64_t c = c0; c < c1; ++c) {
     while (t + 1 < n && table[t + 1].chunk0 <= c) ++t;
     const Entry e = table[t];
-    const int64_t at = (c - e.chunk0) * CHUNK;
-    const int m = (int)(e.n - at < CHUNK ? e.n - at : CHUNK);
+    const int full = chunk_elements(e.type);
+    const int64_t at = (c - e.chunk0) * full;
+    const int m = (int)(e.n - at < full ? e.n - at : full);
     if (e.type == LLMINT8_F16)
       acc += chunk_square_sum(static_cast<const __half *>(e.grad) + at, m);
     else if (e.type == LLMINT8_BF16)
@@ -228,8 +234,9 @@ __global__ void __launch_bounds__(THREADS)
     while (t > 0 && table[t].chunk0 > c) --t;
     const Entry e = table[t];
     if (coef == 1.0f && e.out == e.grad) continue;  // nothing to change in place
-    const int64_t at = (c - e.chunk0) * CHUNK;
-    const int m = (int)(e.n - at < CHUNK ? e.n - at : CHUNK);
+    const int full = chunk_elements(e.type);
+    const int64_t at = (c - e.chunk0) * full;
+    const int m = (int)(e.n - at < full ? e.n - at : full);
     if (e.type == LLMINT8_F16)
       chunk_scale(static_cast<const __half *>(e.grad) + at, static_cast<__half *>(e.out) + at, m,
                   coef);

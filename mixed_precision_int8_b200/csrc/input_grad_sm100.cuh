@@ -76,6 +76,7 @@ constexpr int MAX_PARTS = 2 * MAX_PAIRS;  // fp32 tiles the workspace holds
 constexpr size_t PART_ELEMS = 2 * BM * BN;
 
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+static_assert(RAW_STAGES >= STAGES, "see the converters' waits");
 static_assert((2 * STAGES + 2 * RAW_STAGES + 2 * NUM_ACC + 1) * 8 + 8 <= 256, "barrier block size");
 
 // How the tiles are shared out: the first `whole` ones are computed whole,
@@ -403,7 +404,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int32_t idx = pair; ok && unit_at(p.plan, idx, u); idx += npairs) {
       int32_t kb = u.k0 + skip;
       for (; kb < u.k1; kb += CVT_GROUPS) {
-        ok = mbar_wait_bounded(raw_full_bar(rstage), rphase, abort_flag, p.status,
+        // the slot's turn first, then its codes: once the stage STAGES before
+        // this one has been multiplied, the other group is done with its codes
+        // too, so the parity of the codes' barrier is not mistaken for that of
+        // their slot's previous use
+        ok = mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns) &&
+             mbar_wait_bounded(raw_full_bar(rstage), rphase, abort_flag, p.status,
                                LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         const uint8_t *src = base + RAW_OFF + rstage * RAW_STAGE_BYTES;
@@ -416,9 +423,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const float aw = *reinterpret_cast<const float *>(src + RAW_BYTES + 4 * kr);
           sc[i] = kb * BK + kr < p.o ? aw : 0.0f;
         }
-        ok = mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.status,
-                               LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         uint8_t *dst = base + STAGES * A_STAGE_BYTES + stage * B_STAGE_BYTES + blk * B_BLOCK_BYTES;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
