@@ -159,6 +159,7 @@ constexpr int SH_THREADS = 256;
 constexpr int SH_KB = 64;       // features per stage
 constexpr int SH_DRAIN = 4;     // stages (of 4 MMAs) that one accumulator sums
 constexpr int SH_MAX_STAGES = 8;
+constexpr int SH_MAX_SPLIT = 8;
 constexpr int SH_MAX_ACC = 8;
 constexpr uint32_t SH_X_BYTES = TM * SH_KB * 2;
 
@@ -405,11 +406,18 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
     const int row = (int)cta * rows + i;
     if (row0 + row >= p.s) continue;
     float largest = 0.0f;
+#pragma unroll 2
     for (int t = lane; t < p.r; t += 32) {
       float sum = 0.0f;
       if (p.split > 1) {
+        // every CTA's load under way before the first is added
         const uint32_t at = smem_u32(part + row * ldp + t);
-        for (int q = 0; q < p.split; ++q) sum += ld_cluster_f32(mapa_shared(at, (uint32_t)q));
+        float x[SH_MAX_SPLIT];
+#pragma unroll
+        for (int q = 0; q < SH_MAX_SPLIT; ++q)
+          x[q] = q < p.split ? ld_cluster_f32(mapa_shared(at, (uint32_t)q)) : 0.0f;
+#pragma unroll
+        for (int q = 0; q < SH_MAX_SPLIT; ++q) sum += x[q];
       } else {
         sum = part[row * ldp + t];
       }
@@ -782,6 +790,7 @@ constexpr int OU_SUM_WARPS = 8;
 constexpr int OU_THREADS = 32 * (2 + OU_SUM_WARPS);
 constexpr int OU_DRAIN = 2;        // blocks (of 8 MMAs per product) that one accumulator sums
 constexpr int OU_MAX_STAGES = 6;
+constexpr int OU_MAX_SPLIT = 8;
 constexpr int OU_WINDOW = 512;     // blocks of rows looked through at a time
 constexpr uint32_t OU_Q_BYTES = OU_KB * OU_COLS * 2;
 constexpr uint32_t OU_BLOCK_BYTES = OU_KB * 128;  // 64 features x 64 rows
@@ -1111,18 +1120,31 @@ __global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
   if (p.split > 1) cluster_sync();
   const float f = p.scale[a] * pow2(scale_exponent(__uint_as_float(p.amax[a])));
   const int rk = rank_of(p.rank, a, p.r);
-  for (int t = (int)cta; t < p.r; t += p.split) {
-    float *dst = p.out + ((int64_t)a * p.r + t) * p.w + col0;
-    for (int c = threadIdx.x; c < OU_COLS; c += OU_THREADS) {
-      if (col0 + c >= p.w) continue;
-      float sum = 0.0f;
-      const uint32_t at = smem_u32(part + t * OU_COLS + c);
-      if (p.split > 1)
-        for (int q = 0; q < p.split; ++q) sum += ld_cluster_f32(mapa_shared(at, (uint32_t)q));
-      else
-        sum = part[t * OU_COLS + c];
-      dst[c] = t < rk ? f * sum : 0.0f;
+  // this CTA's terms are cta, cta + split, ...; four features per thread, and
+  // every CTA's load under way before the first is added
+  const int quads = OU_COLS / 4, terms = (p.r - (int)cta + p.split - 1) / p.split;
+#pragma unroll 2
+  for (int i = threadIdx.x; i < terms * quads; i += OU_THREADS) {
+    const int t = (int)cta + (i / quads) * p.split, c = (i % quads) * 4;
+    const uint32_t at = smem_u32(part + t * OU_COLS + c);
+    float4 x[OU_MAX_SPLIT];
+#pragma unroll
+    for (int q = 0; q < OU_MAX_SPLIT; ++q)
+      x[q] = q >= p.split    ? make_float4(0.f, 0.f, 0.f, 0.f)
+             : p.split > 1   ? ld_cluster_f32x4(mapa_shared(at, (uint32_t)q))
+                             : *reinterpret_cast<const float4 *>(part + t * OU_COLS + c);
+    float4 sum = x[0];
+#pragma unroll
+    for (int q = 1; q < OU_MAX_SPLIT; ++q) {
+      sum.x += x[q].x;
+      sum.y += x[q].y;
+      sum.z += x[q].z;
+      sum.w += x[q].w;
     }
+    if (col0 + c < p.w)  // w is a multiple of 16; an unused term is 0 whatever its sum
+      *reinterpret_cast<float4 *>(p.out + ((int64_t)a * p.r + t) * p.w + col0 + c) =
+          t < rk ? make_float4(f * sum.x, f * sum.y, f * sum.z, f * sum.w)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   if (p.split > 1) cluster_sync();
 }

@@ -48,8 +48,10 @@ llmint8_status current_device(Device **out) {
       return LLMINT8_ERR_CUDA;
     d.supported = major == 10 && minor == 0;
     if (d.supported) {
-      if (cudaFuncSetAttribute(igrad::k_input_grad, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)igrad::SMEM_BYTES) != cudaSuccess ||
+      if (cudaFuncSetAttribute(igrad::k_input_grad<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)igrad::Smem<1>::BYTES) != cudaSuccess ||
+          cudaFuncSetAttribute(igrad::k_input_grad<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)igrad::Smem<2>::BYTES) != cudaSuccess ||
           cudaFuncSetAttribute(lora::k_shrink, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)lora::SMEM_LIMIT) != cudaSuccess ||
           cudaFuncSetAttribute(lora::k_expand, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -68,7 +70,7 @@ llmint8_status current_device(Device **out) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 * (unsigned)(d.sm_count / 2));
       cfg.blockDim = dim3(igrad::NUM_THREADS);
-      cfg.dynamicSmemBytes = igrad::SMEM_BYTES;
+      cfg.dynamicSmemBytes = igrad::Smem<2>::BYTES;
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
       attr[0].val.clusterDim.x = 2;
@@ -77,7 +79,7 @@ llmint8_status current_device(Device **out) {
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       int clusters = 0;
-      if (cudaOccupancyMaxActiveClusters(&clusters, igrad::k_input_grad, &cfg) != cudaSuccess ||
+      if (cudaOccupancyMaxActiveClusters(&clusters, igrad::k_input_grad<2>, &cfg) != cudaSuccess ||
           clusters < 1)
         return LLMINT8_ERR_CUDA;
       d.max_pairs = std::min({clusters, d.sm_count / 2, igrad::MAX_PAIRS});
@@ -164,7 +166,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // each of `tiles` clusters an SM per CTA, or 1.
 int cluster_split(int64_t tiles, int64_t limit, int sm_count) {
   int split = 1;
-  while (2 * split <= std::min<int64_t>(limit, 8) && tiles * 2 * split <= sm_count) split *= 2;
+  while (2 * split <= std::min<int64_t>(limit, lora::SH_MAX_SPLIT) && tiles * 2 * split <= sm_count) split *= 2;
   return split;
 }
 
@@ -306,14 +308,16 @@ bool outer_job(lora::OuterJob *job, const uint8_t *packed, const int32_t *info,
 cudaError_t launch_outer(lora::OuterJob *jobs, int n_jobs, int sm_count, cudaStream_t st) {
   int64_t tiles = 0;
   for (int i = 0; i < n_jobs; ++i) tiles += jobs[i].p.col_tiles;
-  // the fewest rounds for their length (a CTA's start counted as four blocks)
+  // the fewest rounds for their length (a CTA's start and end counted as
+  // twelve blocks: at 4096 rows of 5120 and 20480 features and rank 64 a split
+  // of 2 takes 133 us in all, 3 149, 4 143, 5 138)
   const lora::OuterParams &p = jobs[0].p;
   const int64_t blocks = ceil_div(p.s, lora::OU_KB);
   const int64_t room = p.r <= 64 ? 2 * sm_count : sm_count;
   int split = 1;
   int64_t best = INT64_MAX;
-  for (int c = 1; c <= 8 && c <= blocks; ++c) {
-    const int64_t cost = ceil_div(tiles * p.n * c, room) * (ceil_div(blocks, c) + 4);
+  for (int c = 1; c <= lora::OU_MAX_SPLIT && c <= blocks; ++c) {
+    const int64_t cost = ceil_div(tiles * p.n * c, room) * (ceil_div(blocks, c) + 12);
     if (cost < best) {
       best = cost;
       split = c;
@@ -332,16 +336,19 @@ cudaError_t launch_outer(lora::OuterJob *jobs, int n_jobs, int sm_count, cudaStr
 
 // ---------------------------------------- gradient of the projection's input
 
-// Whole rounds of tiles first (one tile per pair); the tiles of the last,
-// partial round are cut along the reduction into as many parts as make the
-// rounds they then take shortest. A part costs an fp32 tile written and read
-// back, counted here as two stages. Planned for MAX_PAIRS pairs on any
-// device, so that the workspace size depends on the sizes alone.
+// Tiles of 512 rows where there are more than 256 (each converted weight tile
+// then serves two MMAs), of 256 else. Whole rounds of tiles first (one tile
+// per pair); the tiles of the last, partial round are cut along the reduction
+// into as many parts as make the rounds they then take shortest. A part costs
+// an fp32 tile written and read back, counted here as two stages. Planned for
+// MAX_PAIRS pairs on any device, so that the workspace size depends on the
+// sizes alone.
 igrad::Plan input_grad_plan(int64_t s, int64_t h, int64_t o) {
   igrad::Plan p;
-  p.num_m = (int32_t)((s + 2 * igrad::BM - 1) / (2 * igrad::BM));
-  p.num_n = (int32_t)((h + igrad::BN - 1) / igrad::BN);
-  p.num_k = (int32_t)((o + igrad::BK - 1) / igrad::BK);
+  p.mt = s > 2 * igrad::BM ? 2 : 1;
+  p.num_m = (int32_t)ceil_div(s, p.mt * 2 * igrad::BM);
+  p.num_n = (int32_t)ceil_div(h, igrad::BN);
+  p.num_k = (int32_t)ceil_div(o, igrad::BK);
   const int64_t tiles = (int64_t)p.num_m * p.num_n;
   p.whole = (int32_t)(tiles / igrad::MAX_PAIRS * igrad::MAX_PAIRS);
   p.rest = (int32_t)(tiles - p.whole);
@@ -349,8 +356,8 @@ igrad::Plan input_grad_plan(int64_t s, int64_t h, int64_t o) {
   int64_t best = INT64_MAX;
   for (int32_t parts = 1; p.rest > 0 && parts <= p.num_k && p.rest * parts <= igrad::MAX_PARTS;
        ++parts) {
-    const int64_t rounds = (p.rest * parts + igrad::MAX_PAIRS - 1) / igrad::MAX_PAIRS;
-    const int64_t cost = rounds * ((p.num_k + parts - 1) / parts + (parts > 1 ? 2 : 0)) +
+    const int64_t rounds = ceil_div(p.rest * parts, igrad::MAX_PAIRS);
+    const int64_t cost = rounds * (ceil_div(p.num_k, parts) + (parts > 1 ? 2 : 0)) +
                          (parts > 1 ? 2 * parts : 0);
     if (cost < best) {
       best = cost;
@@ -362,7 +369,7 @@ igrad::Plan input_grad_plan(int64_t s, int64_t h, int64_t o) {
 
 size_t input_grad_workspace(const igrad::Plan &p) {
   const size_t slots = p.parts > 1 ? (size_t)p.rest * p.parts : 0;
-  return align256(kStateBytes + 4 * igrad::PART_ELEMS * slots);
+  return align256(kStateBytes + 4 * igrad::PART_ELEMS * p.mt * slots);
 }
 
 // ----------------------------------------------------------- layer norm
@@ -615,10 +622,11 @@ size_t llmint8_matmul_backward_workspace_size(int64_t s, int64_t h, int64_t o) {
   // up to MAX_PARTS fp32 tiles: the most that any smaller number of rows needs
   // (the plan repeats every MAX_PAIRS tiles of rows)
   size_t bytes = 0;
-  const int64_t num_m = (s + 2 * igrad::BM - 1) / (2 * igrad::BM);
-  for (int64_t m = 0; m < std::min<int64_t>(num_m, igrad::MAX_PAIRS); ++m)
-    bytes = std::max(bytes, input_grad_workspace(
-                                input_grad_plan((num_m - m) * 2 * igrad::BM, h, o)));
+  const int64_t blocks = ceil_div(s, 2 * igrad::BM);
+  for (int64_t m = 0; m < std::min<int64_t>(blocks, 2 * igrad::MAX_PAIRS); ++m)
+    bytes = std::max(bytes,
+                     input_grad_workspace(input_grad_plan((blocks - m) * 2 * igrad::BM, h, o)));
+  if (blocks > 0) bytes = std::max(bytes, input_grad_workspace(input_grad_plan(1, h, o)));
   return std::max(bytes, kStateBytes);
 }
 
@@ -651,27 +659,30 @@ llmint8_status llmint8_matmul_backward(const uint16_t *dY_dev, int64_t s, const 
   p.wq = w->wq_dev;
   p.aw = w->aw_dev;
   p.base = as_half(base_dev);
+  p.out = as_half(dX_dev);
   p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws_dev) + kStateBytes);
   p.status = static_cast<int32_t *>(ws_dev);
   p.timeout_ns = kTimeoutNs;
-  CUtensorMap tmA, tmW, tmOut;
+  CUtensorMap tmA, tmW;
   if (!make_tmap_i8_plain(&tmW, w->wq_dev, (uint64_t)w->h, (uint64_t)w->o, igrad::BNH,
                           igrad::BK) ||
       !make_tmap_f16(&tmA, const_cast<uint16_t *>(dY_dev), (uint64_t)w->o, (uint64_t)s, igrad::BK,
-                     igrad::BM) ||
-      !make_tmap_f16(&tmOut, dX_dev, (uint64_t)w->h, (uint64_t)s, 32, 32))
+                     igrad::BM))
     return LLMINT8_ERR_CUDA;
   cudaStream_t st = as_stream(stream);
-  const int64_t units = p.plan.whole + (int64_t)p.plan.rest * p.plan.parts;
-  const int pairs = (int)std::min<int64_t>(units, dev->max_pairs);
-  if (launch_pairs(igrad::k_input_grad, dim3(2 * pairs), dim3(igrad::NUM_THREADS),
-                   igrad::SMEM_BYTES, st, false, tmA, tmW, tmOut, p) != cudaSuccess)
-    return LLMINT8_ERR_CUDA;
-  if (p.plan.parts > 1 &&
+  const int64_t units = plan.whole + (int64_t)plan.rest * plan.parts;
+  const unsigned ctas = 2 * (unsigned)std::min<int64_t>(units, dev->max_pairs);
+  const cudaError_t e =
+      plan.mt == 1 ? launch_pairs(igrad::k_input_grad<1>, dim3(ctas), dim3(igrad::NUM_THREADS),
+                                  igrad::Smem<1>::BYTES, st, false, tmA, tmW, p)
+                   : launch_pairs(igrad::k_input_grad<2>, dim3(ctas), dim3(igrad::NUM_THREADS),
+                                  igrad::Smem<2>::BYTES, st, false, tmA, tmW, p);
+  if (e != cudaSuccess) return LLMINT8_ERR_CUDA;
+  if (plan.parts > 1 &&
       launch(igrad::k_input_grad_sum,
-             dim3(blocks_for((int64_t)p.plan.rest * 2 * igrad::BM * (igrad::BN / 8),
+             dim3(blocks_for((int64_t)plan.rest * plan.mt * 2 * igrad::BM * (igrad::BN / 8),
                              igrad::SUM_THREADS)),
-             dim3(igrad::SUM_THREADS), 0, st, true, p, as_half(dX_dev)) != cudaSuccess)
+             dim3(igrad::SUM_THREADS), 0, st, true, p) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   return last_launch();
 }

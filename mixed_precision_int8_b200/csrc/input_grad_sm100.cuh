@@ -47,16 +47,13 @@
 namespace llmint8 {
 namespace igrad {
 
-constexpr int BM = 128;   // rows per CTA (256 per pair)
+constexpr int BM = 128;   // rows per CTA and MMA (256 per pair)
 constexpr int BN = 256;   // columns of h per pair
 constexpr int BNH = 128;  // columns whose weight this CTA converts
 constexpr int BK = 64;    // reduction indices per stage
 constexpr int UMMA_K = 16;
-constexpr int STAGES = 5;
-constexpr int RAW_STAGES = 5;  // stages of int8 codes in flight
-constexpr int NUM_ACC = 2;
-constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t A_STAGE_BYTES = BM * BK * 2;
+constexpr uint32_t TMEM_COLS = 512;  // two accumulators
+constexpr uint32_t A_TILE_BYTES = BM * BK * 2;
 constexpr uint32_t B_STAGE_BYTES = BNH * BK * 2;
 constexpr uint32_t B_BLOCK_BYTES = 64 * BK * 2;  // 64 columns x 64 reduction rows
 constexpr int EPI_WARP0 = 4, EPI_THREADS = 128;
@@ -64,25 +61,35 @@ constexpr int CVT_WARP0 = 8, CVT_WARPS = 8, CVT_THREADS = 32 * CVT_WARPS;
 constexpr int CVT_GROUPS = 2;
 constexpr int NUM_THREADS = 32 * (CVT_WARP0 + CVT_GROUPS * CVT_WARPS);
 constexpr uint32_t FULL_ARRIVALS = 1 + 2 * CVT_WARPS;
-constexpr uint32_t OUT_STAGE_BYTES = 32 * 32 * 2;  // per epilogue warp
-constexpr uint32_t RAW_BYTES = BNH * BK;                 // codes of a stage
-constexpr uint32_t RAW_STAGE_BYTES = RAW_BYTES + 1024;   // + BK column scales
-constexpr uint32_t RAW_OFF = STAGES * (A_STAGE_BYTES + B_STAGE_BYTES);
-constexpr uint32_t OUT_OFF = RAW_OFF + RAW_STAGES * RAW_STAGE_BYTES;
-constexpr uint32_t BAR_OFF = OUT_OFF + 4 * OUT_STAGE_BYTES;
-constexpr size_t SMEM_BYTES = 1024 + BAR_OFF + 256;
+constexpr uint32_t RAW_BYTES = BNH * BK;                    // codes of a stage
+constexpr uint32_t RAW_STAGE_BYTES = RAW_BYTES + 4 * BK;    // + its column scales
 constexpr int MAX_PAIRS = 74;
-constexpr int MAX_PARTS = 2 * MAX_PAIRS;  // fp32 tiles the workspace holds
-constexpr size_t PART_ELEMS = 2 * BM * BN;
+constexpr int MAX_PARTS = 2 * MAX_PAIRS;  // units that leave fp32 tiles
+constexpr size_t PART_ELEMS = 2 * BM * BN;  // of each 256 rows of such a unit
 
-static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
-static_assert(RAW_STAGES >= STAGES, "see the converters' waits");
-static_assert((2 * STAGES + 2 * RAW_STAGES + 2 * NUM_ACC + 1) * 8 + 8 <= 256, "barrier block size");
+// Shared memory by rows per unit (MT times 256): the stages of dY and of the
+// converted weight, the codes, barriers.
+template <int MT>
+struct Smem {
+  static constexpr int STAGES = MT == 1 ? 5 : 4;
+  static constexpr int RAW_STAGES = STAGES;  // stages of int8 codes in flight
+  static constexpr uint32_t A_STAGE = MT * A_TILE_BYTES;
+  static constexpr uint32_t B_OFF = STAGES * A_STAGE;
+  static constexpr uint32_t RAW_OFF = B_OFF + STAGES * B_STAGE_BYTES;
+  static constexpr uint32_t BAR_OFF = RAW_OFF + RAW_STAGES * RAW_STAGE_BYTES;
+  static constexpr size_t BYTES = 1024 + BAR_OFF + 256;
+};
+
+static_assert(Smem<1>::BYTES <= 232448 && Smem<2>::BYTES <= 232448, "shared memory per CTA");
+static_assert(Smem<1>::RAW_STAGES >= Smem<1>::STAGES && Smem<2>::RAW_STAGES >= Smem<2>::STAGES,
+              "see the converters' waits");
+static_assert((4 * Smem<1>::STAGES + 5) * 8 + 8 <= 256, "barrier block size");
 
 // How the tiles are shared out: the first `whole` ones are computed whole,
 // each of the other `rest` in `parts` parts along the reduction.
 struct Plan {
-  int32_t num_m, num_n, num_k;  // tiles of 256 rows, of 256 columns, stages
+  int32_t mt;                   // 256-row blocks of a tile: 1 or 2
+  int32_t num_m, num_n, num_k;  // tiles of mt * 256 rows, of 256 columns, stages
   int32_t whole, rest, parts;
 };
 
@@ -92,7 +99,8 @@ struct Params {
   const int8_t *wq;   // [o][h]
   const float *aw;    // [o]
   const __half *base; // [s][h] or null
-  float *part;        // [rest * parts][256][256]
+  __half *out;        // [s][h]
+  float *part;        // [rest * parts][mt * 256][256]
   int32_t *status;
   uint64_t timeout_ns;
 };
@@ -101,9 +109,11 @@ struct Params {
 struct Unit {
   int32_t m, n, k0, k1;
   int32_t slot;  // fp32 tile it leaves, or -1 for a whole tile
+  int32_t blocks;  // its 256-row blocks that have rows
 };
 
-__device__ __forceinline__ bool unit_at(const Plan &pl, int32_t idx, Unit &u) {
+__device__ __forceinline__ bool unit_at(const Params &p, int32_t idx, Unit &u) {
+  const Plan &pl = p.plan;
   int32_t tile;
   if (idx < pl.whole) {
     tile = idx;
@@ -121,6 +131,7 @@ __device__ __forceinline__ bool unit_at(const Plan &pl, int32_t idx, Unit &u) {
   }
   u.m = tile % pl.num_m;
   u.n = tile / pl.num_m;
+  u.blocks = min(pl.mt, (p.s - u.m * pl.mt * 2 * BM + 2 * BM - 1) / (2 * BM));
   return true;
 }
 
@@ -161,27 +172,28 @@ __device__ __forceinline__ uint2 codes_to_half(uint32_t w, const Factor &f) {
                     scale_pair(prmt(x, 0x64646464u, 0x4342), f));
 }
 
+template <int MT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     k_input_grad(const __grid_constant__ CUtensorMap tmA,
-                 const __grid_constant__ CUtensorMap tmW,
-                 const __grid_constant__ CUtensorMap tmOut, const Params p) {
+                 const __grid_constant__ CUtensorMap tmW, const Params p) {
+  using L = Smem<MT>;
+  constexpr int STAGES = L::STAGES, RAW_STAGES = L::RAW_STAGES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
   uint8_t *base = smem_raw + pad;
   const uint32_t sA = smem_u32(base);
-  const uint32_t sB = sA + STAGES * A_STAGE_BYTES;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(base + BAR_OFF);
+  const uint32_t sB = sA + L::B_OFF;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(base + L::BAR_OFF);
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int st) { return bar0 + 8u * st; };
   auto empty_bar = [&](int st) { return bar0 + 8u * (STAGES + st); };
-  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
-  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + NUM_ACC + a); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NUM_ACC);
-  auto raw_full_bar = [&](int st) { return drain_bar + 8u * (1 + st); };
-  auto raw_empty_bar = [&](int st) { return drain_bar + 8u * (1 + RAW_STAGES + st); };
-  uint32_t *tmem_holder =
-      reinterpret_cast<uint32_t *>(bars + 2 * STAGES + 2 * RAW_STAGES + 2 * NUM_ACC + 1);
+  auto raw_full_bar = [&](int st) { return bar0 + 8u * (2 * STAGES + st); };
+  auto raw_empty_bar = [&](int st) { return bar0 + 8u * (2 * STAGES + RAW_STAGES + st); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 * RAW_STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 * RAW_STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * RAW_STAGES + 4);
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 2 * STAGES + 2 * RAW_STAGES + 5);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -195,7 +207,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(raw_full_bar(i), 1);
       mbar_init(raw_empty_bar(i), CVT_WARPS);
     }
-    for (int a = 0; a < NUM_ACC; ++a) {
+    for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
       mbar_init(tempty_bar(a), 2 * EPI_THREADS);
     }
@@ -204,7 +216,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmOut);
   }
   if (warp == 2) {
     tmem_alloc_pair(smem_u32(tmem_holder), TMEM_COLS);
@@ -217,25 +228,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem_base = *tmem_holder;
   grid_dependency_wait();
 
+  // accumulator of block b of the pair's it-th unit: with one block per unit
+  // the two alternate between units, with two each block has its own
+  auto acc_of = [](int32_t it, int b) { return MT == 1 ? (it & 1) : b; };
+  auto acc_use = [](int32_t it) { return (uint32_t)(MT == 1 ? it >> 1 : it) & 1u; };
   const int32_t pair = (int32_t)blockIdx.x >> 1, npairs = (int32_t)gridDim.x >> 1;
   Unit u;
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------- TMA producer (dY)
-    uint32_t stage = 0, phase = 0, issued = 0, last_par = 0;
-    bool ok = true;
-    for (int32_t idx = pair; ok && unit_at(p.plan, idx, u); idx += npairs) {
-      const int32_t row = u.m * (2 * BM) + (int32_t)rank * BM;
+    uint32_t stage = 0, phase = 0;
+    bool ok = true, issued = false;
+    for (int32_t idx = pair; ok && unit_at(p, idx, u); idx += npairs) {
+      const int32_t row = u.m * (MT * 2 * BM) + (int32_t)rank * BM;
       for (int32_t kb = u.k0; kb < u.k1; ++kb) {
         if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.status,
                                LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns)) {
           ok = false;
           break;
         }
-        if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * A_STAGE_BYTES);
-        tma_load_2d_pair(sA + stage * A_STAGE_BYTES, &tmA, mapa_shared(full_bar(stage), 0),
-                         kb * BK, row);
-        issued |= 1u << stage;
-        last_par = (last_par & ~(1u << stage)) | (phase << stage);
+        if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), u.blocks * 2 * A_TILE_BYTES);
+        for (int b = 0; b < u.blocks; ++b)
+          tma_load_2d_pair(sA + stage * L::A_STAGE + b * A_TILE_BYTES, &tmA,
+                           mapa_shared(full_bar(stage), 0), kb * BK, row + b * 2 * BM);
+        issued = true;
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -255,30 +270,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t stage = 0, phase = 0;
     bool ok = true, any = false;
     int32_t it = 0;
-    for (int32_t idx = pair; ok && unit_at(p.plan, idx, u); idx += npairs, ++it) {
-      const uint32_t acc = it & 1, acc_par = (it >> 1) & 1;
-      if (!mbar_wait_bounded(tempty_bar(acc), acc_par ^ 1u, abort_flag, p.status,
-                                     LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + acc * BN;
-      for (int32_t kb = u.k0; kb < u.k1; ++kb) {
+    for (int32_t idx = pair; ok && unit_at(p, idx, u); idx += npairs, ++it) {
+      for (int32_t kb = u.k0; ok && kb < u.k1; ++kb) {
         if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, p.status,
-                                       LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
+                               LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        const uint64_t a_desc = smem_desc_kmajor_sw128(sA + stage * A_STAGE_BYTES);
         const uint64_t b_desc = smem_desc_mn_sw128(sB + stage * B_STAGE_BYTES, B_BLOCK_BYTES);
+        for (int b = 0; b < u.blocks; ++b) {
+          const int acc = acc_of(it, b);
+          if (kb == u.k0 &&
+              !mbar_wait_bounded(tempty_bar(acc), acc_use(it) ^ 1u, abort_flag, p.status,
+                                 LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t a_desc =
+              smem_desc_kmajor_sw128(sA + stage * L::A_STAGE + b * A_TILE_BYTES);
 #pragma unroll
-        for (int k = 0; k < BK / UMMA_K; ++k)
-          mma_f16_pair(d_tmem, a_desc + (uint64_t)((k * UMMA_K * 2) >> 4),
-                       b_desc + (uint64_t)((k * UMMA_K * 128) >> 4), idesc,
-                       (kb > u.k0 || k > 0) ? 1u : 0u);
-        any = true;
+          for (int k = 0; k < BK / UMMA_K; ++k)
+            mma_f16_pair(tmem_base + acc * BN, a_desc + (uint64_t)((k * UMMA_K * 2) >> 4),
+                         b_desc + (uint64_t)((k * UMMA_K * 128) >> 4), idesc,
+                         (kb > u.k0 || k > 0) ? 1u : 0u);
+          any = true;
+        }
+        if (!ok) break;
         mma_commit_pair(mapa_shared(empty_bar(stage), 0));
         mma_commit_pair(mapa_shared(empty_bar(stage), 1));
         if (++stage == STAGES) {
@@ -287,8 +305,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       if (!ok) break;
-      mma_commit_pair(mapa_shared(tfull_bar(acc), 0));
-      mma_commit_pair(mapa_shared(tfull_bar(acc), 1));
+      // (a block without rows passes its accumulator on unused)
+      for (int b = 0; b < MT; ++b) {
+        if (b >= u.blocks &&
+            !mbar_wait_bounded(tempty_bar(acc_of(it, b)), acc_use(it) ^ 1u, abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        mma_commit_pair(mapa_shared(tfull_bar(acc_of(it, b)), 0));
+        mma_commit_pair(mapa_shared(tfull_bar(acc_of(it, b)), 1));
+      }
     }
     if (!ok && any) {
       volatile int never = 0;
@@ -299,7 +326,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ------------------------- TMA producer of the codes and their scales
     uint32_t stage = 0, phase = 0, issued = 0, last_par = 0;
     bool ok = true;
-    for (int32_t idx = pair; ok && unit_at(p.plan, idx, u); idx += npairs) {
+    for (int32_t idx = pair; ok && unit_at(p, idx, u); idx += npairs) {
       const int32_t col = u.n * BN + (int32_t)rank * BNH;
       for (int32_t kb = u.k0; kb < u.k1; ++kb) {
         if (!mbar_wait_bounded(raw_empty_bar(stage), phase ^ 1u, abort_flag, p.status,
@@ -307,7 +334,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ok = false;
           break;
         }
-        const uint32_t dst = smem_u32(base) + RAW_OFF + stage * RAW_STAGE_BYTES;
+        const uint32_t dst = smem_u32(base) + L::RAW_OFF + stage * RAW_STAGE_BYTES;
         const uint32_t scale_bytes = 4u * (uint32_t)min(BK, p.o - kb * BK);  // o % 16 == 0
         mbar_arrive_expect_tx(raw_full_bar(stage), RAW_BYTES + scale_bytes);
         tma_load_2d(dst, &tmW, raw_full_bar(stage), col, kb * BK);
@@ -330,67 +357,62 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else if (warp >= EPI_WARP0 && warp < CVT_WARP0) {
     // --------------------------------------------------------- epilogue
     const int ew = warp & 3;
-    uint8_t *sOut = base + OUT_OFF + ew * OUT_STAGE_BYTES;  // [32][64 B], 64-byte swizzle
-    const uint32_t sOut_addr = smem_u32(sOut);
     int32_t it = 0;
-    for (int32_t idx = pair; unit_at(p.plan, idx, u); idx += npairs, ++it) {
-      const uint32_t acc = it & 1, acc_par = (it >> 1) & 1;
-      const bool ready = mbar_wait_bounded(tfull_bar(acc), acc_par, abort_flag, p.status,
-                                           LLMINT8_DEV_TIMEOUT_EPILOGUE, p.timeout_ns);
-      if (!__all_sync(0xffffffffu, ready)) break;
-      tc_fence_after();
-      const uint32_t t_row = tmem_base + ((uint32_t)(ew * 32) << 16) + acc * BN;
-      const int32_t row0 = u.m * (2 * BM) + (int32_t)rank * BM + ew * 32;
-      const int32_t row = row0 + lane;
-      for (int c = 0; c < BN / 32; ++c) {
-        const int32_t j0 = u.n * BN + c * 32;
-        uint32_t v[32];
-        __syncwarp();
-        tmem_ld_32x32b_x32(t_row + c * 32, v);
-        if (lane == 0) bulk_wait_group_read0();
-        tmem_ld_wait();
-        __syncwarp();
-        if (c == BN / 32 - 1) {
-          tc_fence_before();
-          mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
-        }
-        if (u.slot >= 0) {
-          if (row < p.s && j0 < p.h) {
-            float4 *dst = reinterpret_cast<float4 *>(
-                p.part + (size_t)u.slot * PART_ELEMS +
-                (size_t)((int)rank * BM + ew * 32 + lane) * BN + c * 32);
+    bool ok = true;
+    for (int32_t idx = pair; ok && unit_at(p, idx, u); idx += npairs, ++it) {
+      for (int b = 0; b < MT; ++b) {
+        const int acc = acc_of(it, b);
+        ok = mbar_wait_bounded(tfull_bar(acc), acc_use(it), abort_flag, p.status,
+                               LLMINT8_DEV_TIMEOUT_EPILOGUE, p.timeout_ns);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        const uint32_t t_row = tmem_base + ((uint32_t)(ew * 32) << 16) + acc * BN;
+        const int in_block = (int)rank * BM + ew * 32 + lane;
+        const int32_t row = (u.m * MT + b) * (2 * BM) + in_block;
+        if (b < u.blocks) {
+          for (int c = 0; c < BN / 32; ++c) {
+            const int32_t j0 = u.n * BN + c * 32;
+            uint32_t v[32];
+            __syncwarp();
+            tmem_ld_32x32b_x32(t_row + c * 32, v);
+            tmem_ld_wait();
+            if (row >= p.s) continue;
+            if (u.slot >= 0) {
+              if (j0 >= p.h) continue;
+              float4 *dst = reinterpret_cast<float4 *>(
+                  p.part + ((size_t)u.slot * MT + b) * PART_ELEMS + (size_t)in_block * BN +
+                  c * 32);
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
-                                   __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+              for (int q = 0; q < 8; ++q)
+                dst[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                     __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+              continue;
+            }
+#pragma unroll
+            for (int q8 = 0; q8 < 4; ++q8) {
+              // h is a multiple of 16: 8 columns are all inside or all outside
+              const int32_t j = j0 + 8 * q8;
+              if (j >= p.h) continue;
+              float f[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * q8 + e]);
+              if (p.base) {
+                Vec8<__half> bv;
+                bv.load(p.base + (int64_t)row * p.h + j);
+                float bf[8];
+                bv.get(bf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] += bf[e];
+              }
+              store8(p.out + (int64_t)row * p.h + j, f);
+            }
           }
-          continue;
         }
-#pragma unroll
-        for (int q8 = 0; q8 < 4; ++q8) {
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * q8 + e]);
-          // h is a multiple of 16: 8 columns are all inside or all outside
-          if (p.base && row < p.s && j0 + 8 * q8 < p.h) {
-            Vec8<__half> b;
-            b.load(p.base + (int64_t)row * p.h + j0 + 8 * q8);
-            float bf[8];
-            b.get(bf);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] += bf[e];
-          }
-          store8(reinterpret_cast<__half *>(sOut + lane * 64 + ((q8 ^ ((lane >> 1) & 3)) * 16)), f);
-        }
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && j0 < p.h && row0 < p.s) {
-          tma_store_2d(&tmOut, sOut_addr, j0, row0);
-          bulk_commit_group();
-        }
+        tc_fence_before();
+        mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
       }
     }
-    if (lane == 0) bulk_wait_group0();
   } else if (warp >= CVT_WARP0) {
     // ------------------------------------------------------- converters
     // group g takes the pair's stages g, g + CVT_GROUPS, ... in order
@@ -401,7 +423,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t stage = group, phase = 0, rstage = group % RAW_STAGES, rphase = 0;
     bool ok = true;
     int32_t skip = group;  // stages of the sequence before this group's next one
-    for (int32_t idx = pair; ok && unit_at(p.plan, idx, u); idx += npairs) {
+    for (int32_t idx = pair; ok && unit_at(p, idx, u); idx += npairs) {
       int32_t kb = u.k0 + skip;
       for (; kb < u.k1; kb += CVT_GROUPS) {
         // the slot's turn first, then its codes: once the stage STAGES before
@@ -413,7 +435,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
              mbar_wait_bounded(raw_full_bar(rstage), rphase, abort_flag, p.status,
                                LLMINT8_DEV_TIMEOUT_PRODUCER, p.timeout_ns);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        const uint8_t *src = base + RAW_OFF + rstage * RAW_STAGE_BYTES;
+        const uint8_t *src = base + L::RAW_OFF + rstage * RAW_STAGE_BYTES;
         uint4 raw[2];
         float sc[2];
 #pragma unroll
@@ -423,7 +445,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const float aw = *reinterpret_cast<const float *>(src + RAW_BYTES + 4 * kr);
           sc[i] = kb * BK + kr < p.o ? aw : 0.0f;
         }
-        uint8_t *dst = base + STAGES * A_STAGE_BYTES + stage * B_STAGE_BYTES + blk * B_BLOCK_BYTES;
+        uint8_t *dst = base + L::B_OFF + stage * B_STAGE_BYTES + blk * B_BLOCK_BYTES;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int kr = r0 + 32 * i;
@@ -473,15 +495,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // The tiles computed in parts: out = fp16(base + the parts in order). A
 // thread holds 8 columns of one row of a tile.
 constexpr int SUM_THREADS = 256;
-__global__ void __launch_bounds__(SUM_THREADS)
-    k_input_grad_sum(const Params p, __half *__restrict__ out) {
+__global__ void __launch_bounds__(SUM_THREADS) k_input_grad_sum(const Params p) {
   grid_dependency_wait();
   const int32_t idx = blockIdx.x * SUM_THREADS + threadIdx.x;
-  const int32_t per_tile = 2 * BM * (BN / 8);
+  const int32_t per_tile = p.plan.mt * 2 * BM * (BN / 8);
   const int32_t t = idx / per_tile, e = idx % per_tile;
   if (t >= p.plan.rest) return;
   const int32_t tile = p.plan.whole + t;
-  const int32_t row = (tile % p.plan.num_m) * (2 * BM) + e / (BN / 8);
+  const int32_t row = (tile % p.plan.num_m) * (p.plan.mt * 2 * BM) + e / (BN / 8);
   const int32_t col = (tile / p.plan.num_m) * BN + (e % (BN / 8)) * 8;
   if (row >= p.s || col >= p.h) return;
   float f[8] = {};
@@ -492,7 +513,8 @@ __global__ void __launch_bounds__(SUM_THREADS)
   }
   float acc[8] = {};
   for (int32_t part = 0; part < p.plan.parts; ++part) {
-    const float *src = p.part + (size_t)(part * p.plan.rest + t) * PART_ELEMS + (size_t)e * 8;
+    const float *src = p.part +
+                       (size_t)(part * p.plan.rest + t) * p.plan.mt * PART_ELEMS + (size_t)e * 8;
     Vec8<float> v;
     v.load(src);
     float g[8];
@@ -502,7 +524,7 @@ __global__ void __launch_bounds__(SUM_THREADS)
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k) f[k] += acc[k];
-  store8(out + (int64_t)row * p.h + col, f);
+  store8(p.out + (int64_t)row * p.h + col, f);
 }
 
 }  // namespace igrad

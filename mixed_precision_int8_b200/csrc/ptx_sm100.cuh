@@ -470,6 +470,15 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // ----------------------------------------- CTA pairs (tcgen05 cta_group::2)
 // A cluster of two CTAs whose tensor-core ops run as one: the MMA issued by
 // rank 0 reads A rows from both CTAs' shared memory (128 each) and B

@@ -393,7 +393,8 @@ def test_another_stream_and_a_captured_graph_with_its_chain():
 # ---------------------------------------------- gradient of the projection's input
 
 BWD = [(1, 16, 16), (5, 528, 272), (16, 1040, 4096), (64, 512, 512), (131, 272, 1040),
-       (256, 784, 528), (257, 2064, 272), (600, 528, 2064), (129, 4096, 4096)]
+       (256, 784, 528), (257, 2064, 272), (600, 528, 2064), (129, 4096, 4096),
+       (1100, 4112, 528), (4353, 1296, 272)]
 
 
 def backward_case(s, h, o, seed=0):
