@@ -416,8 +416,8 @@ LLMINT8_API int64_t llmint8_decode_max_rows(void);
  * they leave. They follow the conventions at the top of this file (device
  * pointers, caller workspaces, asynchronous calls, validation before anything
  * is enqueued, 16-byte alignment of fp16/int8/fp32 tensors unless stated; h
- * and o obey the shape rules; s <= 2^31 - 1 and s == 0 gives the results of
- * an empty sum). Half-precision tensors are binary16 unless a type is given.
+ * and o obey the shape rules; s <= 2^31 - 1024, and s == 0 gives the results
+ * of an empty sum). Half-precision tensors are binary16 unless a type is given.
  * Their workspaces start with the same state block as llmint8_matmul's: clear
  * it once with llmint8_workspace_init, read it with
  * llmint8_read_device_status. A workspace may serve calls of any of them
@@ -540,8 +540,8 @@ typedef struct {
 /* A list of gradients laid out once for repeated calls. The caller sets
  * table_dev (device memory, 256-byte aligned) and table_bytes (at least
  * llmint8_grad_list_size(n)); llmint8_grad_list_init fills the rest and the
- * table. No two outputs, and no output and another entry's gradient, may
- * overlap. */
+ * table. Two outputs, or an output and another entry's gradient, must not
+ * overlap (LLMINT8_ERR_ARG). */
 typedef struct {
     void *table_dev;
     size_t table_bytes;
@@ -552,8 +552,10 @@ typedef struct {
 /* Bytes of the table of a list of n gradients; 0 for n < 0 or n > 2^24. */
 LLMINT8_API size_t llmint8_grad_list_size(int64_t n);
 
-/* grads_host (host memory) is read before the call returns. Asynchronous on
- * `stream`. */
+/* Lays the list out on the current device. grads_host (host memory) is read
+ * before the call returns. Asynchronous on `stream`; calls on the list follow
+ * it there, or are ordered after it. LLMINT8_ERR_TOO_LARGE: no host memory for
+ * the checks. */
 LLMINT8_API llmint8_status llmint8_grad_list_init(const llmint8_grad *grads_host, int64_t n,
                                                   llmint8_grad_list *list, void *stream);
 

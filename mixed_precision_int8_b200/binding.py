@@ -733,9 +733,10 @@ def llmint8_layernorm_backward(dY: torch.Tensor, X: torch.Tensor, gamma: torch.T
 
 
 class GradList:
-    """Gradients laid out once for llmint8_clip_grads: contiguous CUDA tensors
-    (fp16, bf16 or fp32) on one device, clipped in place, or into `outs`
-    (tensors of the same sizes and types). The tensors are kept, not copied."""
+    """Gradients laid out once, on their device's current stream, for repeated
+    llmint8_clip_grads: contiguous CUDA tensors (fp16, bf16 or fp32) on one
+    device, none listed twice, clipped in place, or into `outs` (tensors of the
+    same sizes and types). The tensors are kept, not copied."""
 
     def __init__(self, grads, outs=None, device=None):
         self.grads = list(grads)

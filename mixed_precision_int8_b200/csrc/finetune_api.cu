@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <vector>
 
 #include "llmint8.h"
 #include "host_common.cuh"
@@ -91,8 +92,11 @@ llmint8_status current_device(Device **out) {
   return LLMINT8_OK;
 }
 
+// Row indices, rounded up to whole tiles, stay 32-bit numbers.
+constexpr int64_t kMaxRows = (int64_t)INT32_MAX - 1023;
+
 llmint8_status check_rows(int64_t s) {
-  return s < 0 || s > (int64_t)INT32_MAX ? LLMINT8_ERR_SHAPE : LLMINT8_OK;
+  return s < 0 || s > kMaxRows ? LLMINT8_ERR_SHAPE : LLMINT8_OK;
 }
 
 llmint8_status check_width(int64_t h) {
@@ -469,6 +473,47 @@ cudaError_t ln_backward(const uint16_t *dy, const void *x, int64_t s, int64_t h,
                 static_cast<int32_t *>(ws), kTimeoutNs);
 }
 
+// -------------------------------------------------------------- clipping
+
+// As many blocks as fit the GPU at once, four per SM, and one at least.
+int64_t clip_blocks(int64_t chunks, int sm_count) {
+  return std::max<int64_t>(
+      1, std::min<int64_t>({chunks, 4 * (int64_t)sm_count, clip::MAX_BLOCKS}));
+}
+
+// LLMINT8_ERR_ARG when two outputs share memory, or an output and another
+// entry's gradient: blocks of one call would race on it.
+llmint8_status check_grad_overlaps(const llmint8_grad *grads, int64_t n) {
+  struct Span {
+    uintptr_t begin, end;
+    bool written;
+  };
+  try {
+    std::vector<Span> spans;
+    spans.reserve(2 * (size_t)n);
+    for (int64_t i = 0; i < n; ++i) {
+      const llmint8_grad &g = grads[i];
+      if (g.n == 0) continue;
+      const size_t bytes = (g.type == LLMINT8_F32 ? 4 : 2) * (size_t)g.n;
+      const uintptr_t in = reinterpret_cast<uintptr_t>(g.grad_dev);
+      const uintptr_t out = g.out_dev ? reinterpret_cast<uintptr_t>(g.out_dev) : in;
+      spans.push_back({out, out + bytes, true});
+      if (out != in) spans.push_back({in, in + bytes, false});
+    }
+    std::sort(spans.begin(), spans.end(),
+              [](const Span &a, const Span &b) { return a.begin < b.begin; });
+    uintptr_t read_end = 0, written_end = 0;
+    for (const Span &s : spans) {
+      if (s.begin < written_end || (s.written && s.begin < read_end)) return LLMINT8_ERR_ARG;
+      uintptr_t &end = s.written ? written_end : read_end;
+      end = std::max(end, s.end);
+    }
+  } catch (...) {  // no host memory for the check
+    return LLMINT8_ERR_TOO_LARGE;
+  }
+  return LLMINT8_OK;
+}
+
 bool ln_types_ok(int32_t x_type, int32_t p_type) {
   return (x_type == LLMINT8_F16 || x_type == LLMINT8_F32) &&
          (p_type == LLMINT8_F16 || p_type == LLMINT8_F32);
@@ -762,7 +807,7 @@ llmint8_status llmint8_layernorm_backward(const uint16_t *dy_dev, const void *x_
 
 size_t llmint8_grad_list_size(int64_t n) {
   if (n < 0 || n > (int64_t)1 << 24) return 0;
-  return align256(clip::kPartialBytes + sizeof(clip::Entry) * (size_t)n);
+  return align256(clip::kEntriesOffset + sizeof(clip::Entry) * (size_t)n);
 }
 
 llmint8_status llmint8_grad_list_init(const llmint8_grad *grads_host, int64_t n,
@@ -787,12 +832,36 @@ llmint8_status llmint8_grad_list_init(const llmint8_grad *grads_host, int64_t n,
       return LLMINT8_ERR_ARG;
     chunks += ceil_div(g.n, clip::chunk_elements(g.type));
   }
-  Device *dev = nullptr;
-  llmint8_status rc = current_device(&dev);
+  llmint8_status rc = check_grad_overlaps(grads_host, n);
   if (rc) return rc;
+  Device *dev = nullptr;
+  if ((rc = current_device(&dev))) return rc;
   cudaStream_t st = as_stream(stream);
   clip::Entry *table = reinterpret_cast<clip::Entry *>(static_cast<uint8_t *>(list->table_dev) +
-                                                       clip::kPartialBytes);
+                                                       clip::kEntriesOffset);
+  // the entry that holds each block's first chunk
+  const int64_t blocks = clip_blocks(chunks, dev->sm_count);
+  int32_t *starts = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(list->table_dev) +
+                                                clip::kStartsOffset);
+  int64_t entry = 0, before = 0;  // chunks before `entry`
+  for (int64_t b = 0; b < blocks; b += clip::INIT_STARTS) {
+    const int m = (int)std::min<int64_t>(clip::INIT_STARTS, blocks - b);
+    clip::StartBatch batch = {};
+    for (int k = 0; k < m; ++k) {
+      const int64_t c = clip::range_start(chunks, b + k, blocks);
+      while (entry + 1 < n) {
+        const llmint8_grad &g = grads_host[entry];
+        const int64_t mine = ceil_div(g.n, clip::chunk_elements(g.type));
+        if (before + mine > c) break;
+        before += mine;
+        ++entry;
+      }
+      batch.first[k] = (int32_t)entry;
+    }
+    if (launch(clip::k_starts_init, dim3(1), dim3(clip::INIT_STARTS), 0, st, false, starts + b,
+               batch, m) != cudaSuccess)
+      return LLMINT8_ERR_CUDA;
+  }
   int64_t at = 0;
   for (int64_t i = 0; i < n; i += clip::INIT_ENTRIES) {
     const int m = (int)std::min<int64_t>(clip::INIT_ENTRIES, n - i);
@@ -830,15 +899,15 @@ llmint8_status llmint8_clip_grads(const llmint8_grad_list *list, float max_norm,
   cudaStream_t st = as_stream(stream);
   double *partial = static_cast<double *>(list->table_dev);
   const clip::Entry *table = reinterpret_cast<const clip::Entry *>(
-      static_cast<const uint8_t *>(list->table_dev) + clip::kPartialBytes);
-  // as many blocks as fit the GPU at once, four per SM, and one at least
-  const int64_t blocks = std::max<int64_t>(
-      1, std::min<int64_t>({list->chunks, 4 * (int64_t)dev->sm_count, clip::MAX_BLOCKS}));
+      static_cast<const uint8_t *>(list->table_dev) + clip::kEntriesOffset);
+  const int32_t *starts = reinterpret_cast<const int32_t *>(
+      static_cast<const uint8_t *>(list->table_dev) + clip::kStartsOffset);
+  const int64_t blocks = clip_blocks(list->chunks, dev->sm_count);
   if (launch(clip::k_square_sums, dim3((unsigned)blocks), dim3(clip::THREADS), 0, st, false, table,
-             list->n, list->chunks, partial) != cudaSuccess)
+             list->n, list->chunks, starts, partial) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   if (launch(clip::k_clip_scale, dim3((unsigned)blocks), dim3(clip::THREADS), 0, st, true, table,
-             list->n, list->chunks, (const double *)partial, (int32_t)blocks, max_norm,
+             list->n, list->chunks, starts, (const double *)partial, (int32_t)blocks, max_norm,
              norm_dev) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   return last_launch();

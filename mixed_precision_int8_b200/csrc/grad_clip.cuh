@@ -5,9 +5,10 @@
 //
 // Bound: bytes. The list of tensors is laid out once, on the device, as a
 // table of entries with the running number of chunks (CHUNK_BYTES) before
-// each. A launch cuts the chunks of all tensors into equal contiguous ranges,
-// one per block, so thousands of small tensors and a few large ones load the
-// GPU alike. The norm kernel leaves one fp64 partial sum per block; the
+// each. The chunks of all tensors are cut into equal contiguous ranges, one per
+// block, so thousands of small tensors and a few large ones load the GPU
+// alike; the table also holds the entry in which each range starts (a search
+// for it in the kernel took 4 us of 256 entries). The norm kernel leaves one fp64 partial sum per block; the
 // scaling kernel's blocks each add those partial sums in the same order, so
 // the result does not depend on timing, and take their ranges from the end
 // of the list, where the norm kernel's reads are still in L2.
@@ -31,6 +32,7 @@ constexpr int THREADS = 512;
 constexpr int CHUNK_BYTES = 16384;  // two vectors of 16 bytes per thread
 constexpr int MAX_BLOCKS = 1024;   // partial sums a list holds
 constexpr int INIT_ENTRIES = 48;   // entries one launch of k_list_init carries
+constexpr int INIT_STARTS = 512;   // range starts one launch of k_starts_init carries
 
 struct Entry {
   const void *grad;
@@ -41,8 +43,14 @@ struct Entry {
   int32_t pad;
 };
 
-// The table: MAX_BLOCKS partial sums, then the entries.
-constexpr size_t kPartialBytes = MAX_BLOCKS * sizeof(double);
+// The table: MAX_BLOCKS partial sums, the blocks' first entries, the entries.
+constexpr size_t kStartsOffset = MAX_BLOCKS * sizeof(double);
+constexpr size_t kEntriesOffset = kStartsOffset + MAX_BLOCKS * sizeof(int32_t);
+
+// Chunks [first, last) of block b of `blocks`.
+__host__ __device__ inline int64_t range_start(int64_t chunks, int64_t b, int64_t blocks) {
+  return chunks * b / blocks;
+}
 
 struct InitBatch {
   Entry e[INIT_ENTRIES];
@@ -53,16 +61,14 @@ __global__ void k_list_init(Entry *table, const __grid_constant__ InitBatch batc
   if (i < n) table[i] = batch.e[i];
 }
 
-// The entry that holds chunk c: the last one with chunk0 <= c and n > 0
-// (entries without elements share their successor's chunk0).
-__device__ __forceinline__ int64_t find_entry(const Entry *table, int64_t n, int64_t c) {
-  int64_t lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) >> 1;
-    if (table[mid].chunk0 <= c) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
+struct StartBatch {
+  int32_t first[INIT_STARTS];
+};
+
+__global__ void k_starts_init(int32_t *starts, const __grid_constant__ StartBatch batch,
+                              int32_t n) {
+  const int i = threadIdx.x;
+  if (i < n) starts[i] = batch.first[i];
 }
 
 // Elements of a chunk of a type.
@@ -174,12 +180,13 @@ __device__ __forceinline__ void chunk_scale(const T *g, T *out, int m, float coe
 
 __global__ void __launch_bounds__(THREADS)
     k_square_sums(const Entry *__restrict__ table, int64_t n, int64_t chunks,
-                  double *__restrict__ partial) {
+                  const int32_t *__restrict__ starts, double *__restrict__ partial) {
   __shared__ double red[32];
   grid_dependency_trigger();
-  const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
+  const int64_t c0 = range_start(chunks, blockIdx.x, gridDim.x);
+  const int64_t c1 = range_start(chunks, blockIdx.x + 1, gridDim.x);
   double acc = 0.0;
-  int64_t t = c0 < c1 ? find_entry(table, n, c0) : 0;
+  int64_t t = starts[blockIdx.x];
   for (int64_t c = c0; c < c1; ++c) {
     while (t + 1 < n && table[t + 1].chunk0 <= c) ++t;
     const Entry e = table[t];
@@ -204,8 +211,8 @@ __global__ void __launch_bounds__(THREADS)
 
 __global__ void __launch_bounds__(THREADS)
     k_clip_scale(const Entry *__restrict__ table, int64_t n, int64_t chunks,
-                 const double *__restrict__ partial, int32_t n_partial, float max_norm,
-                 float *__restrict__ norm_out) {
+                 const int32_t *__restrict__ starts, const double *__restrict__ partial,
+                 int32_t n_partial, float max_norm, float *__restrict__ norm_out) {
   __shared__ double red[32];
   __shared__ float s_coef;
   grid_dependency_wait();
@@ -226,12 +233,12 @@ __global__ void __launch_bounds__(THREADS)
   }
   __syncthreads();
   const float coef = s_coef;
+  // ranges from the end of the list, each in order
   const int64_t b = gridDim.x - 1 - blockIdx.x;
-  const int64_t c0 = chunks * b / gridDim.x, c1 = chunks * (b + 1) / gridDim.x;
-  if (c0 >= c1) return;
-  int64_t t = find_entry(table, n, c1 - 1);
-  for (int64_t c = c1 - 1; c >= c0; --c) {
-    while (t > 0 && table[t].chunk0 > c) --t;
+  const int64_t c0 = range_start(chunks, b, gridDim.x), c1 = range_start(chunks, b + 1, gridDim.x);
+  int64_t t = starts[b];
+  for (int64_t c = c0; c < c1; ++c) {
+    while (t + 1 < n && table[t + 1].chunk0 <= c) ++t;
     const Entry e = table[t];
     if (coef == 1.0f && e.out == e.grad) continue;  // nothing to change in place
     const int full = chunk_elements(e.type);

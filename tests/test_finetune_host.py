@@ -28,7 +28,7 @@ def test_workspace_sizes(lib):
     assert lib.llmint8_adapters_workspace_size(0, 256, 256, 1, 8) > 0
     assert (lib.llmint8_adapters_workspace_size(4096, 256, 256, 1, 64)
             > lib.llmint8_adapters_workspace_size(16, 256, 256, 1, 64))
-    for bad in ((-1, 256, 256, 1, 8), (2 ** 31, 256, 256, 1, 8), (4, 250, 256, 1, 8),
+    for bad in ((-1, 256, 256, 1, 8), (2 ** 31 - 1023, 256, 256, 1, 8), (4, 250, 256, 1, 8),
                 (4, 256, 8, 1, 8), (4, 256, 256, 0, 8), (4, 256, 256, 65536, 8),
                 (4, 256, 256, 1, 0), (4, 256, 256, 1, 12), (4, 256, 256, 1, 136)):
         assert lib.llmint8_adapters_workspace_size(*bad) == 0
@@ -62,7 +62,7 @@ def test_adapters_forward_refusals(lib):
         assert call(_adapters(**kw)) == -2
     for kw in (dict(a=ODD), dict(b=ODD), dict(scale=ODD), dict(rank=ODD)):
         assert call(_adapters(**kw)) == -3
-    assert call(s=-1) == -2 and call(s=2 ** 31) == -2
+    assert call(s=-1) == -2 and call(s=2 ** 31 - 1023) == -2
     for kw in ("X", "ids", "out", "ws"):
         assert call(**{kw: None}) == -1
     for kw in ("X", "ids", "base", "out", "v", "ws"):
@@ -160,6 +160,17 @@ def test_clip_refusals(lib):
     assert one(type=3) == -7 and one(n=-1) == -2 and one(grad=None) == -1
     assert one(grad=ODD) == -3 and one(out=ODD) == -3
     assert one(out=ctypes.c_void_p((1 << 20) + 4)) == -7  # a shifted overlap
+    far = ctypes.c_void_p(1 << 24)
+
+    def two(a, b):
+        pair = (binding.llmint8_grad * 2)(a, b)
+        return init(pair, 2, ctypes.byref(lst), None)
+    G = binding.llmint8_grad
+    assert two(G(FAKE, None, 10, 1), G(FAKE, None, 10, 1)) == -7  # one tensor twice
+    assert two(G(FAKE, far, 10, 1), G(far, None, 10, 1)) == -7  # an output that is read
+    assert two(G(FAKE, far, 10, 1), G(FAKE, ctypes.c_void_p((1 << 24) + 36), 10, 1)) == -7
+    # read twice into outputs of their own: allowed (and then no usable device)
+    assert two(G(FAKE, far, 10, 1), G(FAKE, ctypes.c_void_p((1 << 24) + 40), 10, 1)) in (-5, -8)
     small = binding.llmint8_grad_list(FAKE, lib.llmint8_grad_list_size(1) - 1, 0, 0)
     assert init(ctypes.byref(item), 1, ctypes.byref(small), None) == -4
     off = binding.llmint8_grad_list(ODD, BIG, 0, 0)
