@@ -16,7 +16,7 @@
 #include <cstdint>
 #include <cuda_fp16.h>
 
-#include "ptx_sm100.cuh"
+#include "ptx_finetune_sm100.cuh"
 #include "rows_common.cuh"
 
 namespace llmint8 {

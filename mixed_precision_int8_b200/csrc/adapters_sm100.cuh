@@ -38,7 +38,7 @@
 #include <cuda_fp16.h>
 
 #include "adapters.cuh"
-#include "ptx_sm100.cuh"
+#include "ptx_finetune_sm100.cuh"
 #include "rows_common.cuh"
 
 namespace llmint8 {

@@ -13,7 +13,7 @@
 #include <vector>
 
 #include "llmint8.h"
-#include "host_common.cuh"
+#include "finetune_host.cuh"
 #include "adapters.cuh"
 #include "adapters_sm100.cuh"
 #include "grad_clip.cuh"

@@ -1,7 +1,7 @@
-// Host-side helpers shared by the library's source files: the shape and
-// alignment rules of include/llmint8.h, the state block at the front of every
-// workspace, TMA descriptor creation and kernel launches. Everything here has
-// internal linkage.
+// Host-side helpers of finetune_api.cu: the shape and alignment rules of
+// include/llmint8.h and the state block at the front of every workspace (as in
+// llmint8_api.cu), TMA descriptor creation and kernel launches. Everything here
+// has internal linkage.
 #pragma once
 
 #include <cuda.h>
@@ -40,9 +40,9 @@ EncodeTiledFn encode_fn() {
 }
 
 // 2-D int8 tensor [rows][inner] with row stride `inner` bytes, box
-// [box_rows][box_inner] landing in shared memory with the given swizzle.
-bool make_tmap_u8(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t rows,
-                  uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+// [box_rows][box_inner] landing in shared memory row by row.
+bool make_tmap_i8_plain(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t rows,
+                        uint32_t box_inner, uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {inner, rows};
@@ -50,26 +50,14 @@ bool make_tmap_u8(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t ro
   cuuint32_t box[2] = {box_inner, box_rows};
   cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// With the 128-byte swizzle (operands of int8 MMAs), or as the box lies.
-bool make_tmap_i8(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t rows,
-                  uint32_t box_inner, uint32_t box_rows) {
-  return make_tmap_u8(map, ptr, inner, rows, box_inner, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-[[maybe_unused]] bool make_tmap_i8_plain(CUtensorMap *map, const void *ptr, uint64_t inner,
-                                         uint64_t rows, uint32_t box_inner, uint32_t box_rows) {
-  return make_tmap_u8(map, ptr, inner, rows, box_inner, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE);
-}
-
-// 2-D fp16 tensor [rows][inner] (row stride 2*inner bytes) for TMA stores of
-// [box_rows][box_inner] blocks staged with the 128-byte swizzle.
+// 2-D fp16 tensor [rows][inner] (row stride 2*inner bytes) in boxes of
+// [box_rows][64] (128 bytes a row, 128-byte swizzle).
 bool make_tmap_f16(CUtensorMap *map, void *ptr, uint64_t inner, uint64_t rows,
                    uint32_t box_inner, uint32_t box_rows) {
-  const CUtensorMapSwizzle swz = box_inner * 2 == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {inner, rows};
@@ -77,7 +65,7 @@ bool make_tmap_f16(CUtensorMap *map, void *ptr, uint64_t inner, uint64_t rows,
   cuuint32_t box[2] = {box_inner, box_rows};
   cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ptr, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -108,7 +96,8 @@ llmint8_status last_launch() {
 
 // Launch with programmatic stream serialization when `pdl`: the kernel may
 // be scheduled while its predecessor drains; it orders itself after the
-// predecessor with griddepcontrol.wait before touching memory.
+// predecessor with griddepcontrol.wait before it reads the predecessor's
+// results or writes anything.
 template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                    cudaStream_t st, bool pdl, Args &&...args) {

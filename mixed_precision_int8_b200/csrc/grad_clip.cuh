@@ -22,7 +22,7 @@
 
 #include <cstdint>
 
-#include "ptx_sm100.cuh"
+#include "ptx_finetune_sm100.cuh"
 #include "rows_common.cuh"
 
 namespace llmint8 {

@@ -14,7 +14,6 @@
 #include <vector>
 
 #include "llmint8.h"
-#include "host_common.cuh"
 #include "quant_kernels.cuh"
 #include "gemm_sm100.cuh"
 #include "gemm_pair_sm100.cuh"
@@ -24,7 +23,9 @@ namespace {
 
 using namespace llmint8;
 
+constexpr int64_t kMaxH = 133144;  // 127*127*h must fit int32
 constexpr int64_t kDecodeMaxRows = decode::MAX_ROWS;
+constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per individual wait
 // how long a GEMM CTA waits for the other CTAs' shares of the outlier rows of
 // W before it builds them all itself: far longer than the shares take when
 // every CTA is resident (a few microseconds), and shorter than building them
@@ -42,6 +43,7 @@ struct DeviceInfo {
   int max_pairs = 0;  // CTA pairs of the pair GEMM that fit at once (0: none)
   int64_t l2_bytes = 0;
 };
+constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mutex;
 
@@ -97,13 +99,73 @@ llmint8_status device_info(DeviceInfo **out) {
   return LLMINT8_OK;
 }
 
+// ----------------------------------------------------- TMA descriptors
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+// 2-D int8 tensor [rows][inner] with row stride `inner` bytes, box
+// [box_rows][box_inner] landing in shared memory with the 128-byte swizzle.
+bool make_tmap_i8(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t rows,
+                  uint32_t box_inner, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, rows};
+  cuuint64_t strides[1] = {inner};
+  cuuint32_t box[2] = {box_inner, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 2-D fp16 tensor [rows][inner] (row stride 2*inner bytes) for TMA stores of
+// [box_rows][box_inner] blocks staged with the 128-byte swizzle.
+bool make_tmap_f16(CUtensorMap *map, void *ptr, uint64_t inner, uint64_t rows,
+                   uint32_t box_inner, uint32_t box_rows) {
+  const CUtensorMapSwizzle swz = box_inner * 2 == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, rows};
+  cuuint64_t strides[1] = {2 * inner};
+  cuuint32_t box[2] = {box_inner, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ptr, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ------------------------------------------------------ workspace layout
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
 struct Layout {
   size_t status, acc, mask, wprefix, idx, ax, xq, xo, wo, tiles, cacc, end;
   size_t xstage, ostage, end_host;
 };
 
 int32_t mask_words(int64_t h) { return (int32_t)((h + 31) / 32); }
+
+// The state block at the front of a workspace, cleared by
+// llmint8_workspace_init and kept by the kernels between calls: the status
+// words, then the accumulation bitmask of the one-read activation pass
+// (sized for the largest h), which that pass leaves zero on exit.
+constexpr size_t kStateBytes = 256 + ((4 * (size_t)((kMaxH + 31) / 32) + 255) & ~size_t(255));
+static_assert(kStateBytes == LLMINT8_WORKSPACE_STATE_BYTES, "state block size");
 
 // Row stride of the wide outlier layout (more than 16 outlier columns, K-major
 // for the tensor cores, outlier_rows.cuh): the capacity rounded up to 64, or
@@ -149,6 +211,14 @@ float *tensor_scale_word(void *ws) { return reinterpret_cast<float *>(ws) + 5; }
 constexpr int kSelftestWord = 8;  // a status-block word no kernel sets
 
 // --------------------------------------------------------- validation
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+llmint8_status check_hw(int64_t h, int64_t o) {
+  if (h < 16 || h > kMaxH || (h % 16) != 0) return LLMINT8_ERR_SHAPE;
+  if (o < 16 || (o % 16) != 0 || o > (int64_t)INT32_MAX / 2) return LLMINT8_ERR_SHAPE;
+  return LLMINT8_OK;
+}
+
 llmint8_status check_alpha(float alpha) {
   if (std::isnan(alpha) || alpha < 0.0f) return LLMINT8_ERR_ARG;
   return LLMINT8_OK;
@@ -172,6 +242,52 @@ uint32_t threshold_bits(float alpha) {
     else lo = mid + 1;
   }
   return lo;
+}
+
+cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s); }
+
+llmint8_status last_launch() {
+  return cudaGetLastError() == cudaSuccess ? LLMINT8_OK : LLMINT8_ERR_CUDA;
+}
+
+// Launch with programmatic stream serialization when `pdl`: the kernel may
+// be scheduled while its predecessor drains; it orders itself after the
+// predecessor with griddepcontrol.wait before touching memory.
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                   cudaStream_t st, bool pdl, Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// The same for a kernel run by clusters of two CTAs along x.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pairs(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t st, bool pdl, Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 // Steps 1, 2 and 4 (activation side, plus the fp16 outlier rows of W when

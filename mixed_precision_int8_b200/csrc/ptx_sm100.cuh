@@ -51,19 +51,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// The same without ever suspending the thread.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Wait for the phase of parity `parity` of barrier `bar` to complete, for at
 // most `limit_ns` nanoseconds. Returns false (after setting *abort and the
 // status bit) on timeout, or as soon as another role has set *abort.
@@ -135,16 +122,6 @@ __device__ __forceinline__ void bulk_load_1d_hint(uint32_t dst, const void *src,
       : "memory");
 }
 
-// The same without a policy.
-__device__ __forceinline__ void bulk_load_1d(uint32_t dst, const void *src, uint32_t bytes,
-                                             uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map))
                : "memory");
@@ -202,11 +179,6 @@ __device__ __forceinline__ void bulk_commit_group() {
 // Wait until no committed bulk group is still reading shared memory.
 __device__ __forceinline__ void bulk_wait_group_read0() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-
-// The same, but for the last committed group.
-__device__ __forceinline__ void bulk_wait_group_read1() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 
 // Wait until every committed bulk group has completed.
@@ -383,16 +355,6 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&v)
       : "memory");
 }
 
-// 8 columns instead of 32.
-__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&v)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7])
-      : "r"(taddr)
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -412,71 +374,6 @@ __device__ __forceinline__ uint64_t smem_desc_kmajor_sw128(uint32_t saddr) {
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
-}
-
-// Shared-memory matrix descriptor for an MN-major operand tile (the reduction
-// index outside, the M or N index contiguous) in 128-byte-swizzled blocks of
-// 64 fp16 columns: each block's rows are 128 bytes, one per value of the
-// reduction index, and blocks follow each other block_bytes apart. Leading
-// byte offset: from one 64-column block to the next; stride byte offset: from
-// one group of 8 reduction rows to the next (1024). Other fields as above.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t block_bytes) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
-  d |= (uint64_t)(block_bytes >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
-// Shared-memory matrix descriptor for an operand tile of unswizzled core
-// matrices (8 rows of 16 bytes, contiguous). K-major: a core matrix is 8 rows
-// (M or N) of 8 reduction values; lead = bytes to the next one along K,
-// stride = along M / N. MN-major: 8 reduction values' rows of 8 M / N columns;
-// lead = bytes to the next one along K, stride = along M / N.
-__device__ __forceinline__ uint64_t smem_desc_core(uint32_t saddr, uint32_t lead,
-                                                   uint32_t stride) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
-  d |= (uint64_t)(lead >> 4) << 16;
-  d |= (uint64_t)(stride >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  return d;
-}
-
-// 16-byte asynchronous copy global -> shared; zeros when `valid` is false
-// (src is then not read).
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-
-// Wait until at most N committed groups are still under way.
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Reads shared memory of a CTA of the cluster (shared::cluster address).
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
 }
 
 // ----------------------------------------- CTA pairs (tcgen05 cta_group::2)
@@ -509,14 +406,6 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
-}
-
-// The same at the default scope: no wait for the thread's writes to reach the
-// cluster's point of coherence (a round trip to L2 under load). For signals
-// about shared memory of this CTA that only this SM's tensor core reads, after
-// fence.proxy.async has made the writes visible to it.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 // 2-D tiled copy into this CTA's shared memory whose bytes are counted on
@@ -589,13 +478,6 @@ __host__ __device__ constexpr uint32_t idesc_i8_s32(uint32_t M, uint32_t N) {
 // N >> 3 in bits 17-22, M >> 4 in bits 24-28.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
-// The same with the operands' majors chosen: bit 15 (A) and 16 (B) set for
-// MN-major.
-__host__ __device__ constexpr uint32_t idesc_f16_f32_mn(uint32_t M, uint32_t N, bool a_mn,
-                                                        bool b_mn) {
-  return idesc_f16_f32(M, N) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
 }
 
 }  // namespace llmint8
