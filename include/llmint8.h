@@ -454,8 +454,9 @@ LLMINT8_API size_t llmint8_adapters_workspace_size(int64_t s, int64_t h, int64_t
  * and mixtures of both in one call):
  *   v[i][t]   = X[i] . A[a][t]                      a = ids[i], t < rank[a]
  *   out[i][j] = fp16(base[i][j] + scale[a] * sum_t v[i][t] * B[a][t][j])
- * with fp32 sums. ids_dev is int32 [s] (4-byte aligned), in any order; a row
- * whose id is outside [0, n) uses no adapter: its out is its base, unchanged.
+ * with fp32 sums. ids_dev is int32 [s] (4-byte aligned), in any order (past 128
+ * rows a tile of 128 costs a pass per adapter in it: keep a request's rows
+ * together); a row whose id is outside [0, n) uses no adapter: its out is its base, unchanged.
  * base_dev (fp16 [s][o]) is llmint8_matmul's output; NULL stands for zeros.
  * out_dev (fp16 [s][o]) may be base_dev itself; else it must not overlap it,
  * nor X_dev (LLMINT8_ERR_ARG).

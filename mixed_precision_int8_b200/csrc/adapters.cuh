@@ -33,13 +33,17 @@ __device__ __forceinline__ int rank_of(const int32_t *rank, int a, int r) {
   return rank ? max(0, min(rank[a], r)) : r;
 }
 
-// ------------------------------------------------- a few rows (decode steps)
+// ----------------------------- up to a tile of rows (decode steps, short prompts)
 //
-// Each row reads its own adapter's factors once: the work is those bytes, so
-// it is spread over (row, slice of the features) blocks on CUDA cores, with
-// fp32 products and sums. k_rows_shrink leaves one partial sum of v per slice;
-// k_rows_expand, launched as its programmatic dependent, has its first factor
-// rows in registers before it waits for them.
+// Each row reads its own adapter's factors, so the work is spread over (row,
+// slice of the features) blocks on CUDA cores, with fp32 products and sums.
+// k_rows_shrink leaves one partial sum of v per slice; k_rows_expand, launched
+// as its programmatic dependent, has its first factor rows in registers before
+// it waits for them. Against the tensor-core kernels, which multiply a whole
+// tile of rows with every adapter in it (forward, 12288 -> 20480, rank 64):
+// 64 rows of 64 adapters 64 us instead of 832, 128 of 64 104 instead of 840;
+// rows of one adapter, which those kernels suit best, 35 instead of 31 at 64
+// rows and 55 instead of 33 at 128.
 
 constexpr int RS_SLICE = 512;       // features of a k_rows_shrink block
 constexpr int RS_THREADS = 256;
@@ -88,7 +92,8 @@ __global__ void __launch_bounds__(RS_THREADS)
   }
 }
 
-// out[i][8c..] = base + scale * sum_t v[i][t] * F[a][t][8c..]. Grid (slices, s).
+// out[i][8c..] = base + scale * sum_t v[i][t] * F[a][t][8c..]; v itself to
+// v_out (or null). out may be null: v alone. Grid (slices of out, s).
 __global__ void __launch_bounds__(RE_THREADS)
     k_rows_expand(const float *__restrict__ part, int32_t slices, int32_t s, int32_t o,
                   const __half *__restrict__ F, const int32_t *__restrict__ ids,
@@ -102,7 +107,7 @@ __global__ void __launch_bounds__(RE_THREADS)
   const int a = adapter_of(ids, row, n);
   const int rk = a >= 0 ? rank_of(rank, a, r) : 0;
   const __half *f = F + (int64_t)max(a, 0) * r * o + col;
-  const bool in = col < o;
+  const bool in = out != nullptr && col < o;
   Vec8<__half> ahead[RE_AHEAD], b;
 #pragma unroll
   for (int t = 0; t < RE_AHEAD; ++t) {
@@ -152,6 +157,79 @@ __global__ void __launch_bounds__(RE_THREADS)
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = fmaf(scale[a], acc[e], y[e]);
   store8(out + row * o + col, y);
+}
+
+// d[a][t][8c..] = scale[a] * sum of p[i][t] * Q[i][8c..] over the adapter's
+// rows, in order: RO_TERMS terms and eight features per thread. Grid (slices
+// of both jobs, n, ceil(r / RO_TERMS)); only the adapter's rows are read.
+constexpr int RO_THREADS = 128;
+constexpr int RO_SLICE = 8 * RO_THREADS;
+constexpr int RO_TERMS = 8;
+constexpr int RO_MAX_ROWS = 128;
+
+struct RowsOuterJob {
+  const float *p;   // [s][r]
+  const __half *q;  // [s][w]
+  float *d;         // [n][r][w]
+  int32_t w;
+};
+
+__global__ void __launch_bounds__(RO_THREADS)
+    k_rows_outer(const RowsOuterJob j0, const RowsOuterJob j1, int32_t slices0, int32_t s,
+                 const int32_t *__restrict__ ids, const float *__restrict__ scale,
+                 const int32_t *__restrict__ rank, int32_t n, int32_t r) {
+  __shared__ int32_t rows[RO_MAX_ROWS];
+  __shared__ float p[RO_MAX_ROWS][RO_TERMS];
+  __shared__ int32_t per_warp[RO_THREADS / 32];
+  const bool second = (int32_t)blockIdx.x >= slices0;
+  const RowsOuterJob &job = second ? j1 : j0;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int a = blockIdx.y, t0 = blockIdx.z * RO_TERMS;
+  const int col = ((int)blockIdx.x - (second ? slices0 : 0)) * RO_SLICE + tid * 8;
+  // the adapter's rows, in order
+  const bool mine = tid < s && ids[tid] == a;
+  const unsigned v = __ballot_sync(0xffffffffu, mine);
+  if (lane == 0) per_warp[warp] = __popc(v);
+  __syncthreads();
+  int at = __popc(v & ((1u << lane) - 1u)), count = 0;
+  for (int i = 0; i < RO_THREADS / 32; ++i) {
+    if (i < warp) at += per_warp[i];
+    count += per_warp[i];
+  }
+  if (mine) rows[at] = tid;
+  const int rk = rank_of(rank, a, r);
+  grid_dependency_wait();  // p is the preceding kernels'
+  __syncthreads();
+  for (int i = tid; i < count * RO_TERMS; i += RO_THREADS) {
+    const int t = t0 + i % RO_TERMS;
+    p[i / RO_TERMS][i % RO_TERMS] = t < rk ? job.p[(int64_t)rows[i / RO_TERMS] * r + t] : 0.0f;
+  }
+  __syncthreads();
+  if (col >= job.w) return;
+  float acc[RO_TERMS][8] = {};
+  if (t0 < rk) {
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      Vec8<__half> q;
+      q.load(job.q + (int64_t)rows[i] * job.w + col);
+      float x[8];
+      q.get(x);
+#pragma unroll
+      for (int t = 0; t < RO_TERMS; ++t)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[t][e] = fmaf(p[i][t], x[e], acc[t][e]);
+    }
+  }
+  const float f = scale[a];
+#pragma unroll
+  for (int t = 0; t < RO_TERMS; ++t) {
+    if (t0 + t >= r) break;
+    float y[8];
+    // (an unused term is 0 whatever its sum)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = t0 + t < rk ? f * acc[t][e] : 0.0f;
+    store8(job.d + ((int64_t)a * r + t0 + t) * job.w + col, y);
+  }
 }
 
 }  // namespace lora

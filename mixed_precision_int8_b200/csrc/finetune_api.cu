@@ -116,8 +116,18 @@ bool overlap(const void *p, size_t pn, const void *q, size_t qn) {
 
 // ------------------------------------------------------------- adapters
 
-// Rows up to which the forward pass runs the row kernels.
-constexpr int64_t kRowKernelMaxRows = 16;
+// The row kernels (adapters.cuh) take batches of at most one tile of rows, and
+// of 32 rows per adapter held: what the tensor-core kernels lose is a pass per
+// adapter in a tile, so the fewer there can be, the sooner they win (one
+// adapter, backward, 12288 -> 20480, rank 64: rows 38 against 54 us at 32 rows,
+// 58 against 54 at 64; sixteen: 107 against 447 at 128). Widths leave at most
+// kRowMaxSlices partial sums of a row.
+constexpr int64_t kRowMaxSlices = 256;
+
+bool use_row_kernels(int64_t s, const llmint8_adapters *ad) {
+  return s <= std::min<int64_t>(lora::RO_MAX_ROWS, 32 * (int64_t)ad->n) &&
+         std::max(ad->h, ad->o) <= kRowMaxSlices * lora::RS_SLICE;
+}
 
 struct AdapterLayout {
   size_t v, g, vmax, gmax, amax, part, info, vpack, gpack, end;
@@ -125,7 +135,7 @@ struct AdapterLayout {
 
 int64_t row_slices(int64_t h) { return (h + lora::RS_SLICE - 1) / lora::RS_SLICE; }
 
-AdapterLayout adapter_layout(int64_t s, int64_t h, int32_t n, int32_t r) {
+AdapterLayout adapter_layout(int64_t s, int64_t h, int64_t o, int32_t n, int32_t r) {
   AdapterLayout L;
   const size_t sr = 4 * (size_t)s * r, s1 = 4 * (size_t)s;
   const size_t blocks = (size_t)((s + lora::OU_KB - 1) / lora::OU_KB);
@@ -136,8 +146,9 @@ AdapterLayout adapter_layout(int64_t s, int64_t h, int32_t n, int32_t r) {
   L.gmax = align256(L.vmax + s1);
   L.amax = align256(L.gmax + s1);  // [2][n]: v's, g's
   L.part = align256(L.amax + 8 * (size_t)n);
-  L.info = align256(L.part +
-                    4 * (size_t)(row_slices(h) * std::min(s, kRowKernelMaxRows)) * r);
+  const int64_t slices = std::min(row_slices(std::max(h, o)), kRowMaxSlices);
+  L.info =
+      align256(L.part + 4 * (size_t)(slices * std::min<int64_t>(s, lora::RO_MAX_ROWS)) * r);
   L.vpack = align256(L.info + 4 * blocks);
   L.gpack = align256(L.vpack + packed);
   L.end = align256(L.gpack + packed);
@@ -165,6 +176,25 @@ const __half *as_half(const uint16_t *p) { return reinterpret_cast<const __half 
 __half *as_half(uint16_t *p) { return reinterpret_cast<__half *>(p); }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// v = X . F1^T over k features (kept in v_out, or null) and, unless out is
+// null, out = base + scale * v . F2 over w features, by the row kernels.
+llmint8_status enqueue_rows(const uint16_t *X, int64_t s, int64_t k, const uint16_t *F1, int64_t w,
+                            const uint16_t *F2, const llmint8_adapters *ad, const int32_t *ids,
+                            const uint16_t *base, uint16_t *out, float *v_out, float *part,
+                            cudaStream_t st) {
+  const int64_t slices = row_slices(k);
+  if (launch(lora::k_rows_shrink, dim3((unsigned)slices, (unsigned)s), dim3(lora::RS_THREADS), 0,
+             st, false, as_half(X), (int32_t)s, (int32_t)k, as_half(F1), ids, ad->rank_dev, ad->n,
+             ad->r, part) != cudaSuccess ||
+      launch(lora::k_rows_expand,
+             dim3(out ? (unsigned)ceil_div(w, lora::RE_SLICE) : 1u, (unsigned)s),
+             dim3(lora::RE_THREADS), 0, st, true, (const float *)part, (int32_t)slices, (int32_t)s,
+             (int32_t)w, as_half(F2), ids, ad->scale_dev, ad->rank_dev, ad->n, ad->r,
+             as_half(base), as_half(out), v_out) != cudaSuccess)
+    return LLMINT8_ERR_CUDA;
+  return LLMINT8_OK;
+}
 
 // The largest power of two up to `limit` CTAs per cluster that still leaves
 // each of `tiles` clusters an SM per CTA, or 1.
@@ -525,7 +555,7 @@ extern "C" {
 
 size_t llmint8_adapters_workspace_size(int64_t s, int64_t h, int64_t o, int32_t n, int32_t r) {
   if (check_adapter_sizes(s, h, o, n, r)) return 0;
-  return adapter_layout(s, h, n, r).end;
+  return adapter_layout(s, h, o, n, r).end;
 }
 
 llmint8_status llmint8_adapters_forward(const uint16_t *X_dev, int64_t s,
@@ -543,25 +573,16 @@ llmint8_status llmint8_adapters_forward(const uint16_t *X_dev, int64_t s,
   if (overlap(out_dev, out_bytes, X_dev, in_bytes) ||
       (base_dev != out_dev && overlap(out_dev, out_bytes, base_dev, out_bytes)))
     return LLMINT8_ERR_ARG;
-  const AdapterLayout L = adapter_layout(s, ad->h, ad->n, ad->r);
+  const AdapterLayout L = adapter_layout(s, ad->h, ad->o, ad->n, ad->r);
   if (ws_bytes < L.end) return LLMINT8_ERR_WORKSPACE;
   Device *dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   cudaStream_t st = as_stream(stream);
   uint8_t *wsb = static_cast<uint8_t *>(ws_dev);
-  if (s <= kRowKernelMaxRows) {
-    float *part = reinterpret_cast<float *>(wsb + L.part);
-    const int64_t slices = row_slices(ad->h);
-    if (launch(lora::k_rows_shrink, dim3((unsigned)slices, (unsigned)s), dim3(lora::RS_THREADS), 0,
-               st, false, as_half(X_dev), (int32_t)s, (int32_t)ad->h, as_half(ad->a_dev), ids_dev,
-               ad->rank_dev, ad->n, ad->r, part) != cudaSuccess ||
-        launch(lora::k_rows_expand,
-               dim3((unsigned)ceil_div(ad->o, lora::RE_SLICE), (unsigned)s),
-               dim3(lora::RE_THREADS), 0, st, true, (const float *)part, (int32_t)slices,
-               (int32_t)s, (int32_t)ad->o, as_half(ad->b_dev), ids_dev, ad->scale_dev,
-               ad->rank_dev, ad->n, ad->r, as_half(base_dev), as_half(out_dev),
-               v_dev) != cudaSuccess)
-      return LLMINT8_ERR_CUDA;
+  if (use_row_kernels(s, ad)) {
+    if ((rc = enqueue_rows(X_dev, s, ad->h, ad->a_dev, ad->o, ad->b_dev, ad, ids_dev, base_dev,
+                           out_dev, v_dev, reinterpret_cast<float *>(wsb + L.part), st)))
+      return rc;
     return last_launch();
   }
   float *v = v_dev ? v_dev : reinterpret_cast<float *>(wsb + L.v);
@@ -595,7 +616,7 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
   if (overlap(dX_dev, in_bytes, X_dev, in_bytes) || overlap(dX_dev, in_bytes, dY_dev, out_bytes) ||
       (base_dev != dX_dev && overlap(dX_dev, in_bytes, base_dev, in_bytes)))
     return LLMINT8_ERR_ARG;
-  const AdapterLayout L = adapter_layout(s, ad->h, ad->n, ad->r);
+  const AdapterLayout L = adapter_layout(s, ad->h, ad->o, ad->n, ad->r);
   if (s > 0 && ws_bytes < L.end) return LLMINT8_ERR_WORKSPACE;
   Device *dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
@@ -613,6 +634,32 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
   float *gmax = reinterpret_cast<float *>(wsb + L.gmax);
   uint32_t *v_amax = reinterpret_cast<uint32_t *>(wsb + L.amax), *g_amax = v_amax + ad->n;
   const bool need_g = dX_dev || dA_dev;
+  if (use_row_kernels(s, ad)) {
+    float *part = reinterpret_cast<float *>(wsb + L.part);
+    if (need_v && (rc = enqueue_rows(X_dev, s, ad->h, ad->a_dev, ad->o, ad->b_dev, ad, ids_dev,
+                                     nullptr, nullptr, v, part, st)))
+      return rc;
+    if (need_g && (rc = enqueue_rows(dY_dev, s, ad->o, ad->b_dev, ad->h, ad->a_dev, ad, ids_dev,
+                                     base_dev, dX_dev, g, part, st)))
+      return rc;
+    lora::RowsOuterJob jobs[2];
+    int n_jobs = 0;
+    if (dB_dev)
+      jobs[n_jobs++] = {v_dev ? v_dev : v, as_half(dY_dev), dB_dev, (int32_t)ad->o};
+    if (dA_dev) jobs[n_jobs++] = {g, as_half(X_dev), dA_dev, (int32_t)ad->h};
+    if (n_jobs > 0) {
+      const int64_t first = ceil_div(jobs[0].w, lora::RO_SLICE);
+      const int64_t second = n_jobs > 1 ? ceil_div(jobs[1].w, lora::RO_SLICE) : 0;
+      if (launch(lora::k_rows_outer,
+                 dim3((unsigned)(first + second), (unsigned)ad->n,
+                      (unsigned)ceil_div(ad->r, lora::RO_TERMS)),
+                 dim3(lora::RO_THREADS), 0, st, need_g || need_v, jobs[0], jobs[n_jobs - 1],
+                 (int32_t)first, (int32_t)s, ids_dev, ad->scale_dev, ad->rank_dev, ad->n,
+                 ad->r) != cudaSuccess)
+        return LLMINT8_ERR_CUDA;
+    }
+    return last_launch();
+  }
   const bool own_v = dB_dev && v_dev;  // v as the caller kept it: only its maxima
   const bool sums = dA_dev || dB_dev;
   int32_t *info = reinterpret_cast<int32_t *>(wsb + L.info);

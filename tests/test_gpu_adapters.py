@@ -114,7 +114,8 @@ def bits(t):
     return t.view(torch.int16)
 
 
-# sizes: one row, the row kernel's limits, tiles of 128 rows and the rows
+# sizes: one row, the row kernels' limits (32 rows per adapter held, 128 in
+# all), tiles of 128 rows and the rows
 # around their edges, widths that end inside a tile, ranks that are no
 # multiple of 16, more adapters in a tile than accumulators
 CASES = [
@@ -125,7 +126,9 @@ CASES = [
     (17, 1040, 2064, 3, 24, "mixed", "mixed"),
     (32, 272, 784, 40, 128, "mixed", "mixed"),
     (33, 272, 784, 40, 128, "mixed", "mixed"),
+    (33, 272, 784, 1, 128, "mixed", "mixed"),
     (64, 512, 528, 64, 8, "mixed", "full"),
+    (128, 528, 784, 40, 24, "mixed", "mixed"),
     (65, 528, 512, 2, 40, "requests", "full"),
     (128, 2064, 784, 2, 16, "requests_bare", "mixed"),
     (129, 784, 2064, 2, 16, "requests", "full"),
