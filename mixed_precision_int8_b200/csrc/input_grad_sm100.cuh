@@ -9,24 +9,26 @@
 // operand, so nothing is transposed; each int8 tile is turned into fp16 on
 // its way into shared memory.
 //
-// Bound: the fp16 tensor cores (2 s h o operations) at prefill sizes. A pair
-// of CTAs computes a 256 x 256 tile (tcgen05 cta_group::2), so that per stage
-// of 64 reduction indices a CTA stores and reads only its 128 x 64 half of
-// each operand: the converted weight costs shared memory no more than a
-// plain fp16 one would, and its global traffic is half. Two groups of eight
-// warps convert alternate stages: TMA brings the codes (and their column
-// scales) into a ring of their own, a lane takes 16 codes of it and writes 16
-// fp16 values through the 128-byte swizzle. The converters load nothing from
-// global memory themselves: the fence that makes their writes visible to the
-// tensor cores waits for all that a thread has in flight, and with register
-// loads running ahead it took as long as those (measured: 1170 us instead of
-// %%% at 4096 x 5120 x 20480).
+// Bound: the fp16 tensor cores (2 s h o operations) and, back to back, the
+// power cap at prefill sizes (4096 x 5120 x 20480: 679 us in a burst, 800 us
+// under the cap; 596 us in a burst with the conversion switched off). A pair of
+// CTAs computes a tile of MT x 256 rows by 256 columns (tcgen05
+// cta_group::2), so that per stage of 64 reduction indices a CTA stores and
+// reads only half of each operand: the converted weight costs shared memory no
+// more than a plain fp16 one would, and its global traffic is half. With MT = 2
+// (more than 256 rows) a converted tile serves two MMAs: half the conversions,
+// 772 -> 679 us. Two groups of eight warps convert alternate stages: TMA brings
+// the codes and their column scales into a ring of their own, a lane takes 16
+// codes of it and writes 16 fp16 values through the 128-byte swizzle, 11
+// instructions for four codes. Their signal to the issuing CTA is an arrival at
+// the default scope (mbar_arrive_remote): one with cluster-scope release waits
+// for a round trip to L2 in every stage (1238 us instead of 777 with MT = 1).
 //
 //   warp 0      TMA producer of dY
 //   warp 1      one thread of rank 0 issues the MMAs
 //   warp 2      allocates TMEM (two 256-column accumulators); TMA producer of
 //               the codes
-//   warps 4-7   epilogue: TMEM -> + base -> fp16 -> TMA store
+//   warps 4-7   epilogue: TMEM -> + base -> fp16
 //   warps 8-23  converters
 //
 // Tiles that do not fill a round of all pairs (the last ones, or all of a
