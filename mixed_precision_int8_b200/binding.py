@@ -699,8 +699,7 @@ def llmint8_layernorm_forward(X: torch.Tensor, gamma: torch.Tensor,
     with _Launch(dev, stream) as st:
         if out is None:
             out = torch.empty((s, h), dtype=torch.float16, device=dev)
-        mean = torch.empty((s,), dtype=torch.float32, device=dev)
-        rstd = torch.empty((s,), dtype=torch.float32, device=dev)
+        mean, rstd = torch.empty((2, s), dtype=torch.float32, device=dev).unbind(0)
         _check("llmint8_layernorm_forward", load_library().llmint8_layernorm_forward(
             *args, _tensor(out, "out", torch.float16, (s, h), dev), mean.data_ptr(),
             rstd.data_ptr(), st))
@@ -722,8 +721,7 @@ def llmint8_layernorm_backward(dY: torch.Tensor, X: torch.Tensor, gamma: torch.T
     with _Launch(dev, stream) as st:
         if dX is None:
             dX = torch.empty_like(X)
-        dgamma = torch.empty((h,), dtype=f32, device=dev)
-        dbeta = torch.empty((h,), dtype=f32, device=dev)
+        dgamma, dbeta = torch.empty((2, h), dtype=f32, device=dev).unbind(0)
         if workspace is None:
             workspace = LayerNormWorkspace(s, h, dev)
         _check("llmint8_layernorm_backward", load_library().llmint8_layernorm_backward(

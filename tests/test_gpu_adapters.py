@@ -307,6 +307,19 @@ def test_gradients_against_differences():
             t[where] -= 1
 
 
+def test_ranks_outside_their_slots_are_clamped():
+    for s in (9, 300):
+        c = Case(s, 272, 528, 3, 16, "mixed", "mixed", seed=6)
+        c.rank_list = [0, 16, 5]
+        c.ranks.copy_(torch.tensor([-7, 2 ** 31 - 1, 5]))
+        out, _, dX, dA, dB = c.reference()
+        same(L.llmint8_adapters_forward(c.X, c.ad, c.ids, base=c.base), out, torch.float16)
+        got = L.llmint8_adapters_backward(c.X, c.dY, c.ad, c.ids, base=c.dbase)
+        same(got[0], dX, torch.float16)
+        same(got[1], dA, torch.float32)
+        same(got[2], dB, torch.float32)
+
+
 def test_no_rows():
     c = Case(4, 272, 528, 2, 8, "mixed", "full")
     X0 = c.X[:0]
