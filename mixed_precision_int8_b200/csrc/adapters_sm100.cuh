@@ -1,11 +1,12 @@
 // The adapters' products on the tensor cores, for batches of more than a few
-// rows (formulas: adapters.cuh). Three kernels:
+// rows (formulas: adapters.cuh):
 //
 //   k_shrink   v = X . F^T over the features: 128 rows per cluster, the
 //              features cut over the cluster's CTAs, their partial sums added
 //              through distributed shared memory in rank order
-//   k_expand   out = base + scale * v . F: 128 rows x 64 features per step
-//   k_pack     g or v as the operand of the next kernel
+//   k_expand   out = base + scale * v . F: 128 rows x 64 features per step; in
+//              the backward pass further blocks do k_pack's work
+//   k_pack     g or v as the operand of k_outer
 //   k_outer    dF = scale * P^T . Q over the rows of one adapter: 256 features
 //              per cluster, the blocks of 64 rows cut over its CTAs
 //
@@ -453,6 +454,81 @@ __global__ void __launch_bounds__(256)
   if ((threadIdx.x & 31) == 0) atomicMax(amax + a, __float_as_uint(m));
 }
 
+// -------------------------------------------------------------------- k_pack
+
+constexpr int OU_KB = 64;                 // rows of a block
+constexpr uint32_t OU_CORE = OU_KB * 16;  // 8 terms of 64 rows
+
+// r rounded up to 16: columns of a product
+__host__ __device__ inline int32_t outer_r16(int32_t r) { return (r + 15) / 16 * 16; }
+// P of a block of 64 rows: hi octets, then lo octets, each as 8 core matrices
+// of 8 rows x 8 terms
+__host__ __device__ inline uint32_t outer_p_bytes(int32_t r) {
+  return 2 * (uint32_t)(outer_r16(r) / 8) * OU_CORE;
+}
+
+// What is noted about a block of rows: their adapter when all 64 have the same
+// one, or
+constexpr int32_t OU_NONE = -1, OU_MIXED = -2;
+
+struct PackJob {
+  const float *p;        // [s][r]
+  const uint32_t *amax;  // [n]
+  uint8_t *out;          // [blocks of 64 rows][outer_p_bytes]
+};
+
+struct PackParams {
+  PackJob job[2];
+  int32_t jobs, blocks;  // jobs * blocks blocks of threads
+  int32_t s, n, r;
+  const int32_t *ids;
+  int32_t *info;         // [blocks]
+};
+
+// One block of rows of one job (index i of jobs * blocks), by a whole block of
+// threads: each row scaled for its own adapter; zeros for rows without one,
+// rows past s and terms past r.
+__device__ __forceinline__ void pack_block(const PackParams &p, int32_t i) {
+  const PackJob &job = p.job[i / p.blocks];
+  const int32_t b = i % p.blocks;
+  const int64_t row0 = (int64_t)b * OU_KB;
+  if (i < p.blocks) {  // the note, once
+    const int64_t row = row0 + threadIdx.x;
+    const bool mine = threadIdx.x < OU_KB;
+    const int a = mine && row < p.s ? adapter_of(p.ids, row, p.n) : -1;
+    const int lead = adapter_of(p.ids, row0, p.n);
+    const bool same = __syncthreads_and(!mine || a == lead);
+    const bool none = __syncthreads_and(a < 0);
+    if (threadIdx.x == 0) p.info[b] = none ? OU_NONE : same ? lead : OU_MIXED;
+  }
+  uint8_t *dst = job.out + (size_t)b * outer_p_bytes(p.r);
+  const int octs = outer_r16(p.r) / 8;
+  for (int e = threadIdx.x; e < octs * OU_KB; e += blockDim.x) {
+    const int oct = e / OU_KB, k = e % OU_KB;
+    const int64_t row = row0 + k;
+    const int a = row < p.s ? adapter_of(p.ids, row, p.n) : -1;
+    float x[8] = {}, f = 0.0f;
+    if (a >= 0 && oct < p.r / 8) {
+      f = pow2(-scale_exponent(__uint_as_float(job.amax[a])));
+      Vec8<float> v;
+      v.load(job.p + row * p.r + oct * 8);
+      v.get(x);
+    }
+    uint4 hi, lo;
+    split8(x, f, hi, lo);
+    *reinterpret_cast<uint4 *>(dst + oct * OU_CORE + k * 16) = hi;
+    *reinterpret_cast<uint4 *>(dst + (octs + oct) * OU_CORE + k * 16) = lo;
+  }
+}
+
+// On its own where no k_expand runs (dX not wanted). Grid: jobs * blocks.
+constexpr int PK_THREADS = 256;
+__global__ void __launch_bounds__(PK_THREADS) k_pack(const __grid_constant__ PackParams p) {
+  grid_dependency_trigger();
+  grid_dependency_wait();
+  pack_block(p, (int32_t)blockIdx.x);
+}
+
 // ------------------------------------------------------------------ k_expand
 
 constexpr int EX_N = 64;           // features per step
@@ -482,10 +558,19 @@ __host__ __device__ inline uint32_t expand_bytes(int32_t r, int32_t ring, int32_
          (uint32_t)r * 2 * TM * 2 + (uint32_t)sizeof(TileSlots) + TM * 4 + 512 + 1024;
 }
 
-// Grid: row tiles * chunks.
+// Grid: row tiles * chunks, then the blocks that k_pack would have.
 __global__ void __launch_bounds__(EX_THREADS)
     k_expand(const __grid_constant__ CUtensorMap tm_base,
-             const __grid_constant__ CUtensorMap tm_out, const ExpandParams p) {
+             const __grid_constant__ CUtensorMap tm_out, const ExpandParams p,
+             const __grid_constant__ PackParams pack) {
+  const int32_t tiles = (p.s + TM - 1) / TM;
+  if ((int32_t)(blockIdx.x / p.chunks) >= tiles) {
+    grid_dependency_trigger();
+    grid_dependency_wait();
+    pack_block(pack, (int32_t)blockIdx.x - tiles * p.chunks);
+    return;
+  }
+  grid_dependency_trigger();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t *base = smem_raw + pad;
@@ -782,9 +867,8 @@ __global__ void __launch_bounds__(EX_THREADS)
   if (warp == 2) tmem_dealloc(tmem, EX_N * EX_ACC);
 }
 
-// ------------------------------------------------------------ k_pack, k_outer
+// ------------------------------------------------------------------- k_outer
 
-constexpr int OU_KB = 64;          // rows per stage
 constexpr int OU_COLS = 256;       // features per cluster: two M = 128 products
 constexpr int OU_SUM_WARPS = 8;
 constexpr int OU_THREADS = 32 * (2 + OU_SUM_WARPS);
@@ -794,62 +878,6 @@ constexpr int OU_MAX_SPLIT = 8;
 constexpr int OU_WINDOW = 512;     // blocks of rows looked through at a time
 constexpr uint32_t OU_Q_BYTES = OU_KB * OU_COLS * 2;
 constexpr uint32_t OU_BLOCK_BYTES = OU_KB * 128;  // 64 features x 64 rows
-constexpr uint32_t OU_CORE = OU_KB * 16;          // 8 terms of 64 rows
-
-// r rounded up to 16: columns of a product
-__host__ __device__ inline int32_t outer_r16(int32_t r) { return (r + 15) / 16 * 16; }
-// P of a block of 64 rows: hi octets, then lo octets, each as 8 core matrices
-// of 8 rows x 8 terms
-__host__ __device__ inline uint32_t outer_p_bytes(int32_t r) {
-  return 2 * (uint32_t)(outer_r16(r) / 8) * OU_CORE;
-}
-
-// What k_pack notes about a block of rows: their adapter when all 64 have the
-// same one, or
-constexpr int32_t OU_NONE = -1, OU_MIXED = -2;
-
-struct PackJob {
-  const float *p;        // [s][r]
-  const uint32_t *amax;  // [n]
-  uint8_t *out;          // [blocks of 64 rows][outer_p_bytes]
-};
-
-// Each row scaled for its own adapter; zeros for rows without one, rows past
-// s and terms past r. One block of threads per block of rows; grid (blocks,
-// jobs).
-constexpr int PK_THREADS = 256;
-__global__ void __launch_bounds__(PK_THREADS)
-    k_pack(const PackJob j0, const PackJob j1, int32_t s, int32_t n, int32_t r,
-           const int32_t *__restrict__ ids, int32_t *__restrict__ info) {
-  const PackJob &job = blockIdx.y == 0 ? j0 : j1;
-  grid_dependency_trigger();
-  const int k = threadIdx.x % OU_KB;
-  const int64_t row = (int64_t)blockIdx.x * OU_KB + k;
-  const int a = row < s ? adapter_of(ids, row, n) : -1;
-  grid_dependency_wait();
-  if (blockIdx.y == 0) {
-    const int64_t row0 = (int64_t)blockIdx.x * OU_KB;
-    const int lead = adapter_of(ids, row0, n);
-    const bool same = __syncthreads_and(a == lead);
-    const bool none = __syncthreads_and(a < 0);
-    if (threadIdx.x == 0) info[blockIdx.x] = none ? OU_NONE : same ? lead : OU_MIXED;
-  }
-  const float f = a >= 0 ? pow2(-scale_exponent(__uint_as_float(job.amax[a]))) : 0.0f;
-  uint8_t *dst = job.out + (size_t)blockIdx.x * outer_p_bytes(r) + k * 16;
-  const int octs = outer_r16(r) / 8;
-  for (int oct = threadIdx.x / OU_KB; oct < octs; oct += PK_THREADS / OU_KB) {
-    float x[8] = {};
-    if (a >= 0 && oct < r / 8) {
-      Vec8<float> v;
-      v.load(job.p + row * r + oct * 8);
-      v.get(x);
-    }
-    uint4 hi, lo;
-    split8(x, f, hi, lo);
-    *reinterpret_cast<uint4 *>(dst + oct * OU_CORE) = hi;
-    *reinterpret_cast<uint4 *>(dst + (octs + oct) * OU_CORE) = lo;
-  }
-}
 
 struct OuterParams {
   int32_t s, w, n, r;      // rows, features

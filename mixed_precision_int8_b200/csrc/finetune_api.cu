@@ -260,8 +260,8 @@ int shrink_split(int64_t s, int64_t k, int32_t r, int n_jobs, int sm_count) {
 // out = base + scale * v . F
 llmint8_status enqueue_expand(const float *v, const float *vmax, int64_t s, int64_t o,
                               const uint16_t *F, const llmint8_adapters *ad, const int32_t *ids,
-                              const uint16_t *base, uint16_t *out, void *ws, int sm_count,
-                              cudaStream_t st) {
+                              const uint16_t *base, uint16_t *out, const lora::PackParams *pack,
+                              void *ws, int sm_count, cudaStream_t st) {
   lora::ExpandParams p;
   p.s = (int32_t)s;
   p.o = (int32_t)o;
@@ -275,12 +275,17 @@ llmint8_status enqueue_expand(const float *v, const float *vmax, int64_t s, int6
   p.ring = 2;
   while (p.ring < lora::EX_MAX_RING && lora::expand_bytes(ad->r, p.ring + 1, p.fbufs) <= limit)
     ++p.ring;
-  // chunks of steps per row tile: the fewest CTA rounds for their length (a
-  // CTA's start counted as three steps)
+  // chunks of steps per row tile: the fewest CTA rounds for their length, a
+  // CTA's start counted as three steps and one per octet of terms. In a single
+  // round nothing overlaps the starts and the ends, which is counted as eight
+  // steps more (4096 x 20480 at rank 16: 67 us with 9 chunks, 58 with 18; 4096
+  // x 5120 at rank 64: 23 us with 9, 31 with 18).
   const int64_t tiles = ceil_div(s, lora::TM), room = (int64_t)per_sm * sm_count;
   int64_t best = INT64_MAX;
-  for (int64_t c = 1; c <= std::min<int64_t>(p.steps, std::max<int64_t>(room / tiles, 16)); ++c) {
-    const int64_t cost = ceil_div(tiles * c, room) * (ceil_div(p.steps, c) + 3);
+  for (int64_t c = 1; c <= std::min<int64_t>(p.steps, std::max<int64_t>(2 * room / tiles, 16));
+       ++c) {
+    const int64_t rounds = ceil_div(tiles * c, room);
+    const int64_t cost = rounds * (ceil_div(p.steps, c) + 3 + ad->r / 8) + (rounds == 1 ? 8 : 0);
     if (cost < best) {
       best = cost;
       p.chunks = (int32_t)c;
@@ -300,9 +305,11 @@ llmint8_status enqueue_expand(const float *v, const float *vmax, int64_t s, int6
       !make_tmap_f16(&tm_base, const_cast<uint16_t *>(base ? base : out), (uint64_t)o, (uint64_t)s,
                      lora::EX_N, lora::TM))
     return LLMINT8_ERR_CUDA;
-  if (launch(lora::k_expand, dim3((unsigned)(tiles * p.chunks)), dim3(lora::EX_THREADS),
-             lora::expand_bytes(ad->r, p.ring, p.fbufs), st, true, tm_base, tm_out,
-             p) != cudaSuccess)
+  const lora::PackParams none = {};
+  const int64_t pack_blocks = pack ? (int64_t)pack->jobs * pack->blocks : 0;
+  if (launch(lora::k_expand, dim3((unsigned)(tiles * p.chunks + pack_blocks)),
+             dim3(lora::EX_THREADS), lora::expand_bytes(ad->r, p.ring, p.fbufs), st, true, tm_base,
+             tm_out, p, pack ? *pack : none) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   return LLMINT8_OK;
 }
@@ -592,8 +599,8 @@ llmint8_status llmint8_adapters_forward(const uint16_t *X_dev, int64_t s,
                   nullptr, shrink_split(s, ad->h, ad->r, 1, dev->sm_count), ws_dev) ||
       launch_shrink(&job, 1, st) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
-  if ((rc = enqueue_expand(v, vmax, s, ad->o, ad->b_dev, ad, ids_dev, base_dev, out_dev, ws_dev,
-                           dev->sm_count, st)))
+  if ((rc = enqueue_expand(v, vmax, s, ad->o, ad->b_dev, ad, ids_dev, base_dev, out_dev, nullptr,
+                           ws_dev, dev->sm_count, st)))
     return rc;
   return last_launch();
 }
@@ -661,11 +668,16 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
     return last_launch();
   }
   const bool own_v = dB_dev && v_dev;  // v as the caller kept it: only its maxima
-  const bool sums = dA_dev || dB_dev;
   int32_t *info = reinterpret_cast<int32_t *>(wsb + L.info);
   lora::ShrinkJob shrink[2];
   lora::OuterJob outer[2];
-  lora::PackJob pack[2];
+  lora::PackParams pack = {};
+  pack.blocks = (int32_t)ceil_div(s, lora::OU_KB);
+  pack.s = (int32_t)s;
+  pack.n = ad->n;
+  pack.r = ad->r;
+  pack.ids = ids_dev;
+  pack.info = info;
   int n_shrink = 0, n_outer = 0;
   const int want = (need_g ? 1 : 0) + (need_v ? 1 : 0);
   const int split = std::min(shrink_split(s, ad->h, ad->r, want, dev->sm_count),
@@ -678,18 +690,18 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
                             v_amax, nullptr, nullptr, split, ws_dev))
     return LLMINT8_ERR_CUDA;
   if (dB_dev) {
-    pack[n_outer] = {v_dev ? v_dev : v, v_amax, wsb + L.vpack};
-    if (!outer_job(&outer[n_outer++], wsb + L.vpack, info, v_amax, dY_dev, s, ad->o, ad, ids_dev, dB_dev,
-                   ws_dev))
+    pack.job[n_outer] = {v_dev ? v_dev : v, v_amax, wsb + L.vpack};
+    if (!outer_job(&outer[n_outer++], wsb + L.vpack, info, v_amax, dY_dev, s, ad->o, ad, ids_dev,
+                   dB_dev, ws_dev))
       return LLMINT8_ERR_CUDA;
   }
   if (dA_dev) {
-    pack[n_outer] = {g, g_amax, wsb + L.gpack};
-    if (!outer_job(&outer[n_outer++], wsb + L.gpack, info, g_amax, X_dev, s, ad->h, ad, ids_dev, dA_dev,
-                   ws_dev))
+    pack.job[n_outer] = {g, g_amax, wsb + L.gpack};
+    if (!outer_job(&outer[n_outer++], wsb + L.gpack, info, g_amax, X_dev, s, ad->h, ad, ids_dev,
+                   dA_dev, ws_dev))
       return LLMINT8_ERR_CUDA;
   }
-  if (sums && cudaMemsetAsync(v_amax, 0, 8 * (size_t)ad->n, st) != cudaSuccess)
+  if (n_outer > 0 && cudaMemsetAsync(v_amax, 0, 8 * (size_t)ad->n, st) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   if (n_shrink > 0) {
     if (launch_shrink(shrink, n_shrink, st) != cudaSuccess) return LLMINT8_ERR_CUDA;
@@ -697,14 +709,17 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
                              false, v_dev, s, ad->n, ad->r, ids_dev, v_amax) != cudaSuccess) {
     return LLMINT8_ERR_CUDA;
   }
-  if (dX_dev && (rc = enqueue_expand(g, gmax, s, ad->h, ad->a_dev, ad, ids_dev, base_dev, dX_dev,
-                                     ws_dev, dev->sm_count, st)))
-    return rc;
-  if (n_outer > 0 &&
-      (launch(lora::k_pack, dim3((unsigned)ceil_div(s, lora::OU_KB), (unsigned)n_outer),
-              dim3(lora::PK_THREADS), 0, st, true, pack[0], pack[n_outer - 1], (int32_t)s, ad->n,
-              ad->r, ids_dev, info) != cudaSuccess ||
-       launch_outer(outer, n_outer, dev->sm_count, st) != cudaSuccess))
+  pack.jobs = n_outer;
+  if (dX_dev) {
+    if ((rc = enqueue_expand(g, gmax, s, ad->h, ad->a_dev, ad, ids_dev, base_dev, dX_dev,
+                             n_outer > 0 ? &pack : nullptr, ws_dev, dev->sm_count, st)))
+      return rc;
+  } else if (n_outer > 0 &&
+             launch(lora::k_pack, dim3((unsigned)(n_outer * pack.blocks)), dim3(lora::PK_THREADS),
+                    0, st, true, pack) != cudaSuccess) {
+    return LLMINT8_ERR_CUDA;
+  }
+  if (n_outer > 0 && launch_outer(outer, n_outer, dev->sm_count, st) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   return last_launch();
 }
