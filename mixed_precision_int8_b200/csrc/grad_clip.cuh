@@ -10,8 +10,14 @@
 // alike; the table also holds the entry in which each range starts (a search
 // for it in the kernel took 4 us of 256 entries). The norm kernel leaves one fp64 partial sum per block; the
 // scaling kernel's blocks each add those partial sums in the same order, so
-// the result does not depend on timing, and take their ranges from the end
-// of the list, where the norm kernel's reads are still in L2.
+// the result does not depend on timing, and walk their ranges from the end.
+// The norm kernel reads the last KEPT_CHUNKS of all ranges with the default L2
+// policy and what lies before as data not needed again, as the scaling kernel
+// does all it reads and writes: so those ends are still in L2 when it comes to
+// them. Measured: 16 tensors of 420 MB (fp16) in 221 us, 229 with ranges walked
+// forwards and no policy (5.7 TB/s over two reads and a write; the bytes alone
+// 192 us), 233 backwards without the policy; 256 tensors of 67 MB (fp32) 40 us
+// instead of 43. Chunks of 32 KB instead of 16: 233 and 43 us.
 //
 // Sums are fp64. The squares of a 16-byte vector are added in fp32 first
 // (converting every element to fp64 took twice as long as its bytes), unless
@@ -30,6 +36,7 @@ namespace clip {
 
 constexpr int THREADS = 512;
 constexpr int CHUNK_BYTES = 16384;  // two vectors of 16 bytes per thread
+constexpr int KEPT_CHUNKS = 5120;  // 80 MB of the 126 MB of L2
 constexpr int MAX_BLOCKS = 1024;   // partial sums a list holds
 constexpr int INIT_ENTRIES = 48;   // entries one launch of k_list_init carries
 constexpr int INIT_STARTS = 512;   // range starts one launch of k_starts_init carries
@@ -114,9 +121,10 @@ __device__ __forceinline__ double vector_square_sum(const Pack<T> &p) {
   return acc;
 }
 
-// Sum of squares of elements [0, m) of g, at most a chunk.
+// Sum of squares of elements [0, m) of g, at most a chunk; `again`: it should
+// stay in L2.
 template <typename T>
-__device__ __forceinline__ double chunk_square_sum(const T *g, int m) {
+__device__ __forceinline__ double chunk_square_sum(const T *g, int m, bool again) {
   double acc = 0.0;
   constexpr int N = Pack<T>::N;
   constexpr int PER = CHUNK_BYTES / 16 / THREADS;  // vectors per thread in a full chunk
@@ -126,8 +134,10 @@ __device__ __forceinline__ double chunk_square_sum(const T *g, int m) {
     if (nv == PER * THREADS) {
       Pack<T> p[PER];
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        p[i].q = __ldg(reinterpret_cast<const uint4 *>(g) + threadIdx.x + i * THREADS);
+      for (int i = 0; i < PER; ++i) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(g) + threadIdx.x + i * THREADS;
+        p[i].q = again ? __ldg(q) : __ldcs(q);
+      }
 #pragma unroll
       for (int i = 0; i < PER; ++i) acc += vector_square_sum(p[i]);
     } else {
@@ -157,12 +167,12 @@ __device__ __forceinline__ void chunk_scale(const T *g, T *out, int m, float coe
       Pack<T> p[PER];
 #pragma unroll
       for (int i = 0; i < PER; ++i)
-        p[i].q = reinterpret_cast<const uint4 *>(g)[threadIdx.x + i * THREADS];
+        p[i].q = __ldcs(reinterpret_cast<const uint4 *>(g) + threadIdx.x + i * THREADS);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
 #pragma unroll
         for (int e = 0; e < N; ++e) from_f(p[i].v[e], to_f(p[i].v[e]) * coef);
-        reinterpret_cast<uint4 *>(out)[threadIdx.x + i * THREADS] = p[i].q;
+        __stcs(reinterpret_cast<uint4 *>(out) + threadIdx.x + i * THREADS, p[i].q);
       }
     } else {
       for (int i = threadIdx.x; i < nv; i += THREADS) {
@@ -185,6 +195,7 @@ __global__ void __launch_bounds__(THREADS)
   grid_dependency_trigger();
   const int64_t c0 = range_start(chunks, blockIdx.x, gridDim.x);
   const int64_t c1 = range_start(chunks, blockIdx.x + 1, gridDim.x);
+  const int64_t kept = c1 - KEPT_CHUNKS / gridDim.x;
   double acc = 0.0;
   int64_t t = starts[blockIdx.x];
   for (int64_t c = c0; c < c1; ++c) {
@@ -194,11 +205,11 @@ __global__ void __launch_bounds__(THREADS)
     const int64_t at = (c - e.chunk0) * full;
     const int m = (int)(e.n - at < full ? e.n - at : full);
     if (e.type == LLMINT8_F16)
-      acc += chunk_square_sum(static_cast<const __half *>(e.grad) + at, m);
+      acc += chunk_square_sum(static_cast<const __half *>(e.grad) + at, m, c >= kept);
     else if (e.type == LLMINT8_BF16)
-      acc += chunk_square_sum(static_cast<const __nv_bfloat16 *>(e.grad) + at, m);
+      acc += chunk_square_sum(static_cast<const __nv_bfloat16 *>(e.grad) + at, m, c >= kept);
     else
-      acc += chunk_square_sum(static_cast<const float *>(e.grad) + at, m);
+      acc += chunk_square_sum(static_cast<const float *>(e.grad) + at, m, c >= kept);
   }
   acc = warp_sum(acc);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = acc;
@@ -233,12 +244,13 @@ __global__ void __launch_bounds__(THREADS)
   }
   __syncthreads();
   const float coef = s_coef;
-  // ranges from the end of the list, each in order
-  const int64_t b = gridDim.x - 1 - blockIdx.x;
-  const int64_t c0 = range_start(chunks, b, gridDim.x), c1 = range_start(chunks, b + 1, gridDim.x);
-  int64_t t = starts[b];
-  for (int64_t c = c0; c < c1; ++c) {
-    while (t + 1 < n && table[t + 1].chunk0 <= c) ++t;
+  // from the end of the range
+  const int64_t c0 = range_start(chunks, blockIdx.x, gridDim.x);
+  const int64_t c1 = range_start(chunks, blockIdx.x + 1, gridDim.x);
+  if (c0 == c1) return;
+  int64_t t = blockIdx.x + 1 < gridDim.x ? starts[blockIdx.x + 1] : n - 1;
+  for (int64_t c = c1 - 1; c >= c0; --c) {
+    while (table[t].chunk0 > c) --t;
     const Entry e = table[t];
     if (coef == 1.0f && e.out == e.grad) continue;  // nothing to change in place
     const int full = chunk_elements(e.type);
