@@ -974,8 +974,10 @@ __global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
   for (int t = 0; t < NC * 8; ++t) acc[t] = 0.0f;
 
   const int64_t blocks = ((int64_t)p.s + OU_KB - 1) / OU_KB;
-  uint32_t it0 = 0;  // blocks this CTA has used before the window (a multiple
-                     // of OU_DRAIN: a window's last accumulator may sum fewer)
+  // blocks and accumulators that this CTA has used before the window, counted
+  // apart: a window's last accumulator may sum fewer than OU_DRAIN blocks, but
+  // the ring passes over no slot
+  uint32_t it0 = 0, use0 = 0;
   uint32_t cleaned = 0;  // phase of each slot's clean barrier, which only
                          // mixed blocks use
   bool failed = false;
@@ -1031,10 +1033,10 @@ __global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
       // ----------------------------------------------------- MMA issuer
       const uint32_t idesc = idesc_f16_f32_mn(128, r16, true, true);
       for (int32_t i = 0; i < mine; ++i) {
-        const uint32_t it = it0 + i, use = it / OU_DRAIN, buf = use & 1u;
+        const uint32_t it = it0 + i, use = use0 + i / OU_DRAIN, buf = use & 1u;
         const int st = (int)(it % p.stages);
         const uint32_t par = (it / p.stages) & 1u;
-        const bool fresh = it % OU_DRAIN == 0;
+        const bool fresh = i % OU_DRAIN == 0;
         if ((fresh && !mbar_wait_bounded(tempty(buf), ((use >> 1) & 1u) ^ 1u, abort_flag, p.status,
                                          LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) ||
             !mbar_wait_bounded(full(st), par, abort_flag, p.status, LLMINT8_DEV_TIMEOUT_MMA,
@@ -1057,7 +1059,7 @@ __global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
                                      OU_CORE),
                       idesc, (!fresh || hl > 0 || k > 0) ? 1u : 0u);
         mma_commit(empty(st));
-        if (it % OU_DRAIN == OU_DRAIN - 1 || i + 1 == mine) mma_commit(tfull(buf));
+        if (i % OU_DRAIN == OU_DRAIN - 1 || i + 1 == mine) mma_commit(tfull(buf));
       }
     } else if (warp >= 2) {
       const int ct = threadIdx.x - 64;
@@ -1095,7 +1097,7 @@ __global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
           if (lane == 0) mbar_arrive(clean(st));
         }
         if (!ok || j == 0) continue;
-        const uint32_t use = it0 / OU_DRAIN + j - 1, buf = use & 1u;
+        const uint32_t use = use0 + j - 1, buf = use & 1u;
         ok = mbar_wait_bounded(tfull(buf), (use >> 1) & 1u, abort_flag, p.status,
                                LLMINT8_DEV_TIMEOUT_EPILOGUE, p.timeout_ns);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -1116,7 +1118,8 @@ __global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
       }
     }
     __syncthreads();
-    it0 += (uint32_t)((mine + OU_DRAIN - 1) / OU_DRAIN * OU_DRAIN);
+    it0 += (uint32_t)mine;
+    use0 += (uint32_t)((mine + OU_DRAIN - 1) / OU_DRAIN);
     if (*abort_flag) {
       failed = true;
       break;

@@ -190,6 +190,31 @@ def test_backward_exact(case):
     assert L.llmint8_read_device_status(ws) == 0
 
 
+# more rows than one pass over the blocks of rows looks through (512 blocks of
+# 64), shared by adapters at random places: a CTA's share of a pass may end on
+# an odd block
+@pytest.mark.parametrize("s,h,o,n,r,layout", [
+    (33345, 48, 272, 3, 8, "requests"), (33345, 272, 48, 3, 64, "mixed"),
+    (66001, 48, 16, 5, 24, "requests_bare"), (66001, 16, 528, 1, 16, "requests"),
+    (100000, 16, 16, 2, 128, "requests")])
+def test_factor_gradients_of_many_rows_exact(s, h, o, n, r, layout):
+    c = Case(s, h, o, n, r, layout, "full")
+    _, v, dX, dA, dB = c.reference()
+    g = sum(torch.where((c.ids == a)[:, None], c.dY.double() @ c.B[a].double().T, 0.0)
+            for a in range(n))
+    # every partial sum is below 2^24 units: exact in fp32, whatever its order
+    assert (g.abs().T @ c.X.double().abs()).max() < 2 ** 24
+    assert (v.abs().T @ c.dY.double().abs()).max() < 2 ** 24
+    ws = L.AdapterWorkspace(s, h, o, n, r)
+    for keep in (v.float(), None):
+        got = L.llmint8_adapters_backward(c.X, c.dY, c.ad, c.ids, v=keep, base=c.dbase,
+                                          workspace=ws)
+        same(got[0], dX, torch.float16)
+        same(got[1], dA, torch.float32)
+        same(got[2], dB, torch.float32)
+    assert L.llmint8_read_device_status(ws) == 0
+
+
 def test_rows_of_unused_slots_and_other_adapters_never_reach_a_result():
     """NaN and infinities in unused rank slots, in adapters without rows, in
     rows without an adapter and in one request's own row stay where they are."""
