@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(RO_THREADS)
     count += per_warp[i];
   }
   if (mine) rows[at] = tid;
-  const int rk = rank_of(rank, a, r);
+  // (an adapter without rows has zeros, whatever its scale)
+  const int rk = count > 0 ? rank_of(rank, a, r) : 0;
   grid_dependency_wait();  // p is the preceding kernels'
   __syncthreads();
   for (int i = tid; i < count * RO_TERMS; i += RO_THREADS) {

@@ -980,7 +980,7 @@ __global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
   uint32_t it0 = 0, use0 = 0;
   uint32_t cleaned = 0;  // phase of each slot's clean barrier, which only
                          // mixed blocks use
-  bool failed = false;
+  bool failed = false, used = false;
   for (int64_t w0 = 0; w0 < blocks; w0 += OU_WINDOW) {
     const int nb = (int)min((int64_t)OU_WINDOW, blocks - w0);
     // which rows of each block are the adapter's
@@ -1010,6 +1010,7 @@ __global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
     }
     __syncthreads();
     const int32_t total = *listed;
+    used |= total > 0;
     // this CTA's i-th block of the window is list[cta + i * split]
     const int32_t mine = total > (int32_t)cta ? (total - (int32_t)cta + p.split - 1) / p.split : 0;
     if (warp == 0 && lane == 0) {
@@ -1150,7 +1151,8 @@ __global__ void __launch_bounds__(OU_THREADS, NC <= 8 ? 2 : 1)
   if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
   if (p.split > 1) cluster_sync();
   const float f = p.scale[a] * pow2(scale_exponent(__uint_as_float(p.amax[a])));
-  const int rk = rank_of(p.rank, a, p.r);
+  // (an adapter without rows has zeros, whatever its scale)
+  const int rk = used ? rank_of(p.rank, a, p.r) : 0;
   // this CTA's terms are cta, cta + split, ...; four features per thread, and
   // every CTA's load under way before the first is added
   const int quads = OU_COLS / 4, terms = (p.r - (int)cta + p.split - 1) / p.split;

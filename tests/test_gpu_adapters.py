@@ -254,6 +254,19 @@ def test_rows_of_unused_slots_and_other_adapters_never_reach_a_result():
             same(got[2][a], dB[a], torch.float32)
 
 
+@pytest.mark.parametrize("s", [12, 300])
+def test_gradients_of_adapters_without_rows_are_zeros_whatever_their_scale(s):
+    c = Case(s, 528, 784, 4, 16, "mixed", "full")
+    c.ids[c.ids == 2] = 1
+    c.scale[2] = float("nan")
+    got = L.llmint8_adapters_backward(c.X, c.dY, c.ad, c.ids, base=c.dbase)
+    c.scale[2] = 1.0
+    ref = L.llmint8_adapters_backward(c.X, c.dY, c.ad, c.ids, base=c.dbase)
+    for a, b in zip(got, ref):
+        assert torch.equal(a, b)
+    assert not got[1][2].any() and not got[2][2].any()
+
+
 def test_rows_without_an_adapter_keep_the_bits_of_their_base():
     for s in (9, 200):
         c = Case(s, 272, 528, 2, 8, "mixed", "full", seed=5)
