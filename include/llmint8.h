@@ -458,8 +458,8 @@ LLMINT8_API size_t llmint8_adapters_workspace_size(int64_t s, int64_t h, int64_t
  * rows a tile of 128 costs a pass per adapter in it: keep a request's rows
  * together); a row whose id is outside [0, n) uses no adapter: its out is its base, unchanged.
  * base_dev (fp16 [s][o]) is llmint8_matmul's output; NULL stands for zeros.
- * out_dev (fp16 [s][o]) may be base_dev itself; else it must not overlap it,
- * nor X_dev (LLMINT8_ERR_ARG).
+ * out_dev (fp16 [s][o]) may be base_dev itself; else neither it nor v_dev
+ * overlaps an input or the other (LLMINT8_ERR_ARG).
  * v_dev, when not NULL, receives v (fp32 [s][r], 16-byte aligned; 0 where a
  * row has no adapter or t >= rank[a]) for the backward pass. A row's result
  * depends on its own row of X and its own adapter only: infinities and NaN of
@@ -478,8 +478,9 @@ LLMINT8_API llmint8_status llmint8_adapters_forward(
  * there, or NULL: then v is computed again from X. base_dev (fp16 [s][h]) is
  * the gradient that reaches X through the projection itself
  * (llmint8_matmul_backward); NULL stands for zeros. dX_dev (fp16 [s][h]) may
- * be base_dev itself, and overlaps no other input (LLMINT8_ERR_ARG). dA_dev, dB_dev: fp32, the factors' shapes, written
- * whole (zeros for unused slots and adapters without rows). Any of the three
+ * be base_dev itself; else no output overlaps an input or another output
+ * (LLMINT8_ERR_ARG). dA_dev, dB_dev: fp32, the factors' shapes, written whole
+ * (zeros for unused slots and adapters without rows). Any of the three
  * outputs may be NULL (not wanted); X_dev may be NULL when dA_dev is and v
  * need not be computed. The sums over rows run in a fixed order. */
 LLMINT8_API llmint8_status llmint8_adapters_backward(
@@ -507,7 +508,9 @@ LLMINT8_API llmint8_status llmint8_matmul_backward(const uint16_t *dY_dev, int64
  *   y_j = fp16((x_j - mean) * rstd * gamma_j + beta_j)
  * x is fp16 or fp32 (x_type), gamma and beta [h] fp16 or fp32 (p_type);
  * beta_dev may be NULL (zeros). mean_dev, rstd_dev (fp32 [s], 4-byte aligned,
- * or NULL) keep the statistics for the backward pass. eps >= 0 and finite. */
+ * or NULL) keep the statistics for the backward pass. eps >= 0 and finite.
+ * y_dev may be x_dev itself where x is fp16; else no output overlaps an input
+ * or another output (LLMINT8_ERR_ARG). */
 LLMINT8_API llmint8_status llmint8_layernorm_forward(const void *x_dev, int32_t x_type, int64_t s,
                                                      int64_t h, const void *gamma_dev,
                                                      const void *beta_dev, int32_t p_type,
@@ -518,8 +521,10 @@ LLMINT8_API llmint8_status llmint8_layernorm_forward(const void *x_dev, int32_t 
  *   xh = (x - mean) * rstd, g = dy * gamma
  *   dx = rstd * (g - sum_j g / h - xh * sum_j (g * xh) / h)     in x's type
  *   dgamma_j = sum_i dy_ij * xh_ij,  dbeta_j = sum_i dy_ij      fp32 [h]
- * dx_dev, dgamma_dev and dbeta_dev may be NULL (not wanted). The sums over
- * rows run in a fixed order. */
+ * dx_dev, dgamma_dev and dbeta_dev may be NULL (not wanted). dx_dev may be
+ * x_dev itself or, where x is fp16, dy_dev; else no output overlaps an input
+ * or another output (LLMINT8_ERR_ARG). The sums over rows run in a fixed
+ * order. */
 LLMINT8_API size_t llmint8_layernorm_workspace_size(int64_t s, int64_t h);
 LLMINT8_API llmint8_status llmint8_layernorm_backward(
     const uint16_t *dy_dev, const void *x_dev, int32_t x_type, int64_t s, int64_t h,

@@ -690,7 +690,8 @@ def llmint8_layernorm_forward(X: torch.Tensor, gamma: torch.Tensor,
                               beta: Optional[torch.Tensor] = None, eps: float = 1e-5,
                               out: Optional[torch.Tensor] = None, stream=None):
     """(Y fp16 [s,h], mean float32 [s], rstd float32 [s]) = layer norm of the
-    rows of X (fp16 or fp32 [s,h]); gamma and beta [h] are fp16 or fp32 alike."""
+    rows of X (fp16 or fp32 [s,h]); gamma and beta [h] are fp16 or fp32 alike.
+    out may be an fp16 X itself."""
     s, h = _matrix(X, "X")
     dev, ptype = X.device, gamma.dtype
     tx, tp = _ln_type(X, "X"), _ln_type(gamma, "gamma")
@@ -711,7 +712,8 @@ def llmint8_layernorm_backward(dY: torch.Tensor, X: torch.Tensor, gamma: torch.T
                                dX: Optional[torch.Tensor] = None,
                                workspace: Optional[LayerNormWorkspace] = None, stream=None):
     """(dX in X's type, dgamma float32 [h], dbeta float32 [h]) for dY fp16
-    [s,h], with the forward call's mean and rstd."""
+    [s,h], with the forward call's mean and rstd. dX may be X itself, or dY
+    where X is fp16."""
     s, h = _matrix(X, "X")
     dev, f32 = X.device, torch.float32
     tx, tp = _ln_type(X, "X"), _ln_type(gamma, "gamma")

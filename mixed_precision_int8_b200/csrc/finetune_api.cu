@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -114,6 +115,23 @@ bool overlap(const void *p, size_t pn, const void *q, size_t qn) {
   return a < b + qn && b < a + pn;
 }
 
+struct Span {
+  const void *p;
+  size_t n;
+};
+
+// Whether `out` shares a byte with any of these tensors.
+bool overlaps_any(Span out, std::initializer_list<Span> others) {
+  for (const Span &t : others)
+    if (overlap(out.p, out.n, t.p, t.n)) return true;
+  return false;
+}
+
+// Whether `out` overlaps `in` without being the same tensor.
+bool overlaps_partly(Span out, Span in) {
+  return (out.p != in.p || out.n != in.n) && overlap(out.p, out.n, in.p, in.n);
+}
+
 // ------------------------------------------------------------- adapters
 
 // The row kernels (adapters.cuh) take batches of at most one tile of rows, and
@@ -170,6 +188,13 @@ llmint8_status check_adapters(const llmint8_adapters *ad, int64_t s) {
       !aligned(ad->rank_dev, 4))
     return LLMINT8_ERR_ALIGN;
   return LLMINT8_OK;
+}
+
+Span factor_a(const llmint8_adapters *ad) {
+  return {ad->a_dev, 2 * (size_t)ad->n * ad->r * ad->h};
+}
+Span factor_b(const llmint8_adapters *ad) {
+  return {ad->b_dev, 2 * (size_t)ad->n * ad->r * ad->o};
 }
 
 const __half *as_half(const uint16_t *p) { return reinterpret_cast<const __half *>(p); }
@@ -521,12 +546,12 @@ int64_t clip_blocks(int64_t chunks, int sm_count) {
 // LLMINT8_ERR_ARG when two outputs share memory, or an output and another
 // entry's gradient: blocks of one call would race on it.
 llmint8_status check_grad_overlaps(const llmint8_grad *grads, int64_t n) {
-  struct Span {
+  struct Range {
     uintptr_t begin, end;
     bool written;
   };
   try {
-    std::vector<Span> spans;
+    std::vector<Range> spans;
     spans.reserve(2 * (size_t)n);
     for (int64_t i = 0; i < n; ++i) {
       const llmint8_grad &g = grads[i];
@@ -538,9 +563,9 @@ llmint8_status check_grad_overlaps(const llmint8_grad *grads, int64_t n) {
       if (out != in) spans.push_back({in, in + bytes, false});
     }
     std::sort(spans.begin(), spans.end(),
-              [](const Span &a, const Span &b) { return a.begin < b.begin; });
+              [](const Range &a, const Range &b) { return a.begin < b.begin; });
     uintptr_t read_end = 0, written_end = 0;
-    for (const Span &s : spans) {
+    for (const Range &s : spans) {
       if (s.begin < written_end || (s.written && s.begin < read_end)) return LLMINT8_ERR_ARG;
       uintptr_t &end = s.written ? written_end : read_end;
       end = std::max(end, s.end);
@@ -550,6 +575,8 @@ llmint8_status check_grad_overlaps(const llmint8_grad *grads, int64_t n) {
   }
   return LLMINT8_OK;
 }
+
+size_t type_size(int32_t type) { return type == LLMINT8_F32 ? 4 : 2; }
 
 bool ln_types_ok(int32_t x_type, int32_t p_type) {
   return (x_type == LLMINT8_F16 || x_type == LLMINT8_F32) &&
@@ -576,9 +603,12 @@ llmint8_status llmint8_adapters_forward(const uint16_t *X_dev, int64_t s,
   if (!aligned(X_dev, 16) || !aligned(ids_dev, 4) || !aligned(base_dev, 16) ||
       !aligned(out_dev, 16) || !aligned(v_dev, 16) || !aligned(ws_dev, 256))
     return LLMINT8_ERR_ALIGN;
-  const size_t in_bytes = 2 * (size_t)s * ad->h, out_bytes = 2 * (size_t)s * ad->o;
-  if (overlap(out_dev, out_bytes, X_dev, in_bytes) ||
-      (base_dev != out_dev && overlap(out_dev, out_bytes, base_dev, out_bytes)))
+  const Span X = {X_dev, 2 * (size_t)s * ad->h}, base = {base_dev, 2 * (size_t)s * ad->o};
+  const Span out = {out_dev, base.n}, kept = {v_dev, 4 * (size_t)s * ad->r};
+  const Span ids = {ids_dev, 4 * (size_t)s}, A = factor_a(ad), B = factor_b(ad);
+  const Span scale = {ad->scale_dev, 4 * (size_t)ad->n}, rank = {ad->rank_dev, scale.n};
+  if (overlaps_any(out, {X, kept, ids, A, B, scale, rank}) || overlaps_partly(out, base) ||
+      overlaps_any(kept, {X, base, ids, A, B, scale, rank}))
     return LLMINT8_ERR_ARG;
   const AdapterLayout L = adapter_layout(s, ad->h, ad->o, ad->n, ad->r);
   if (ws_bytes < L.end) return LLMINT8_ERR_WORKSPACE;
@@ -619,9 +649,14 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
       !aligned(base_dev, 16) || !aligned(dX_dev, 16) || !aligned(dA_dev, 16) ||
       !aligned(dB_dev, 16) || !aligned(ws_dev, 256))
     return LLMINT8_ERR_ALIGN;
-  const size_t in_bytes = 2 * (size_t)s * ad->h, out_bytes = 2 * (size_t)s * ad->o;
-  if (overlap(dX_dev, in_bytes, X_dev, in_bytes) || overlap(dX_dev, in_bytes, dY_dev, out_bytes) ||
-      (base_dev != dX_dev && overlap(dX_dev, in_bytes, base_dev, in_bytes)))
+  const Span X = {X_dev, 2 * (size_t)s * ad->h}, dY = {dY_dev, 2 * (size_t)s * ad->o};
+  const Span base = {base_dev, X.n}, dX = {dX_dev, X.n}, kept = {v_dev, 4 * (size_t)s * ad->r};
+  const Span ids = {ids_dev, 4 * (size_t)s}, A = factor_a(ad), B = factor_b(ad);
+  const Span scale = {ad->scale_dev, 4 * (size_t)ad->n}, rank = {ad->rank_dev, scale.n};
+  const Span dA = {dA_dev, 2 * A.n}, dB = {dB_dev, 2 * B.n};
+  if (overlaps_any(dX, {X, dY, kept, ids, A, B, scale, rank}) || overlaps_partly(dX, base) ||
+      overlaps_any(dA, {X, dY, base, dX, kept, ids, A, B, scale, rank}) ||
+      overlaps_any(dB, {X, dY, base, dX, kept, ids, A, B, scale, rank, dA}))
     return LLMINT8_ERR_ARG;
   const AdapterLayout L = adapter_layout(s, ad->h, ad->o, ad->n, ad->r);
   if (s > 0 && ws_bytes < L.end) return LLMINT8_ERR_WORKSPACE;
@@ -750,9 +785,11 @@ llmint8_status llmint8_matmul_backward(const uint16_t *dY_dev, int64_t s, const 
   if (!aligned(dY_dev, 16) || !aligned(base_dev, 16) || !aligned(dX_dev, 16) ||
       !aligned(ws_dev, 256))
     return LLMINT8_ERR_ALIGN;
-  const size_t dx_bytes = 2 * (size_t)s * w->h;
-  if (overlap(dX_dev, dx_bytes, dY_dev, 2 * (size_t)s * w->o) ||
-      (base_dev != dX_dev && overlap(dX_dev, dx_bytes, base_dev, dx_bytes)))
+  const Span dX = {dX_dev, 2 * (size_t)s * w->h};
+  if (overlaps_any(dX, {{dY_dev, 2 * (size_t)s * w->o},
+                        {w->wq_dev, (size_t)w->h * w->o},
+                        {w->aw_dev, 4 * (size_t)w->o}}) ||
+      overlaps_partly(dX, {base_dev, dX.n}))
     return LLMINT8_ERR_ARG;
   const igrad::Plan plan = input_grad_plan(s, w->h, w->o);
   if (ws_bytes < input_grad_workspace(plan)) return LLMINT8_ERR_WORKSPACE;
@@ -807,6 +844,13 @@ llmint8_status llmint8_layernorm_forward(const void *x_dev, int32_t x_type, int6
   if (!aligned(x_dev, 16) || !aligned(gamma_dev, 16) || !aligned(beta_dev, 16) ||
       !aligned(y_dev, 16) || !aligned(mean_dev, 4) || !aligned(rstd_dev, 4))
     return LLMINT8_ERR_ALIGN;
+  // y in place of an fp16 x: a thread has read what it writes
+  const Span x = {x_dev, type_size(x_type) * (size_t)s * h}, y = {y_dev, 2 * (size_t)s * h};
+  const Span gamma = {gamma_dev, type_size(p_type) * (size_t)h}, beta = {beta_dev, gamma.n};
+  const Span mean = {mean_dev, 4 * (size_t)s}, rstd = {rstd_dev, mean.n};
+  if (overlaps_partly(y, x) || overlaps_any(y, {gamma, beta, mean, rstd}) ||
+      overlaps_any(mean, {x, gamma, beta, rstd}) || overlaps_any(rstd, {x, gamma, beta}))
+    return LLMINT8_ERR_ARG;
   Device *dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   cudaStream_t st = as_stream(stream);
@@ -841,6 +885,16 @@ llmint8_status llmint8_layernorm_backward(const uint16_t *dy_dev, const void *x_
       !aligned(dgamma_dev, 16) || !aligned(dbeta_dev, 16) || !aligned(ws_dev, 256))
     return LLMINT8_ERR_ALIGN;
   if (s > 0 && ws_bytes < llmint8_layernorm_workspace_size(s, h)) return LLMINT8_ERR_WORKSPACE;
+  // dx in place of x or dy of its type: a row's block has read the row
+  const Span x = {x_dev, type_size(x_type) * (size_t)s * h}, dy = {dy_dev, 2 * (size_t)s * h};
+  const Span dx = {dx_dev, x.n}, gamma = {gamma_dev, type_size(p_type) * (size_t)h};
+  const Span mean = {mean_dev, 4 * (size_t)s}, rstd = {rstd_dev, mean.n};
+  const Span dgamma = {dgamma_dev, 4 * (size_t)h}, dbeta = {dbeta_dev, dgamma.n};
+  if (overlaps_partly(dx, x) || overlaps_partly(dx, dy) ||
+      overlaps_any(dx, {gamma, mean, rstd, dgamma, dbeta}) ||
+      overlaps_any(dgamma, {x, dy, gamma, mean, rstd, dbeta}) ||
+      overlaps_any(dbeta, {x, dy, gamma, mean, rstd}))
+    return LLMINT8_ERR_ARG;
   Device *dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   cudaStream_t st = as_stream(stream);

@@ -194,3 +194,90 @@ def test_binding_refuses_tensors_it_cannot_take():
         binding.llmint8_layernorm_forward(torch.zeros(4, 32), torch.ones(32))
     with pytest.raises(ValueError):
         binding.llmint8_layernorm_forward(torch.zeros(32), torch.ones(32))
+
+
+def _overlapping(base_args, spans, allowed, call):
+    """Every output moved onto the last byte's place of every other tensor (or
+    onto its first) is refused; `allowed` pairs may be the same tensor."""
+    outs = [k for k, (_, written) in spans.items() if written]
+    for out in outs:
+        for other, (size, _) in spans.items():
+            if other == out:
+                continue
+            for shift in (0, size - 16 if size > 16 else 0):
+                if shift == 0 and (out, other) in allowed:
+                    continue
+                at = base_args[other].value + shift
+                args = dict(base_args, **{out: ctypes.c_void_p(at // 16 * 16)})
+                assert call(**args) == -7, (out, other, shift)
+
+
+def _places(names):
+    return {k: ctypes.c_void_p((i + 4) << 26) for i, k in enumerate(names)}
+
+
+@needs_no_gpu
+def test_outputs_that_overlap_are_refused(lib):
+    s, h, o, n, r = 40, 256, 528, 2, 8
+    size = dict(X=2 * s * h, dY=2 * s * o, ids=4 * s, base=2 * s * o, out=2 * s * o, v=4 * s * r,
+                a=2 * n * r * h, b=2 * n * r * o, scale=4 * n, rank=4 * n, dX=2 * s * h,
+                dA=4 * n * r * h, dB=4 * n * r * o)
+
+    def ad(a, b, scale, rank):
+        return ctypes.byref(binding.llmint8_adapters(h, o, n, r, a, b, scale, rank))
+
+    def forward(X, ids, base, out, v, a, b, scale, rank):
+        return lib.llmint8_adapters_forward(X, s, ad(a, b, scale, rank), ids, base, out, v, FAKE,
+                                            BIG, None)
+    names = ("X", "ids", "base", "out", "v", "a", "b", "scale", "rank")
+    spans = {k: (size[k], k in ("out", "v")) for k in names}
+    assert forward(**_places(names)) in (-5, -8)  # sound, but for the GPU
+    _overlapping(_places(names), spans, {("out", "base")}, forward)
+
+    def backward(X, dY, ids, v, base, dX, dA, dB, a, b, scale, rank):
+        return lib.llmint8_adapters_backward(X, dY, s, ad(a, b, scale, rank), ids, v, base, dX,
+                                             dA, dB, FAKE, BIG, None)
+    names = ("X", "dY", "ids", "v", "base", "dX", "dA", "dB", "a", "b", "scale", "rank")
+    size["base"] = 2 * s * h
+    spans = {k: (size[k], k in ("dX", "dA", "dB")) for k in names}
+    assert backward(**_places(names)) in (-5, -8)
+    _overlapping(_places(names), spans, {("dX", "base")}, backward)
+
+    def matmul(dY, wq, aw, base, dX):
+        w = binding.llmint8_weight(h, o, wq, aw)
+        return lib.llmint8_matmul_backward(dY, s, ctypes.byref(w), base, dX, FAKE, BIG, None)
+    names = ("dY", "wq", "aw", "base", "dX")
+    size.update(wq=h * o, aw=4 * o)
+    spans = {k: (size[k], k == "dX") for k in names}
+    assert matmul(**_places(names)) in (-5, -8)
+    _overlapping(_places(names), spans, {("dX", "base")}, matmul)
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("xt", [0, 1])
+def test_layernorm_outputs_that_overlap_are_refused(lib, xt):
+    s, h = 40, 256
+    xb = 4 if xt else 2
+
+    def fwd(x, g, b, y, mean, rstd):
+        return lib.llmint8_layernorm_forward(x, xt, s, h, g, b, 1, 1e-5, y, mean, rstd, None)
+    spans = dict(x=(xb * s * h, False), g=(4 * h, False), b=(4 * h, False),
+                 y=(2 * s * h, True), mean=(4 * s, True), rstd=(4 * s, True))
+    assert fwd(**_places(spans)) in (-5, -8)
+    _overlapping(_places(spans), spans, set() if xt else {("y", "x")}, fwd)
+    if not xt:  # in place
+        at = _places(spans)
+        assert fwd(**dict(at, y=at["x"])) in (-5, -8)
+
+    def bwd(dy, x, g, mean, rstd, dx, dg, db):
+        return lib.llmint8_layernorm_backward(dy, x, xt, s, h, g, 1, mean, rstd, dx, dg, db, FAKE,
+                                              BIG, None)
+    spans = dict(dy=(2 * s * h, False), x=(xb * s * h, False), g=(4 * h, False),
+                 mean=(4 * s, False), rstd=(4 * s, False), dx=(xb * s * h, True),
+                 dg=(4 * h, True), db=(4 * h, True))
+    allowed = {("dx", "x")} | (set() if xt else {("dx", "dy")})
+    assert bwd(**_places(spans)) in (-5, -8)
+    _overlapping(_places(spans), spans, allowed, bwd)
+    at = _places(spans)
+    for out, other in allowed:
+        assert bwd(**dict(at, **{out: at[other]})) in (-5, -8)

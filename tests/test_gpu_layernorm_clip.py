@@ -121,6 +121,28 @@ def test_layernorm_without_beta_and_its_rows_alone():
     assert torch.equal(dbuf[1:-1][ok], one)
 
 
+@pytest.mark.parametrize("s,h", [(5, 528), (700, 4096), (3, 16400)])
+def test_layernorm_in_place(s, h):
+    g = torch.Generator(device="cuda").manual_seed(s)
+    gamma = torch.randn(h, generator=g, device="cuda").half()
+    for xt in (torch.float16, torch.float32):
+        X = torch.randn(s, h, generator=g, device="cuda").to(xt)
+        dY = torch.randn(s, h, generator=g, device="cuda").half()
+        y, mean, rstd = L.llmint8_layernorm_forward(X, gamma)
+        ref = L.llmint8_layernorm_backward(dY, X, gamma, mean, rstd)
+        for place in ("x", "dy") if xt is torch.float16 else ("x",):
+            x2, dy2 = X.clone(), dY.clone()
+            got = L.llmint8_layernorm_backward(dy2, x2, gamma, mean, rstd,
+                                               dX=x2 if place == "x" else dy2)
+            for a, b in zip(got, ref):
+                assert torch.equal(a, b)
+        if xt is torch.float16:
+            x2 = X.clone()
+            got = L.llmint8_layernorm_forward(x2, gamma, out=x2)
+            for a, b in zip(got, (y, mean, rstd)):
+                assert torch.equal(a, b)
+
+
 def test_layernorm_gradient_against_differences():
     """Central differences of sum(y dY) in 64 bits, next to the kernels'
     gradients of the same inputs."""
