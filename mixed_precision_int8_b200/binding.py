@@ -745,6 +745,8 @@ class GradList:
             raise ValueError("outs must match grads one for one")
         device = self.grads[0].device if self.grads else torch.empty(
             0, device=device or "cuda").device
+        if device.type != "cuda":
+            raise ValueError(f"grads must be on a CUDA device, not on {device}")
         n = len(self.grads)
         items = (llmint8_grad * max(n, 1))()
         for i, (g, out) in enumerate(zip(self.grads, self.outs)):

@@ -194,6 +194,8 @@ def test_binding_refuses_tensors_it_cannot_take():
         binding.llmint8_layernorm_forward(torch.zeros(4, 32), torch.ones(32))
     with pytest.raises(ValueError):
         binding.llmint8_layernorm_forward(torch.zeros(32), torch.ones(32))
+    with pytest.raises(ValueError, match="on a CUDA device"):
+        binding.GradList([torch.zeros(8)])
 
 
 def _overlapping(base_args, spans, allowed, call):
