@@ -160,7 +160,7 @@ constexpr int SH_THREADS = 256;
 constexpr int SH_KB = 64;       // features per stage
 constexpr int SH_DRAIN = 4;     // stages (of 4 MMAs) that one accumulator sums
 constexpr int SH_MAX_STAGES = 8;
-constexpr int SH_MAX_SPLIT = 8;
+constexpr int SH_MAX_SPLIT = 16;  // clusters past 8 CTAs need the device's leave
 constexpr int SH_MAX_ACC = 8;
 constexpr uint32_t SH_X_BYTES = TM * SH_KB * 2;
 
@@ -208,7 +208,10 @@ __device__ __forceinline__ float warp_row_max(const float *x, int r) {
   return m;
 }
 
-// Grid: (m tiles * split, 1, jobs), clusters of `split` along x.
+// Grid: (m tiles * split, y, jobs), clusters of `split` along x. Where the row
+// tiles leave SMs free, y clusters share the passes over the adapters of a tile
+// of mixed rows (150 rows of 16 adapters, rank 128, 12288 -> 512: 184 us with
+// one cluster per tile, 56 with 9).
 __global__ void __launch_bounds__(SH_THREADS, 2)
     k_shrink(const __grid_constant__ ShrinkJob j0, const __grid_constant__ ShrinkJob j1) {
   const ShrinkJob &job = blockIdx.z == 0 ? j0 : j1;
@@ -237,7 +240,9 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
   // this CTA's blocks of features are cta, cta + split, ...: the cluster reads
   // neighbouring parts of a row at a time
   const int32_t blocks = (nk - (int32_t)cta + p.split - 1) / p.split;
-  const int early = min(p.stages, blocks);
+  // this cluster's passes over the adapters are blockIdx.y, + gridDim.y, ...
+  const int32_t first = (int32_t)blockIdx.y * p.slots, step = (int32_t)gridDim.y * p.slots;
+  const int early = first == 0 ? min(p.stages, blocks) : 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -275,7 +280,7 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
     uint32_t stage = 0, phase = 0, issued = (1u << early) - 1u, last_par = 0;
     bool ok = true;
     int32_t ahead = early;  // stages whose X is under way
-    for (int32_t s0 = 0; ok && s0 < ts.count; s0 += p.slots) {
+    for (int32_t s0 = first; ok && s0 < ts.count; s0 += step) {
       const int32_t ns = min(p.slots, ts.count - s0);
       for (int32_t i = 0; i < blocks; ++i, --ahead) {
         const int32_t kb = (int32_t)cta + i * p.split;
@@ -316,7 +321,7 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
     uint32_t stage = 0, phase = 0, aphase = 0;
     int acc = 0;
     bool ok = true, any = false;
-    for (int32_t s0 = 0; ok && s0 < ts.count; s0 += p.slots) {
+    for (int32_t s0 = first; ok && s0 < ts.count; s0 += step) {
       const uint32_t idesc =
           idesc_f16_f32(TM, (min(p.slots, ts.count - s0) * p.r + 15) / 16 * 16);
       for (int32_t kb = 0; kb < blocks; ++kb) {
@@ -364,7 +369,7 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
     int acc = 0;
     uint32_t aphase = 0;
     bool ok = true;
-    for (int32_t s0 = 0; ok && s0 < ts.count; s0 += p.slots) {
+    for (int32_t s0 = first; ok && s0 < ts.count; s0 += step) {
       const int32_t s1 = min(s0 + p.slots, ts.count);
       for (int32_t kb = 0; kb < blocks; kb += SH_DRAIN) {
         ok = mbar_wait_bounded(tfull(acc), aphase, abort_flag, p.status,
@@ -406,19 +411,28 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
   for (int i = warp; i < rows; i += SH_THREADS / 32) {
     const int row = (int)cta * rows + i;
     if (row0 + row >= p.s) continue;
+    const int a = ts.id[row];
+    if (p.w != nullptr && a >= 0 && first == 0) {
+      const float wm = warp_row_max(p.w + (row0 + row) * p.r, p.r);
+      if (lane == 0) atomicMax(p.w_amax + a, __float_as_uint(wm));
+    }
+    // (rows without an adapter are the first cluster's)
+    if (gridDim.y > 1 && max(ts.slot[row], 0) / p.slots % gridDim.y != blockIdx.y) continue;
     float largest = 0.0f;
 #pragma unroll 2
     for (int t = lane; t < p.r; t += 32) {
       float sum = 0.0f;
       if (p.split > 1) {
-        // every CTA's load under way before the first is added
+        // eight CTAs' loads under way before the first is added
         const uint32_t at = smem_u32(part + row * ldp + t);
-        float x[SH_MAX_SPLIT];
+        for (int q0 = 0; q0 < p.split; q0 += 8) {
+          float x[8];
 #pragma unroll
-        for (int q = 0; q < SH_MAX_SPLIT; ++q)
-          x[q] = q < p.split ? ld_cluster_f32(mapa_shared(at, (uint32_t)q)) : 0.0f;
+          for (int q = 0; q < 8; ++q)
+            x[q] = q0 + q < p.split ? ld_cluster_f32(mapa_shared(at, (uint32_t)(q0 + q))) : 0.0f;
 #pragma unroll
-        for (int q = 0; q < SH_MAX_SPLIT; ++q) sum += x[q];
+          for (int q = 0; q < 8; ++q) sum += x[q];
+        }
       } else {
         sum = part[row * ldp + t];
       }
@@ -428,14 +442,9 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
       largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
-    const int a = ts.id[row];
     if (lane == 0) {
       p.vmax[row0 + row] = largest;
       if (p.amax != nullptr && a >= 0) atomicMax(p.amax + a, __float_as_uint(largest));
-    }
-    if (p.w != nullptr && a >= 0) {
-      const float wm = warp_row_max(p.w + (row0 + row) * p.r, p.r);
-      if (lane == 0) atomicMax(p.w_amax + a, __float_as_uint(wm));
     }
   }
   if (p.split > 1) cluster_sync();  // no CTA leaves while its sums are read

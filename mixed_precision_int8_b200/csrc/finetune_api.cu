@@ -33,6 +33,7 @@ struct Device {
   bool supported = false;
   int sm_count = 0;
   int max_pairs = 0;  // CTA pairs of k_input_grad that fit at once
+  int shrink_split = 8;  // CTAs of a k_shrink cluster: 16 where the device runs such
 };
 Device g_device[kMaxDevices];
 std::mutex g_device_mutex;
@@ -85,6 +86,17 @@ llmint8_status current_device(Device **out) {
           clusters < 1)
         return LLMINT8_ERR_CUDA;
       d.max_pairs = std::min({clusters, d.sm_count / 2, igrad::MAX_PAIRS});
+      cfg.gridDim = dim3(lora::SH_MAX_SPLIT);
+      cfg.blockDim = dim3(lora::SH_THREADS);
+      cfg.dynamicSmemBytes = lora::SMEM_LIMIT;
+      attr[0].val.clusterDim.x = lora::SH_MAX_SPLIT;
+      if (cudaFuncSetAttribute(lora::k_shrink, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                               1) == cudaSuccess &&
+          cudaOccupancyMaxActiveClusters(&clusters, lora::k_shrink, &cfg) == cudaSuccess &&
+          clusters > 0)
+        d.shrink_split = lora::SH_MAX_SPLIT;
+      else
+        (void)cudaGetLastError();
     }
     d.init = true;
   }
@@ -221,12 +233,32 @@ llmint8_status enqueue_rows(const uint16_t *X, int64_t s, int64_t k, const uint1
   return LLMINT8_OK;
 }
 
-// The largest power of two up to `limit` CTAs per cluster that still leaves
-// each of `tiles` clusters an SM per CTA, or 1.
-int cluster_split(int64_t tiles, int64_t limit, int sm_count) {
-  int split = 1;
-  while (2 * split <= std::min<int64_t>(limit, lora::SH_MAX_SPLIT) && tiles * 2 * split <= sm_count) split *= 2;
-  return split;
+// How k_shrink's work is cut: CTAs of a cluster (over the features), clusters
+// of a row tile (over the passes that mixed rows take).
+struct ShrinkGrid {
+  int split, y;
+};
+
+// Powers of two up to 8 CTAs per cluster that leave every CTA its place, then
+// clusters for the passes, then clusters of 16 if there is still room (1000
+// rows of 16 adapters, rank 64, 12288 -> 12288: 87 us with 8 CTAs and one
+// cluster, 59 with 8 and 4, 64 with 16 and 2; 37 rows of one adapter, rank 64,
+// 11456 -> 1104: 21 us with 8, 17 with 16). A pass of fewer than eight stages
+// is over sooner than another cluster's start (221 rows of 5 adapters, rank
+// 16, 768 features: 31 us, 32.5 with 2).
+ShrinkGrid shrink_grid(int64_t s, int64_t k, const llmint8_adapters *ad, int n_jobs,
+                       const Device &dev) {
+  const int64_t room = (ad->r <= 64 ? 2 : 1) * dev.sm_count;  // two CTAs per SM up to r = 64
+  const int64_t tiles = n_jobs * ceil_div(s, lora::TM);
+  const int64_t limit = std::min<int64_t>(dev.shrink_split, ceil_div(k, 2 * lora::SH_KB));
+  ShrinkGrid g = {1, 1};
+  while (2 * g.split <= std::min<int64_t>(limit, 8) && tiles * 2 * g.split <= room) g.split *= 2;
+  const int64_t passes =
+      ceil_div(std::min<int64_t>(ad->n, lora::TM), lora::shrink_slots(ad->r));
+  if (ceil_div(k, lora::SH_KB) >= 8 * g.split)
+    g.y = (int)std::max<int64_t>(1, std::min(passes, room / (tiles * g.split)));
+  if (g.split == 8 && limit >= 16 && tiles * 16 * g.y <= room) g.split = 16;
+  return g;
 }
 
 // Shared memory of a CTA when an SM holds two.
@@ -268,18 +300,13 @@ bool shrink_job(lora::ShrinkJob *job, const uint16_t *X, int64_t s, int64_t k, c
                        (uint64_t)ad->n * ad->r, lora::SH_KB, (uint32_t)ad->r);
 }
 
-cudaError_t launch_shrink(const lora::ShrinkJob *jobs, int n_jobs, cudaStream_t st) {
+cudaError_t launch_shrink(const lora::ShrinkJob *jobs, int n_jobs, int y, cudaStream_t st) {
   const lora::ShrinkParams &p = jobs[0].p;
   const int64_t tiles = ceil_div(p.s, lora::TM);
   const uint32_t smem = lora::shrink_fixed_bytes(p.r) + p.stages * p.stage_bytes;
-  return launch_clusters(lora::k_shrink, dim3((unsigned)(tiles * p.split), 1, n_jobs),
+  return launch_clusters(lora::k_shrink, dim3((unsigned)(tiles * p.split), (unsigned)y, n_jobs),
                          dim3(lora::SH_THREADS), smem, st, p.split, false, jobs[0],
                          jobs[n_jobs - 1]);
-}
-
-int shrink_split(int64_t s, int64_t k, int32_t r, int n_jobs, int sm_count) {
-  return cluster_split(n_jobs * ceil_div(s, lora::TM), ceil_div(k, 2 * lora::SH_KB),
-                       r <= 64 ? 2 * sm_count : sm_count);
 }
 
 // out = base + scale * v . F
@@ -624,10 +651,11 @@ llmint8_status llmint8_adapters_forward(const uint16_t *X_dev, int64_t s,
   }
   float *v = v_dev ? v_dev : reinterpret_cast<float *>(wsb + L.v);
   float *vmax = reinterpret_cast<float *>(wsb + L.vmax);
+  const ShrinkGrid grid = shrink_grid(s, ad->h, ad, 1, *dev);
   lora::ShrinkJob job;
   if (!shrink_job(&job, X_dev, s, ad->h, ad->a_dev, ad, ids_dev, v, vmax, nullptr, nullptr,
-                  nullptr, shrink_split(s, ad->h, ad->r, 1, dev->sm_count), ws_dev) ||
-      launch_shrink(&job, 1, st) != cudaSuccess)
+                  nullptr, grid.split, ws_dev) ||
+      launch_shrink(&job, 1, grid.y, st) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   if ((rc = enqueue_expand(v, vmax, s, ad->o, ad->b_dev, ad, ids_dev, base_dev, out_dev, nullptr,
                            ws_dev, dev->sm_count, st)))
@@ -715,14 +743,14 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
   pack.info = info;
   int n_shrink = 0, n_outer = 0;
   const int want = (need_g ? 1 : 0) + (need_v ? 1 : 0);
-  const int split = std::min(shrink_split(s, ad->h, ad->r, want, dev->sm_count),
-                             shrink_split(s, ad->o, ad->r, want, dev->sm_count));
+  const int64_t width = !need_v ? ad->o : !need_g ? ad->h : std::min(ad->h, ad->o);
+  const ShrinkGrid grid = shrink_grid(s, width, ad, std::max(want, 1), *dev);
   if (need_g && !shrink_job(&shrink[n_shrink++], dY_dev, s, ad->o, ad->b_dev, ad, ids_dev, g, gmax,
-                            dA_dev ? g_amax : nullptr, own_v ? v_dev : nullptr, v_amax, split,
+                            dA_dev ? g_amax : nullptr, own_v ? v_dev : nullptr, v_amax, grid.split,
                             ws_dev))
     return LLMINT8_ERR_CUDA;
   if (need_v && !shrink_job(&shrink[n_shrink++], X_dev, s, ad->h, ad->a_dev, ad, ids_dev, v, vmax,
-                            v_amax, nullptr, nullptr, split, ws_dev))
+                            v_amax, nullptr, nullptr, grid.split, ws_dev))
     return LLMINT8_ERR_CUDA;
   if (dB_dev) {
     pack.job[n_outer] = {v_dev ? v_dev : v, v_amax, wsb + L.vpack};
@@ -739,7 +767,7 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
   if (n_outer > 0 && cudaMemsetAsync(v_amax, 0, 8 * (size_t)ad->n, st) != cudaSuccess)
     return LLMINT8_ERR_CUDA;
   if (n_shrink > 0) {
-    if (launch_shrink(shrink, n_shrink, st) != cudaSuccess) return LLMINT8_ERR_CUDA;
+    if (launch_shrink(shrink, n_shrink, grid.y, st) != cudaSuccess) return LLMINT8_ERR_CUDA;
   } else if (own_v && launch(lora::k_adapter_max, dim3((unsigned)ceil_div(s, 8)), dim3(256), 0, st,
                              false, v_dev, s, ad->n, ad->r, ids_dev, v_amax) != cudaSuccess) {
     return LLMINT8_ERR_CUDA;

@@ -137,6 +137,10 @@ CASES = [
     (513, 1040, 1296, 3, 64, "requests", "mixed"),
     (700, 272, 272, 2, 8, "none", "full"),
     (300, 272, 528, 5, 24, "wild", "full"),
+    # wide features: clusters of 16, and several that share a tile's adapters
+    (150, 8208, 528, 5, 24, "mixed", "mixed"),
+    (260, 528, 16400, 12, 128, "mixed", "mixed"),
+    (300, 16400, 8208, 7, 16, "requests_bare", "full"),
 ]
 
 
