@@ -194,10 +194,10 @@ __host__ __device__ inline int32_t shrink_cols(int32_t r) {
 __host__ __device__ inline uint32_t shrink_stage_bytes(int32_t r) {
   return SH_X_BYTES + (uint32_t)shrink_cols(r) * 128;
 }
-// partial sums [TM][r + 1], slots, barriers, alignment
-__host__ __device__ inline uint32_t shrink_fixed_bytes(int32_t r) {
-  return (uint32_t)(TM * (r + 1) * 4 + 15) / 16 * 16 + (uint32_t)sizeof(TileSlots) + 384 + 1024;
-}
+// slots, barriers, alignment (the partial sums [TM][r + 1] take the ring's place)
+constexpr uint32_t SH_FIXED_BYTES = (uint32_t)sizeof(TileSlots) + 16 + 384 + 1024;
+static_assert(SH_X_BYTES * 4 >= TM * (64 + 1) * 4 && SH_X_BYTES * 5 >= TM * (MAX_R + 1) * 4,
+              "partial sums in a ring of four or more stages");
 
 // Largest finite |x[t]|, t < r, over a warp.
 __device__ __forceinline__ float warp_row_max(const float *x, int r) {
@@ -212,7 +212,9 @@ __device__ __forceinline__ float warp_row_max(const float *x, int r) {
 // tiles leave SMs free, y clusters share the passes over the adapters of a tile
 // of mixed rows (150 rows of 16 adapters, rank 128, 12288 -> 512: 184 us with
 // one cluster per tile, 56 with 9).
-__global__ void __launch_bounds__(SH_THREADS, 2)
+// NC: octets of terms that a thread sums in registers (r <= 8 NC).
+template <int NC>
+__global__ void __launch_bounds__(SH_THREADS, NC <= 8 ? 2 : 1)
     k_shrink(const __grid_constant__ ShrinkJob j0, const __grid_constant__ ShrinkJob j1) {
   const ShrinkJob &job = blockIdx.z == 0 ? j0 : j1;
   const ShrinkParams &p = job.p;
@@ -221,8 +223,7 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
   uint8_t *base = smem_raw + pad;
   const uint32_t ring = smem_u32(base);
   const int ldp = p.r + 1;
-  float *part = reinterpret_cast<float *>(base + p.stages * p.stage_bytes);
-  uint8_t *after = reinterpret_cast<uint8_t *>(part) + (TM * ldp * 4 + 15) / 16 * 16;
+  uint8_t *after = base + p.stages * p.stage_bytes;
   TileSlots &ts = *reinterpret_cast<TileSlots *>(after);
   uint64_t *bars = reinterpret_cast<uint64_t *>(after + (sizeof(TileSlots) + 15) / 16 * 16);
   const uint32_t bar0 = smem_u32(bars);
@@ -274,6 +275,9 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
   tile_slots(p.ids, row0, p.s, p.n, p.rank, p.r, ts);  // ends with a barrier
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
+  float sums[NC * 8];  // epilogue warps: their row's v over this CTA's features
+#pragma unroll
+  for (int t = 0; t < NC * 8; ++t) sums[t] = 0.0f;
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------ TMA producer
@@ -363,9 +367,6 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
     // ----------------------------------- epilogue: this CTA's partial sums
     const int row = threadIdx.x - 128;
     const int slot = ts.slot[row];
-    const int rk = slot >= 0 ? ts.rank[slot] : 0;
-    float *mine = part + row * ldp;
-    for (int t = 0; t < p.r; ++t) mine[t] = 0.0f;
     int acc = 0;
     uint32_t aphase = 0;
     bool ok = true;
@@ -379,16 +380,15 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
         const uint32_t src = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc * p.cols;
         for (int32_t sl = s0; sl < s1; ++sl) {
           if (!__any_sync(0xffffffffu, slot == sl)) continue;
-          for (int c = 0; c < p.r; c += 8) {
-            uint32_t v[8];
-            tmem_ld_32x32b_x8(src + (uint32_t)((sl - s0) * p.r + c), v);
-            tmem_ld_wait();
-            if (slot == sl) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (c + e < rk) mine[c + e] += __uint_as_float(v[e]);
-            }
-            __syncwarp();
+          for (int c = 0; c < NC; ++c) {
+            if (c * 8 >= p.r) break;
+            uint32_t v[8];
+            tmem_ld_32x32b_x8(src + (uint32_t)((sl - s0) * p.r + c * 8), v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              sums[c * 8 + e] += slot == sl ? __uint_as_float(v[e]) : 0.0f;
           }
         }
         tc_fence_before();
@@ -405,6 +405,17 @@ __global__ void __launch_bounds__(SH_THREADS, 2)
   __syncthreads();
   tc_fence_after();
   if (warp == 2) tmem_dealloc(tmem, p.tmem_cols);
+  // the partial sums over the ring's memory (its copies have landed, its
+  // products are done)
+  float *part = reinterpret_cast<float *>(base);
+  if (warp >= 4) {
+    const int row = threadIdx.x - 128, slot = ts.slot[row];
+    const int rk = slot >= 0 ? ts.rank[slot] : 0;
+#pragma unroll
+    for (int t = 0; t < NC * 8; ++t)
+      if (t < p.r) part[row * ldp + t] = t < rk ? sums[t] : 0.0f;
+  }
+  __syncthreads();
   // the cluster's partial sums, in rank order; this CTA finishes TM / split rows
   if (p.split > 1) cluster_sync();
   const int rows = TM / p.split;

@@ -28,6 +28,19 @@ using namespace llmint8;
 template <typename TX, typename TP>
 bool ln_backward_setup();
 
+auto shrink_kernel(int32_t r) {
+  return r <= 16   ? lora::k_shrink<2>
+         : r <= 32 ? lora::k_shrink<4>
+         : r <= 64 ? lora::k_shrink<8>
+                   : lora::k_shrink<16>;
+}
+
+bool shrink_setup(cudaFuncAttribute attr, int value) {
+  for (int32_t r : {16, 32, 64, 128})
+    if (cudaFuncSetAttribute(shrink_kernel(r), attr, value) != cudaSuccess) return false;
+  return true;
+}
+
 struct Device {
   bool init = false;
   bool supported = false;
@@ -55,8 +68,7 @@ llmint8_status current_device(Device **out) {
                                (int)igrad::Smem<1>::BYTES) != cudaSuccess ||
           cudaFuncSetAttribute(igrad::k_input_grad<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)igrad::Smem<2>::BYTES) != cudaSuccess ||
-          cudaFuncSetAttribute(lora::k_shrink, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)lora::SMEM_LIMIT) != cudaSuccess ||
+          !shrink_setup(cudaFuncAttributeMaxDynamicSharedMemorySize, (int)lora::SMEM_LIMIT) ||
           cudaFuncSetAttribute(lora::k_expand, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)lora::SMEM_LIMIT) != cudaSuccess ||
           cudaFuncSetAttribute(lora::k_outer<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -90,9 +102,8 @@ llmint8_status current_device(Device **out) {
       cfg.blockDim = dim3(lora::SH_THREADS);
       cfg.dynamicSmemBytes = lora::SMEM_LIMIT;
       attr[0].val.clusterDim.x = lora::SH_MAX_SPLIT;
-      if (cudaFuncSetAttribute(lora::k_shrink, cudaFuncAttributeNonPortableClusterSizeAllowed,
-                               1) == cudaSuccess &&
-          cudaOccupancyMaxActiveClusters(&clusters, lora::k_shrink, &cfg) == cudaSuccess &&
+      if (shrink_setup(cudaFuncAttributeNonPortableClusterSizeAllowed, 1) &&
+          cudaOccupancyMaxActiveClusters(&clusters, lora::k_shrink<16>, &cfg) == cudaSuccess &&
           clusters > 0)
         d.shrink_split = lora::SH_MAX_SPLIT;
       else
@@ -277,11 +288,11 @@ bool shrink_job(lora::ShrinkJob *job, const uint16_t *X, int64_t s, int64_t k, c
   p.split = split;
   p.slots = lora::shrink_slots(ad->r);
   p.stage_bytes = lora::shrink_stage_bytes(ad->r);
-  // two CTAs per SM (three stages at least in half of its shared memory) up
-  // to r = 64, one above
+  // two CTAs per SM (four stages in half of its shared memory) up to r = 64,
+  // one above
   const uint32_t limit = ad->r <= 64 ? kHalfSmem : lora::SMEM_LIMIT;
-  p.stages = (int32_t)std::min<uint32_t>(
-      lora::SH_MAX_STAGES, (limit - lora::shrink_fixed_bytes(ad->r)) / p.stage_bytes);
+  p.stages = (int32_t)std::min<uint32_t>(lora::SH_MAX_STAGES,
+                                         (limit - lora::SH_FIXED_BYTES) / p.stage_bytes);
   p.cols = lora::shrink_cols(ad->r);
   p.tmem_cols = 256;
   p.accs = std::min(lora::SH_MAX_ACC, p.tmem_cols / p.cols);
@@ -303,8 +314,8 @@ bool shrink_job(lora::ShrinkJob *job, const uint16_t *X, int64_t s, int64_t k, c
 cudaError_t launch_shrink(const lora::ShrinkJob *jobs, int n_jobs, int y, cudaStream_t st) {
   const lora::ShrinkParams &p = jobs[0].p;
   const int64_t tiles = ceil_div(p.s, lora::TM);
-  const uint32_t smem = lora::shrink_fixed_bytes(p.r) + p.stages * p.stage_bytes;
-  return launch_clusters(lora::k_shrink, dim3((unsigned)(tiles * p.split), (unsigned)y, n_jobs),
+  const uint32_t smem = lora::SH_FIXED_BYTES + p.stages * p.stage_bytes;
+  return launch_clusters(shrink_kernel(p.r), dim3((unsigned)(tiles * p.split), (unsigned)y, n_jobs),
                          dim3(lora::SH_THREADS), smem, st, p.split, false, jobs[0],
                          jobs[n_jobs - 1]);
 }
