@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(256)
 
 // -------------------------------------------------------------------- k_pack
 
-constexpr int OU_KB = 64;                 // rows of a block
+constexpr int OU_KB = 64;                 // rows of a block; 32: 121 us instead of 116 for the
+                                          // backward pass of 4096 x 20480 at rank 64
 constexpr uint32_t OU_CORE = OU_KB * 16;  // 8 terms of 64 rows
 
 // r rounded up to 16: columns of a product
