@@ -41,6 +41,25 @@ bool shrink_setup(cudaFuncAttribute attr, int value) {
   return true;
 }
 
+auto input_grad_kernel(int32_t mt, bool base) {
+  return mt == 1 ? (base ? igrad::k_input_grad<1, true> : igrad::k_input_grad<1, false>)
+                 : (base ? igrad::k_input_grad<2, true> : igrad::k_input_grad<2, false>);
+}
+
+size_t input_grad_smem(int32_t mt) {
+  return mt == 1 ? igrad::Smem<1>::BYTES : igrad::Smem<2>::BYTES;
+}
+
+bool input_grad_setup() {
+  for (int32_t mt : {1, 2})
+    for (bool base : {false, true})
+      if (cudaFuncSetAttribute(input_grad_kernel(mt, base),
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)input_grad_smem(mt)) != cudaSuccess)
+        return false;
+  return true;
+}
+
 struct Device {
   bool init = false;
   bool supported = false;
@@ -64,10 +83,7 @@ llmint8_status current_device(Device **out) {
       return LLMINT8_ERR_CUDA;
     d.supported = major == 10 && minor == 0;
     if (d.supported) {
-      if (cudaFuncSetAttribute(igrad::k_input_grad<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)igrad::Smem<1>::BYTES) != cudaSuccess ||
-          cudaFuncSetAttribute(igrad::k_input_grad<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)igrad::Smem<2>::BYTES) != cudaSuccess ||
+      if (!input_grad_setup() ||
           !shrink_setup(cudaFuncAttributeMaxDynamicSharedMemorySize, (int)lora::SMEM_LIMIT) ||
           cudaFuncSetAttribute(lora::k_expand, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)lora::SMEM_LIMIT) != cudaSuccess ||
@@ -94,7 +110,7 @@ llmint8_status current_device(Device **out) {
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       int clusters = 0;
-      if (cudaOccupancyMaxActiveClusters(&clusters, igrad::k_input_grad<2>, &cfg) != cudaSuccess ||
+      if (cudaOccupancyMaxActiveClusters(&clusters, igrad::k_input_grad<2, true>, &cfg) != cudaSuccess ||
           clusters < 1)
         return LLMINT8_ERR_CUDA;
       d.max_pairs = std::min({clusters, d.sm_count / 2, igrad::MAX_PAIRS});
@@ -855,12 +871,11 @@ llmint8_status llmint8_matmul_backward(const uint16_t *dY_dev, int64_t s, const 
   cudaStream_t st = as_stream(stream);
   const int64_t units = plan.whole + (int64_t)plan.rest * plan.parts;
   const unsigned ctas = 2 * (unsigned)std::min<int64_t>(units, dev->max_pairs);
-  const cudaError_t e =
-      plan.mt == 1 ? launch_pairs(igrad::k_input_grad<1>, dim3(ctas), dim3(igrad::NUM_THREADS),
-                                  igrad::Smem<1>::BYTES, st, false, tmA, tmW, p)
-                   : launch_pairs(igrad::k_input_grad<2>, dim3(ctas), dim3(igrad::NUM_THREADS),
-                                  igrad::Smem<2>::BYTES, st, false, tmA, tmW, p);
-  if (e != cudaSuccess) return LLMINT8_ERR_CUDA;
+  // (with parts, the base of the tiles cut is added by their sum)
+  if (launch_pairs(input_grad_kernel(plan.mt, base_dev != nullptr), dim3(ctas),
+                   dim3(igrad::NUM_THREADS), input_grad_smem(plan.mt), st, false, tmA, tmW,
+                   p) != cudaSuccess)
+    return LLMINT8_ERR_CUDA;
   if (plan.parts > 1 &&
       launch(igrad::k_input_grad_sum,
              dim3(blocks_for((int64_t)plan.rest * plan.mt * 2 * igrad::BM * (igrad::BN / 8),

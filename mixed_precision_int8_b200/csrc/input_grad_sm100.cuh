@@ -182,7 +182,29 @@ __device__ __forceinline__ uint2 codes_to_half(uint32_t w, const Factor &f) {
                     scale_pair(prmt(x, 0x64646464u, 0x4342), f));
 }
 
-template <int MT>
+// Item i of lane j of every four lanes becomes item j of lane i.
+__device__ __forceinline__ void quad_transpose(uint4 (&t)[4], int lane) {
+#pragma unroll
+  for (int bit = 1; bit < 4; bit *= 2) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int lo = 0; lo < 4; ++lo) {
+      if (lo & bit) continue;
+      uint4 &a = t[lo], &b = t[lo + bit];
+      uint4 m = up ? a : b;
+      m.x = __shfl_xor_sync(0xffffffffu, m.x, bit);
+      m.y = __shfl_xor_sync(0xffffffffu, m.y, bit);
+      m.z = __shfl_xor_sync(0xffffffffu, m.z, bit);
+      m.w = __shfl_xor_sync(0xffffffffu, m.w, bit);
+      a = up ? m : a;
+      b = up ? b : m;
+    }
+  }
+}
+
+// BASE: whether another gradient is added (p.base; its registers would cost the
+// kernel without one spills).
+template <int MT, bool BASE>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     k_input_grad(const __grid_constant__ CUtensorMap tmA,
                  const __grid_constant__ CUtensorMap tmW, const Params p) {
@@ -386,9 +408,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             __syncwarp();
             tmem_ld_32x32b_x32(t_row + c * 32, v);
             tmem_ld_wait();
-            if (row >= p.s) continue;
+            if (row - lane >= p.s || j0 >= p.h) continue;  // (the whole warp)
             if (u.slot >= 0) {
-              if (j0 >= p.h) continue;
+              if (row >= p.s) continue;
               float4 *dst =
                   reinterpret_cast<float4 *>(p.part) +
                   part_quad(((size_t)u.slot * MT + b) * (2 * BM) + in_block, c * 8);
@@ -399,24 +421,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
               continue;
             }
+            // h is a multiple of 16: 8 columns are all inside or all outside
+            if constexpr (!BASE) {
+#pragma unroll
+              for (int q8 = 0; q8 < 4; ++q8) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * q8 + e]);
+                if (row < p.s && j0 + 8 * q8 < p.h)
+                  store8(p.out + (int64_t)row * p.h + j0 + 8 * q8, f);
+              }
+              continue;
+            }
+            // with a base to read, four lanes' rows change places with their
+            // octets, so that four lanes load and store 64 bytes of one row
+            // (4096 rows, 4096 x 1024: 78 us instead of 98; stores alone gain
+            // nothing from it)
+            const int32_t quad = row - (lane & 3), col = j0 + 8 * (lane & 3);
+            uint4 t[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              t[q] = make_uint4(0u, 0u, 0u, 0u);
+              if (quad + q < p.s && col < p.h)
+                t[q] = *reinterpret_cast<const uint4 *>(p.base + (int64_t)(quad + q) * p.h + col);
+            }
+            quad_transpose(t, lane);
 #pragma unroll
             for (int q8 = 0; q8 < 4; ++q8) {
-              // h is a multiple of 16: 8 columns are all inside or all outside
-              const int32_t j = j0 + 8 * q8;
-              if (j >= p.h) continue;
+              Vec8<__half> bv;
+              bv.q = t[q8];
               float f[8];
+              bv.get(f);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * q8 + e]);
-              if (p.base) {
-                Vec8<__half> bv;
-                bv.load(p.base + (int64_t)row * p.h + j);
-                float bf[8];
-                bv.get(bf);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] += bf[e];
-              }
-              store8(p.out + (int64_t)row * p.h + j, f);
+              for (int e = 0; e < 8; ++e) f[e] += __uint_as_float(v[8 * q8 + e]);
+              t[q8] = pack8(f);
             }
+            quad_transpose(t, lane);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (quad + q < p.s && col < p.h)
+                *reinterpret_cast<uint4 *>(p.out + (int64_t)(quad + q) * p.h + col) = t[q];
           }
         }
         __syncwarp();

@@ -43,14 +43,18 @@ struct Vec8<float> {
   }
 };
 
-__device__ __forceinline__ void store8(__half *p, const float (&f)[8]) {
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t *>(&v);
   }
-  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void store8(__half *p, const float (&f)[8]) {
+  *reinterpret_cast<uint4 *>(p) = pack8(f);
 }
 
 __device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
