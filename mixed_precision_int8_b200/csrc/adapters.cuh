@@ -40,10 +40,10 @@ __device__ __forceinline__ int rank_of(const int32_t *rank, int a, int r) {
 // k_rows_shrink leaves one partial sum of v per slice; k_rows_expand, launched
 // as its programmatic dependent, has its first factor rows in registers before
 // it waits for them. Against the tensor-core kernels, which multiply a whole
-// tile of rows with every adapter in it (forward, 12288 -> 20480, rank 64):
-// 64 rows of 64 adapters 64 us instead of 832, 128 of 64 104 instead of 840;
-// rows of one adapter, which those kernels suit best, 35 instead of 31 at 64
-// rows and 55 instead of 33 at 128.
+// tile of rows with every adapter in it (forward, 12288 -> 20480, rank 64): 64
+// rows of 64 adapters 48 us instead of 178, 128 of 64 68 instead of 184; rows
+// of one adapter, which those kernels suit best, 25 instead of 19 at 64 rows
+// and 45 instead of 21 at 128.
 
 constexpr int RS_SLICE = 512;       // features of a k_rows_shrink block
 constexpr int RS_THREADS = 256;

@@ -173,17 +173,24 @@ bool overlaps_partly(Span out, Span in) {
 
 // ------------------------------------------------------------- adapters
 
-// The row kernels (adapters.cuh) take batches of at most one tile of rows, and
-// of 32 rows per adapter held: what the tensor-core kernels lose is a pass per
-// adapter in a tile, so the fewer there can be, the sooner they win (one
-// adapter, backward, 12288 -> 20480, rank 64: rows 38 against 54 us at 32 rows,
-// 58 against 54 at 64; sixteen: 107 against 447 at 128). Widths leave at most
-// kRowMaxSlices partial sums of a row.
+// The row kernels (adapters.cuh) take batches of at most one tile of rows while
+// their work, s r (h + o), is small: it costs them time in proportion, and the
+// tensor-core kernels, whose time it hardly changes, a pass per adapter held.
+// Backward they also sum an adapter's rows one after another. Rows against
+// tensor cores, us: 12288 -> 20480, rank 64, forward, one adapter 15 against 17
+// at 32 rows, 22 against 18 at 48; four 22 against 25 at 48, 35 against 27 at
+// 96; sixteen 54 against 62 at 128; backward, one 34 against 37 at 48, 43
+// against 37 at 64; four 56 against 58 at 96, 71 against 57 at 128. 4096 ->
+// 4096, rank 16, one adapter at 128 rows: forward 7 against 12, backward 27
+// against 21 (17 against 18 at 64). Widths leave at most kRowMaxSlices partial
+// sums of a row.
 constexpr int64_t kRowMaxSlices = 256;
 
-bool use_row_kernels(int64_t s, const llmint8_adapters *ad) {
-  return s <= std::min<int64_t>(lora::RO_MAX_ROWS, 32 * (int64_t)ad->n) &&
-         std::max(ad->h, ad->o) <= kRowMaxSlices * lora::RS_SLICE;
+bool use_row_kernels(int64_t s, const llmint8_adapters *ad, bool backward) {
+  if (s > lora::RO_MAX_ROWS || std::max(ad->h, ad->o) > kRowMaxSlices * lora::RS_SLICE)
+    return false;
+  const int64_t n = ad->n, work = s * ad->r * (ad->h + ad->o);
+  return backward ? s <= 64 * n && work <= (80 + 24 * n) << 20 : work <= (64 + 16 * n) << 20;
 }
 
 struct AdapterLayout {
@@ -670,7 +677,7 @@ llmint8_status llmint8_adapters_forward(const uint16_t *X_dev, int64_t s,
   if ((rc = current_device(&dev))) return rc;
   cudaStream_t st = as_stream(stream);
   uint8_t *wsb = static_cast<uint8_t *>(ws_dev);
-  if (use_row_kernels(s, ad)) {
+  if (use_row_kernels(s, ad, false)) {
     if ((rc = enqueue_rows(X_dev, s, ad->h, ad->a_dev, ad->o, ad->b_dev, ad, ids_dev, base_dev,
                            out_dev, v_dev, reinterpret_cast<float *>(wsb + L.part), st)))
       return rc;
@@ -731,7 +738,7 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
   float *gmax = reinterpret_cast<float *>(wsb + L.gmax);
   uint32_t *v_amax = reinterpret_cast<uint32_t *>(wsb + L.amax), *g_amax = v_amax + ad->n;
   const bool need_g = dX_dev || dA_dev;
-  if (use_row_kernels(s, ad)) {
+  if (use_row_kernels(s, ad, true)) {
     float *part = reinterpret_cast<float *>(wsb + L.part);
     if (need_v && (rc = enqueue_rows(X_dev, s, ad->h, ad->a_dev, ad->o, ad->b_dev, ad, ids_dev,
                                      nullptr, nullptr, v, part, st)))

@@ -114,9 +114,8 @@ def bits(t):
     return t.view(torch.int16)
 
 
-# sizes: one row, the row kernels' limits (32 rows per adapter held, 128 in
-# all), tiles of 128 rows and the rows
-# around their edges, widths that end inside a tile, ranks that are no
+# sizes: one row, the row kernels' limits (128 rows, the work, backward 64 rows
+# per adapter held), tiles of 128 rows and the rows around their edges, widths that end inside a tile, ranks that are no
 # multiple of 16, more adapters in a tile than accumulators
 CASES = [
     (1, 16, 16, 1, 8, "requests", "full"),
@@ -131,6 +130,10 @@ CASES = [
     (128, 528, 784, 40, 24, "mixed", "mixed"),
     (65, 528, 512, 2, 40, "requests", "full"),
     (128, 2064, 784, 2, 16, "requests_bare", "mixed"),
+    (64, 528, 784, 1, 24, "requests", "full"),
+    (65, 528, 784, 1, 24, "requests", "full"),
+    (70, 12288, 16400, 1, 64, "mixed", "mixed"),
+    (127, 16400, 12288, 2, 64, "requests", "full"),
     (129, 784, 2064, 2, 16, "requests", "full"),
     (200, 1024, 784, 150, 64, "mixed", "mixed"),
     (300, 528, 272, 4, 128, "requests_bare", "full"),
