@@ -437,7 +437,7 @@ cudaError_t launch_outer(lora::OuterJob *jobs, int n_jobs, int sm_count, cudaStr
   for (int i = 0; i < n_jobs; ++i) tiles += jobs[i].p.col_tiles;
   // the fewest rounds for their length (a CTA's start and end counted as
   // twelve blocks: at 4096 rows of 5120 and 20480 features and rank 64 a split
-  // of 2 takes 133 us in all, 3 149, 4 143, 5 138)
+  // of 2 takes 116 us in all, 3 135, 4 128, 5 123)
   const lora::OuterParams &p = jobs[0].p;
   const int64_t blocks = ceil_div(p.s, lora::OU_KB);
   const int64_t room = p.r <= 64 ? 2 * sm_count : sm_count;
