@@ -532,3 +532,83 @@ def test_input_gradient_recovers_weights_of_any_size():
 def test_input_gradient_no_rows():
     w, dY, _, _ = backward_case(4, 272, 528)
     assert L.llmint8_matmul_backward(dY[:0], w).shape == (0, 272)
+
+
+# More units of work than CTA pairs (74): pairs that take a second and a third
+# unit, on one accumulator after the other (up to 256 rows) or on both at once,
+# with odd numbers of stages between them; whole tiles alone, with others
+# behind them, and with others cut along the reduction; parts on every pair
+MANY_UNITS = [(131, 19216, 272), (200, 18944, 336), (150, 42000, 272), (200, 10256, 4112),
+              (4353, 2576, 1296), (4353, 4112, 272), (513, 14208, 208), (1537, 12304, 144),
+              (1025, 37888, 80)]
+
+
+@pytest.mark.parametrize("s,h,o", MANY_UNITS)
+def test_input_gradient_of_many_units_exact(s, h, o):
+    test_input_gradient_exact(s, h, o)
+
+
+@pytest.mark.parametrize("s,h,o", [(131, 19216, 272), (4353, 2576, 1296)])
+def test_input_gradient_of_many_units_repeats_itself(s, h, o):
+    """The same bits from every one of many calls, with normal values, on one
+    workspace, and next to another stream's calls."""
+    g = torch.Generator(device="cuda").manual_seed(h)
+    W = (torch.randn(h, o, generator=g, device="cuda") * 0.02).half()
+    pw = L.llmint8_prepare_weight(W)
+    dY = (torch.randn(s, o, generator=g, device="cuda") * 0.1).half()
+    base = torch.randn(s, h, generator=g, device="cuda").half()
+    ws, other_ws = L.BackwardWorkspace(s, h, o), L.BackwardWorkspace(s, h, o)
+    first = L.llmint8_matmul_backward(dY, pw, base=base, workspace=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(50):
+        other = L.llmint8_matmul_backward(dY, pw, base=base, workspace=other_ws, stream=side)
+        assert torch.equal(bits(L.llmint8_matmul_backward(dY, pw, base=base, workspace=ws)),
+                           bits(first))
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(bits(other), bits(first))
+        side.wait_stream(torch.cuda.current_stream())
+    for w in (ws, other_ws):
+        assert L.llmint8_read_device_status(w) == 0
+
+
+def test_input_gradient_of_a_row_with_an_infinity_repeats_itself():
+    """That row's values repeat themselves too, its NaN in the same places."""
+    s, h, o = 300, 1040, 2064
+    g = torch.Generator(device="cuda").manual_seed(4)
+    pw = L.llmint8_prepare_weight((torch.randn(h, o, generator=g, device="cuda") * 0.02).half())
+    dY = (torch.randn(s, o, generator=g, device="cuda") * 0.1).half()
+    dY[0, 3] = float("inf")
+    got, again = (L.llmint8_matmul_backward(dY, pw) for _ in range(2))
+    assert torch.equal(got.isnan(), again.isnan())
+    assert torch.equal(got.nan_to_num(0.5), again.nan_to_num(0.5))
+    # inf times the recovered weight: its sign, or NaN where the code is zero
+    codes = pw.wq[3].int()
+    assert (got[0].isnan() == (codes == 0)).all()
+    assert torch.equal(got[0][codes != 0], codes[codes != 0].sign() * torch.tensor(
+        float("inf"), dtype=torch.float16, device="cuda"))
+
+
+@pytest.mark.parametrize("s,h,o", [(77, 1040, 49152), (520, 528, 49152)])
+@pytest.mark.parametrize("sign", ["mixed", "positive"])
+def test_input_gradient_of_a_long_reduction(s, h, o, sign):
+    """49152 products per sum. On the tensor cores a sum is rounded toward zero
+    once per 16 of them, each time by at most 2^-23 of a partial sum, and where
+    it is cut into parts (at most 16) once more for each: together below
+    (o / 16 + 16) 2^-23 of the largest partial sum, which is the result itself
+    where every term is positive and at most |dY| |WR| else."""
+    g = torch.Generator(device="cuda").manual_seed(s)
+    wq = torch.randint(-127, 128, (o, h), generator=g, device="cuda").to(torch.int8)
+    aw = (0.08 + 0.01 * torch.rand(o, generator=g, device="cuda")).half().float()
+    dY = (torch.randn(s, o, generator=g, device="cuda") * 0.01).half()
+    if sign == "positive":
+        wq, dY = wq.abs(), dY.abs()
+    got = L.llmint8_matmul_backward(dY, L.PreparedWeight(wq, aw)).double()
+    WR = (wq.float() * (aw[:, None] / 127)).half().double()
+    ref = dY.double() @ WR
+    lim = 2.0 ** -11 * ref.abs() + 2.0 ** -25
+    if sign == "positive":
+        lim += (o / 16 + 16) * 2.0 ** -23 * ref
+    else:
+        lim += (o / 16 + 16) * 2.0 ** -23 * dY.double().norm(dim=1)[:, None] * WR.norm(dim=0)
+    assert ((got - ref).abs() <= lim).all()
