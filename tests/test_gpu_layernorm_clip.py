@@ -297,3 +297,23 @@ def test_norm_layer_and_clip_on_a_stream_and_in_a_graph():
         got = [t.clone() for t in held] + [g.clone() for g in grads]
         for a, b in zip(got, list(step()) + grads):
             assert torch.equal(a, b)
+
+
+# Backward, more groups of rows per block than its ring has stages (so that
+# slots are taken again, their phases flipped) and two rows per stage, with a
+# last group of one row: at 148 SMs every shape but the 1201 rows is of the
+# first kind, all with h <= 4096 in fp16 and those of 528 and 16 columns in
+# fp32 too of the second
+REFILLS = [(2047, 4096), (1201, 528), (8001, 528), (700, 12288), (1501, 16384), (20001, 16),
+           (1777, 8192)]
+
+
+@pytest.mark.parametrize("s,h", REFILLS)
+@pytest.mark.parametrize("xt,pt", TYPES)
+def test_layernorm_of_many_rows(s, h, xt, pt):
+    test_layernorm(s, h, xt, pt)
+
+
+@pytest.mark.parametrize("s,h", [(2047, 4096), (8001, 528), (1777, 8192), (1501, 16384)])
+def test_layernorm_of_many_rows_in_place(s, h):
+    test_layernorm_in_place(s, h)
