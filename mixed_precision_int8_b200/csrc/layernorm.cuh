@@ -15,7 +15,8 @@
 // Bound: bytes. A row is read once and kept in registers (forward; NV vectors
 // of eight elements per thread) or shared memory (backward) between the sums
 // and the store; rows too long for that are re-read from L2 by the *_long
-// kernels.
+// kernels. y may be x, and dx may be x or dy: a thread reads an element before
+// it writes it, and none of these pointers is __restrict__.
 #pragma once
 
 #include <cstdint>
@@ -32,8 +33,8 @@ constexpr int64_t MAX_ROW = 8LL * MAX_VEC * MAX_THREADS;  // longest row held in
 
 template <typename TX, typename TP, int NV>
 __global__ void __launch_bounds__(MAX_THREADS)
-    k_ln_forward(const TX *__restrict__ x, int32_t h, const TP *__restrict__ gamma,
-                 const TP *__restrict__ beta, float eps, __half *__restrict__ y,
+    k_ln_forward(const TX *x, int32_t h, const TP *__restrict__ gamma,
+                 const TP *__restrict__ beta, float eps, __half *y,
                  float *__restrict__ mean_out, float *__restrict__ rstd_out) {
   __shared__ float red[2][32];
   const int64_t row = blockIdx.x;
@@ -92,8 +93,8 @@ __global__ void __launch_bounds__(MAX_THREADS)
 // Rows longer than MAX_ROW: the same sums with the row read three times.
 template <typename TX, typename TP>
 __global__ void __launch_bounds__(MAX_THREADS)
-    k_ln_forward_long(const TX *__restrict__ x, int32_t h, const TP *__restrict__ gamma,
-                      const TP *__restrict__ beta, float eps, __half *__restrict__ y,
+    k_ln_forward_long(const TX *x, int32_t h, const TP *__restrict__ gamma,
+                      const TP *__restrict__ beta, float eps, __half *y,
                       float *__restrict__ mean_out, float *__restrict__ rstd_out) {
   __shared__ float red[2][32];
   const int64_t row = blockIdx.x;
@@ -188,9 +189,9 @@ __device__ __forceinline__ void store_pairs(float *p, const uint64_t *f, int pai
 
 template <typename TX, typename TP, int NU, int RB>
 __global__ void __launch_bounds__(MAX_THREADS, NU * (int)(16 / sizeof(TX)) <= 8 ? 2 : 1)
-    k_ln_backward(const __half *__restrict__ dy, const TX *__restrict__ x, int64_t s, int32_t h,
+    k_ln_backward(const __half *dy, const TX *x, int64_t s, int32_t h,
                   int32_t stages, const TP *__restrict__ gamma, const float *__restrict__ mean,
-                  const float *__restrict__ rstd, TX *__restrict__ dx, float *__restrict__ part,
+                  const float *__restrict__ rstd, TX *dx, float *__restrict__ part,
                   int32_t *status, uint64_t timeout_ns) {
   constexpr int U = 16 / (int)sizeof(TX), P = U / 2;
   extern __shared__ __align__(128) uint8_t ring[];
@@ -356,9 +357,9 @@ __global__ void __launch_bounds__(MAX_THREADS, NU * (int)(16 / sizeof(TX)) <= 8 
 // this block's slice of `part`.
 template <typename TX, typename TP>
 __global__ void __launch_bounds__(MAX_THREADS)
-    k_ln_backward_long(const __half *__restrict__ dy, const TX *__restrict__ x, int64_t s,
+    k_ln_backward_long(const __half *dy, const TX *x, int64_t s,
                        int32_t h, const TP *__restrict__ gamma, const float *__restrict__ mean,
-                       const float *__restrict__ rstd, TX *__restrict__ dx,
+                       const float *__restrict__ rstd, TX *dx,
                        float *__restrict__ part) {
   __shared__ float2 red[2][32];
   const int nvec = h >> 3;
