@@ -94,8 +94,10 @@ __global__ void __launch_bounds__(RS_THREADS)
 
 // out[i][8c..] = base + scale * sum_t v[i][t] * F[a][t][8c..]; v itself to
 // v_out (or null). out may be null: v alone. Grid (slices of out, s).
+// (part is k_rows_shrink's, which may still run when this kernel starts: not
+// __restrict__, so that no read of it can move before the wait.)
 __global__ void __launch_bounds__(RE_THREADS)
-    k_rows_expand(const float *__restrict__ part, int32_t slices, int32_t s, int32_t o,
+    k_rows_expand(const float *part, int32_t slices, int32_t s, int32_t o,
                   const __half *__restrict__ F, const int32_t *__restrict__ ids,
                   const float *__restrict__ scale, const int32_t *__restrict__ rank, int32_t n,
                   int32_t r, const __half *base, __half *out, float *__restrict__ v_out) {

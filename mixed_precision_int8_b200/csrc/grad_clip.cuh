@@ -220,9 +220,11 @@ __global__ void __launch_bounds__(THREADS)
   }
 }
 
+// (partial is still being written when this kernel starts: not __restrict__, so
+// that no read of it can move before the wait.)
 __global__ void __launch_bounds__(THREADS)
     k_clip_scale(const Entry *__restrict__ table, int64_t n, int64_t chunks,
-                 const int32_t *__restrict__ starts, const double *__restrict__ partial,
+                 const int32_t *__restrict__ starts, const double *partial,
                  int32_t n_partial, float max_norm, float *__restrict__ norm_out) {
   __shared__ double red[32];
   __shared__ float s_coef;

@@ -428,10 +428,12 @@ __global__ void __launch_bounds__(MAX_THREADS)
 
 // dgamma / dbeta = the blocks' partial sums, added in a fixed order: 32
 // threads of four columns each by 32 lanes of blocks, then the lanes in order.
+// (part is still being written when this kernel starts: not __restrict__, so
+// that no read of it can move before the wait.)
 constexpr int RED_COLS = 128;
 constexpr int RED_LANES = 32;
 __global__ void __launch_bounds__(RED_COLS / 4 * RED_LANES)
-    k_ln_reduce(const float *__restrict__ part, int32_t blocks, int32_t h,
+    k_ln_reduce(const float *part, int32_t blocks, int32_t h,
                 float *__restrict__ dgamma, float *__restrict__ dbeta) {
   __shared__ float4 sums[RED_LANES][RED_COLS / 4];
   grid_dependency_wait();

@@ -1,5 +1,6 @@
 """What the kernels' sources promise the compiler, read from their signatures:
-no `__restrict__` on a pointer that a documented call may alias."""
+no `__restrict__` on a pointer that a documented call may alias, or whose data
+the preceding grid still writes when the kernel starts."""
 import os
 import re
 
@@ -33,3 +34,16 @@ def test_pointers_that_may_be_the_same_are_not_restrict(source, kernel, names):
     params = signature(source, kernel)
     for name in names:
         assert "*" in params[name] and "__restrict__" not in params[name], params[name]
+
+
+# what the preceding grid still writes while a programmatic dependent starts:
+# a read through `const __restrict__` may take the read-only path, or move
+# before the wait for that grid
+WRITTEN_BY_THE_PRECEDING_GRID = [("adapters.cuh", "k_rows_expand", ("part",)),
+                                 ("layernorm.cuh", "k_ln_reduce", ("part",)),
+                                 ("grad_clip.cuh", "k_clip_scale", ("partial",))]
+
+
+@pytest.mark.parametrize("source,kernel,names", WRITTEN_BY_THE_PRECEDING_GRID)
+def test_results_of_a_grid_still_running_are_not_restrict(source, kernel, names):
+    test_pointers_that_may_be_the_same_are_not_restrict(source, kernel, names)
