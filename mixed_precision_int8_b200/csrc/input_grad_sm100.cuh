@@ -20,9 +20,12 @@
 // 772 -> 679 us. Two groups of eight warps convert alternate stages: TMA brings
 // the codes and their column scales into a ring of their own, a lane takes 16
 // codes of it and writes 16 fp16 values through the 128-byte swizzle, 11
-// instructions for four codes. Their signal to the issuing CTA is an arrival at
-// the default scope (mbar_arrive_remote): one with cluster-scope release waits
-// for a round trip to L2 in every stage (1238 us instead of 777 with MT = 1).
+// instructions for four codes. Their signal to the issuing CTA releases, at
+// cluster scope, what they wrote to shared memory and nothing else
+// (mbar_arrive_smem): a release of all memory waits for a round trip to L2 in
+// every stage (1238 us instead of 777 with MT = 1), and even if single threads
+// pass the stages on for the others, the way is longer by it (131 x 4096 x 4096
+// 24.4 us instead of 22.5, 250 x 5120 x 20480 74 to 108 instead of 72).
 //
 //   warp 0      TMA producer of dY
 //   warp 1      one thread of rank 0 issues the MMAs
@@ -304,8 +307,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int32_t it = 0;
     for (int32_t idx = pair; ok && unit_at(p, idx, u); idx += npairs, ++it) {
       for (int32_t kb = u.k0; ok && kb < u.k1; ++kb) {
-        if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, p.status,
-                               LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
+        if (!mbar_wait_bounded_cluster(full_bar(stage), phase, abort_flag, p.status,
+                                       LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
           ok = false;
           break;
         }
@@ -313,8 +316,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int b = 0; b < u.blocks; ++b) {
           const int acc = acc_of(it, b);
           if (kb == u.k0 &&
-              !mbar_wait_bounded(tempty_bar(acc), acc_use(it) ^ 1u, abort_flag, p.status,
-                                 LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
+              !mbar_wait_bounded_cluster(tempty_bar(acc), acc_use(it) ^ 1u, abort_flag, p.status,
+                                         LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
             ok = false;
             break;
           }
@@ -340,8 +343,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // (a block without rows passes its accumulator on unused)
       for (int b = 0; b < MT; ++b) {
         if (b >= u.blocks &&
-            !mbar_wait_bounded(tempty_bar(acc_of(it, b)), acc_use(it) ^ 1u, abort_flag, p.status,
-                               LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
+            !mbar_wait_bounded_cluster(tempty_bar(acc_of(it, b)), acc_use(it) ^ 1u, abort_flag,
+                                       p.status, LLMINT8_DEV_TIMEOUT_MMA, p.timeout_ns)) {
           ok = false;
           break;
         }
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_remote(mapa_shared(full_bar(stage), 0));
+          mbar_arrive_smem(mapa_shared(full_bar(stage), 0));
           mbar_arrive(raw_empty_bar(rstage));
         }
         stage += CVT_GROUPS;

@@ -118,13 +118,46 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   return v;
 }
 
-// Arrive on an mbarrier given by its shared::cluster address, at the default
-// scope: unlike mbar_arrive_cluster it does not wait for the thread's writes to
-// reach the cluster's point of coherence (a round trip to L2 under load). For signals
-// about shared memory of this CTA that only this SM's tensor core reads, after
-// fence.proxy.async has made the writes visible to it.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+// Arrive on an mbarrier given by its shared::cluster address, with a release at
+// cluster scope of accesses to this CTA's shared memory only: unlike
+// mbar_arrive_cluster it does not wait for the thread's other writes to reach
+// the cluster's point of coherence (a round trip to L2 under load). For signals
+// about shared memory, whose waiter acquires at cluster scope.
+__device__ __forceinline__ void mbar_arrive_smem(uint32_t cluster_bar) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+      : "memory");
+}
+
+// mbar_wait_bounded for a barrier on which threads of the other CTA arrive: what
+// they released at cluster scope is acquired at cluster scope.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_bounded_cluster(uint32_t bar, uint32_t parity,
+                                                          volatile int *abort_flag, int *status,
+                                                          int code, uint64_t limit_ns) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > limit_ns) {
+      *abort_flag = 1;
+      atomicOr(status, code);
+      return false;
+    }
+  }
 }
 
 // Instruction descriptor of tcgen05.mma kind::f16 (idesc_f16_f32) with the

@@ -1,6 +1,7 @@
 """What the kernels' sources promise the compiler, read from their signatures:
 no `__restrict__` on a pointer that a documented call may alias, or whose data
-the preceding grid still writes when the kernel starts."""
+the preceding grid still writes when the kernel starts; and the scopes of the
+signals between the CTAs of a pair."""
 import os
 import re
 
@@ -47,3 +48,27 @@ WRITTEN_BY_THE_PRECEDING_GRID = [("adapters.cuh", "k_rows_expand", ("part",)),
 @pytest.mark.parametrize("source,kernel,names", WRITTEN_BY_THE_PRECEDING_GRID)
 def test_results_of_a_grid_still_running_are_not_restrict(source, kernel, names):
     test_pointers_that_may_be_the_same_are_not_restrict(source, kernel, names)
+
+
+def test_arrivals_in_the_other_cta_release_at_cluster_scope():
+    """An arrival without a scope has that of its own CTA: it would not order
+    its thread's writes for a waiter in the other one."""
+    seen = 0
+    for name in sorted(os.listdir(build.CSRC)):
+        text = open(os.path.join(build.CSRC, name)).read()
+        for op in re.finditer(r"mbarrier\.arrive[\w.:]*shared::cluster[\w.:]*", text):
+            before = text[text.rindex("asm", 0, op.start()):op.start()]
+            assert (".release.cluster" in op[0] or ".relaxed.cluster" in op[0] and
+                    "fence.release.sync_restrict::shared::cta.cluster;" in before), (name, op[0])
+            seen += 1
+    assert seen  # k_input_grad's
+
+
+def test_the_input_gradient_s_issuer_acquires_what_the_other_cta_released():
+    text = open(os.path.join(build.CSRC, "input_grad_sm100.cuh")).read()
+    issuer = text[text.index("- MMA issuer"):text.index("- TMA producer of the codes")]
+    waits = re.findall(r"mbar_wait\w*\((\w+)", issuer)
+    assert {w: f for f, w in re.findall(r"(mbar_wait\w*)\((\w+)", issuer)} == {
+        "full_bar": "mbar_wait_bounded_cluster", "tempty_bar": "mbar_wait_bounded_cluster",
+        "drain_bar": "mbar_wait_bounded"}  # drain: this thread's own commit
+    assert len(waits) == 4
