@@ -422,7 +422,8 @@ LLMINT8_API int64_t llmint8_decode_max_rows(void);
  * it once with llmint8_workspace_init, read it with
  * llmint8_read_device_status. A workspace may serve calls of any of them
  * whose size it covers, one after another on one stream (captured graphs
- * included); calls that can overlap need one each.
+ * included); calls that can overlap need one each. No tensor of a call may lie
+ * in the bytes of the workspace that it uses (LLMINT8_ERR_ARG).
  * ------------------------------------------------------------------------- */
 
 /* Element types of the operators below. */

@@ -673,6 +673,8 @@ llmint8_status llmint8_adapters_forward(const uint16_t *X_dev, int64_t s,
     return LLMINT8_ERR_ARG;
   const AdapterLayout L = adapter_layout(s, ad->h, ad->o, ad->n, ad->r);
   if (ws_bytes < L.end) return LLMINT8_ERR_WORKSPACE;
+  if (overlaps_any({ws_dev, L.end}, {X, base, out, kept, ids, A, B, scale, rank}))
+    return LLMINT8_ERR_ARG;
   Device *dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   cudaStream_t st = as_stream(stream);
@@ -722,6 +724,9 @@ llmint8_status llmint8_adapters_backward(const uint16_t *X_dev, const uint16_t *
     return LLMINT8_ERR_ARG;
   const AdapterLayout L = adapter_layout(s, ad->h, ad->o, ad->n, ad->r);
   if (s > 0 && ws_bytes < L.end) return LLMINT8_ERR_WORKSPACE;
+  if (s > 0 && overlaps_any({ws_dev, L.end},
+                            {X, dY, base, dX, kept, ids, A, B, scale, rank, dA, dB}))
+    return LLMINT8_ERR_ARG;
   Device *dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   cudaStream_t st = as_stream(stream);
@@ -847,14 +852,14 @@ llmint8_status llmint8_matmul_backward(const uint16_t *dY_dev, int64_t s, const 
   if (!aligned(dY_dev, 16) || !aligned(base_dev, 16) || !aligned(dX_dev, 16) ||
       !aligned(ws_dev, 256))
     return LLMINT8_ERR_ALIGN;
-  const Span dX = {dX_dev, 2 * (size_t)s * w->h};
-  if (overlaps_any(dX, {{dY_dev, 2 * (size_t)s * w->o},
-                        {w->wq_dev, (size_t)w->h * w->o},
-                        {w->aw_dev, 4 * (size_t)w->o}}) ||
-      overlaps_partly(dX, {base_dev, dX.n}))
-    return LLMINT8_ERR_ARG;
+  const Span dX = {dX_dev, 2 * (size_t)s * w->h}, base = {base_dev, dX.n};
+  const Span dY = {dY_dev, 2 * (size_t)s * w->o}, aw = {w->aw_dev, 4 * (size_t)w->o};
+  const Span wq = {w->wq_dev, (size_t)w->h * w->o};
+  if (overlaps_any(dX, {dY, wq, aw}) || overlaps_partly(dX, base)) return LLMINT8_ERR_ARG;
   const igrad::Plan plan = input_grad_plan(s, w->h, w->o);
-  if (ws_bytes < input_grad_workspace(plan)) return LLMINT8_ERR_WORKSPACE;
+  const size_t need = input_grad_workspace(plan);
+  if (ws_bytes < need) return LLMINT8_ERR_WORKSPACE;
+  if (overlaps_any({ws_dev, need}, {dX, base, dY, wq, aw})) return LLMINT8_ERR_ARG;
   Device *dev = nullptr;
   if ((rc = current_device(&dev))) return rc;
   igrad::Params p;
@@ -945,7 +950,8 @@ llmint8_status llmint8_layernorm_backward(const uint16_t *dy_dev, const void *x_
       !aligned(mean_dev, 4) || !aligned(rstd_dev, 4) || !aligned(dx_dev, 16) ||
       !aligned(dgamma_dev, 16) || !aligned(dbeta_dev, 16) || !aligned(ws_dev, 256))
     return LLMINT8_ERR_ALIGN;
-  if (s > 0 && ws_bytes < llmint8_layernorm_workspace_size(s, h)) return LLMINT8_ERR_WORKSPACE;
+  const size_t need = s > 0 ? llmint8_layernorm_workspace_size(s, h) : 0;
+  if (ws_bytes < need) return LLMINT8_ERR_WORKSPACE;
   // dx in place of x or dy of its type: a row's block has read the row
   const Span x = {x_dev, type_size(x_type) * (size_t)s * h}, dy = {dy_dev, 2 * (size_t)s * h};
   const Span dx = {dx_dev, x.n}, gamma = {gamma_dev, type_size(p_type) * (size_t)h};
@@ -954,7 +960,8 @@ llmint8_status llmint8_layernorm_backward(const uint16_t *dy_dev, const void *x_
   if (overlaps_partly(dx, x) || overlaps_partly(dx, dy) ||
       overlaps_any(dx, {gamma, mean, rstd, dgamma, dbeta}) ||
       overlaps_any(dgamma, {x, dy, gamma, mean, rstd, dbeta}) ||
-      overlaps_any(dbeta, {x, dy, gamma, mean, rstd}))
+      overlaps_any(dbeta, {x, dy, gamma, mean, rstd}) ||
+      overlaps_any({ws_dev, need}, {x, dy, gamma, mean, rstd, dx, dgamma, dbeta}))
     return LLMINT8_ERR_ARG;
   Device *dev = nullptr;
   if ((rc = current_device(&dev))) return rc;

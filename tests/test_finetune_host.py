@@ -283,3 +283,46 @@ def test_layernorm_outputs_that_overlap_are_refused(lib, xt):
     at = _places(spans)
     for out, other in allowed:
         assert bwd(**dict(at, **{out: at[other]})) in (-5, -8)
+
+
+@needs_no_gpu
+def test_tensors_inside_the_workspace_are_refused(lib):
+    """Its first byte, its last and one in between; a tensor right behind it is
+    none of its bytes."""
+    s, h, o, n, r = 40, 256, 528, 2, 8
+    ws = ctypes.c_void_p(1 << 34)
+
+    def check(names, nbytes, call):
+        at = _places(names)
+        assert call(**at) in (-5, -8)  # sound, but for the GPU
+        for name in names:
+            for offset in (0, nbytes // 2 // 256 * 256, nbytes - 256):
+                assert call(**dict(at, **{name: ctypes.c_void_p(ws.value + offset)})) == -7, \
+                    (name, offset)
+            assert call(**dict(at, **{name: ctypes.c_void_p(ws.value + nbytes)})) in (-5, -8)
+
+    def forward(X, ids, base, out, v, a, b, scale, rank):
+        ad = binding.llmint8_adapters(h, o, n, r, a, b, scale, rank)
+        return lib.llmint8_adapters_forward(X, s, ctypes.byref(ad), ids, base, out, v, ws, BIG,
+                                            None)
+    size = lib.llmint8_adapters_workspace_size(s, h, o, n, r)
+    check(("X", "ids", "base", "out", "v", "a", "b", "scale", "rank"), size, forward)
+
+    def backward(X, dY, ids, v, base, dX, dA, dB, a, b, scale, rank):
+        ad = binding.llmint8_adapters(h, o, n, r, a, b, scale, rank)
+        return lib.llmint8_adapters_backward(X, dY, s, ctypes.byref(ad), ids, v, base, dX, dA,
+                                             dB, ws, BIG, None)
+    check(("X", "dY", "ids", "v", "base", "dX", "dA", "dB", "a", "b", "scale", "rank"), size,
+          backward)
+
+    def matmul(dY, wq, aw, base, dX):
+        w = binding.llmint8_weight(h, o, wq, aw)
+        return lib.llmint8_matmul_backward(dY, s, ctypes.byref(w), base, dX, ws, BIG, None)
+    check(("dY", "wq", "aw", "base", "dX"), lib.llmint8_matmul_backward_workspace_size(s, h, o),
+          matmul)
+
+    def layernorm(dy, x, g, mean, rstd, dx, dg, db):
+        return lib.llmint8_layernorm_backward(dy, x, 0, s, h, g, 1, mean, rstd, dx, dg, db, ws,
+                                              BIG, None)
+    check(("dy", "x", "g", "mean", "rstd", "dx", "dg", "db"),
+          lib.llmint8_layernorm_workspace_size(s, h), layernorm)
