@@ -547,8 +547,8 @@ typedef struct {
 /* A list of gradients laid out once for repeated calls. The caller sets
  * table_dev (device memory, 256-byte aligned) and table_bytes (at least
  * llmint8_grad_list_size(n)); llmint8_grad_list_init fills the rest and the
- * table. Two outputs, or an output and another entry's gradient, must not
- * overlap (LLMINT8_ERR_ARG). */
+ * table. Two outputs, an output and another entry's gradient, or an output and
+ * the table must not overlap (LLMINT8_ERR_ARG). */
 typedef struct {
     void *table_dev;
     size_t table_bytes;
@@ -569,7 +569,8 @@ LLMINT8_API llmint8_status llmint8_grad_list_init(const llmint8_grad *grads_host
 /* Global norm over a list, and clipping:
  *   norm = sqrt(sum of all squares)  (fp64 sums in a fixed order)
  *   out = g * min(1, max_norm / (norm + 1e-6))
- * *norm_dev (fp32) receives the norm before clipping. max_norm >= 0; +inf asks
+ * *norm_dev (fp32) receives the norm before clipping; it lies outside the table
+ * (LLMINT8_ERR_ARG). max_norm >= 0; +inf asks
  * for the norm alone (in place nothing is written, other outputs get copies).
  * A norm of inf or NaN clips every element by 0 or NaN: test the norm before
  * using the gradients. Calls that can overlap need a list each. */

@@ -1011,8 +1011,9 @@ llmint8_status llmint8_grad_list_init(const llmint8_grad *grads_host, int64_t n,
     if (!g.grad_dev) return LLMINT8_ERR_NULL;
     const uintptr_t size = g.type == LLMINT8_F32 ? 4 : 2;
     if (!aligned(g.grad_dev, size) || !aligned(g.out_dev, size)) return LLMINT8_ERR_ALIGN;
-    if (g.out_dev != g.grad_dev &&
-        overlap(g.out_dev, size * (size_t)g.n, g.grad_dev, size * (size_t)g.n))
+    const size_t bytes = size * (size_t)g.n;
+    if ((g.out_dev != g.grad_dev && overlap(g.out_dev, bytes, g.grad_dev, bytes)) ||
+        overlap(g.out_dev ? g.out_dev : g.grad_dev, bytes, list->table_dev, need))
       return LLMINT8_ERR_ARG;
     chunks += ceil_div(g.n, clip::chunk_elements(g.type));
   }
@@ -1077,6 +1078,7 @@ llmint8_status llmint8_clip_grads(const llmint8_grad_list *list, float max_norm,
   if (need == 0 || list->chunks < 0) return LLMINT8_ERR_SHAPE;
   if (!aligned(list->table_dev, 256) || !aligned(norm_dev, 4)) return LLMINT8_ERR_ALIGN;
   if (list->table_bytes < need) return LLMINT8_ERR_WORKSPACE;
+  if (overlap(norm_dev, sizeof(float), list->table_dev, need)) return LLMINT8_ERR_ARG;
   Device *dev = nullptr;
   llmint8_status rc = current_device(&dev);
   if (rc) return rc;

@@ -326,3 +326,26 @@ def test_tensors_inside_the_workspace_are_refused(lib):
                                               BIG, None)
     check(("dy", "x", "g", "mean", "rstd", "dx", "dg", "db"),
           lib.llmint8_layernorm_workspace_size(s, h), layernorm)
+
+
+@needs_no_gpu
+def test_clip_refuses_outputs_and_norms_inside_its_table(lib):
+    G, table = binding.llmint8_grad, 1 << 34
+    size = lib.llmint8_grad_list_size(3)
+    lst = binding.llmint8_grad_list(ctypes.c_void_p(table), BIG, 3, 3)
+
+    def init(out):
+        grads = (G * 3)(G(FAKE, None, 10, 1), G(ctypes.c_void_p(1 << 24), out, 64, 1),
+                        G(None, None, 0, 1))
+        return lib.llmint8_grad_list_init(grads, 3, ctypes.byref(lst), None)
+
+    def clip(norm):
+        return lib.llmint8_clip_grads(ctypes.byref(lst), 1.0, norm, None)
+    for offset in (0, size // 2 // 256 * 256, size - 4):
+        assert init(ctypes.c_void_p(table + offset)) == -7
+        assert clip(ctypes.c_void_p(table + offset)) == -7
+    assert init(ctypes.c_void_p(table - 4)) == -7
+    assert init(ctypes.c_void_p(table + size)) in (-5, -8)  # sound, but for the GPU
+    assert init(ctypes.c_void_p(table - 256)) in (-5, -8)
+    assert clip(ctypes.c_void_p(table + size)) in (-5, -8)
+    assert clip(ctypes.c_void_p(table - 4)) in (-5, -8)
