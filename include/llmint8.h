@@ -570,7 +570,8 @@ LLMINT8_API llmint8_status llmint8_grad_list_init(const llmint8_grad *grads_host
  *   norm = sqrt(sum of all squares)  (fp64 sums in a fixed order)
  *   out = g * min(1, max_norm / (norm + 1e-6))
  * *norm_dev (fp32) receives the norm before clipping; it lies outside the table
- * (LLMINT8_ERR_ARG). max_norm >= 0; +inf asks
+ * (LLMINT8_ERR_ARG) and outside every gradient and output (the caller's part:
+ * the list is on the device and is not looked through). max_norm >= 0; +inf asks
  * for the norm alone (in place nothing is written, other outputs get copies).
  * A norm of inf or NaN clips every element by 0 or NaN: test the norm before
  * using the gradients. Calls that can overlap need a list each. */

@@ -8,6 +8,7 @@ CPU fallback.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import math
 import os
@@ -732,6 +733,26 @@ def llmint8_layernorm_backward(dY: torch.Tensor, X: torch.Tensor, gamma: torch.T
     return dX, dgamma, dbeta
 
 
+def _address_ranges(tensors):
+    """The addresses [begin, end) of contiguous tensors, merged and in order."""
+    merged = []
+    for begin, end in sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                             for t in tensors if t.numel()):
+        if merged and begin <= merged[-1][1]:
+            merged[-1] = (merged[-1][0], max(end, merged[-1][1]))
+        else:
+            merged.append((begin, end))
+    return merged
+
+
+def _overlaps(ranges, t: torch.Tensor) -> bool:
+    """Whether t shares a byte with one of these merged ranges."""
+    begin = t.data_ptr()
+    end = begin + t.numel() * t.element_size()
+    i = bisect.bisect_left(ranges, (end,))  # the ranges before i begin below end
+    return i > 0 and begin < min(end, ranges[i - 1][1])
+
+
 class GradList:
     """Gradients laid out once, on their device's current stream, for repeated
     llmint8_clip_grads: contiguous CUDA tensors (fp16, bf16 or fp32) on one
@@ -756,6 +777,7 @@ class GradList:
                                     _tensor(out, f"outs[{i}]", g.dtype, g.shape, device),
                                     g.numel(), _TYPES[g.dtype])
         self.device = device
+        self.ranges = _address_ranges(self.grads + self.outs)
         lib = load_library()
         nbytes = int(lib.llmint8_grad_list_size(n))
         with _Launch(device) as st:
@@ -767,9 +789,12 @@ class GradList:
 
 def llmint8_clip_grads(grads: GradList, max_norm: float, norm: Optional[torch.Tensor] = None,
                        stream=None) -> torch.Tensor:
-    """The global norm of a list's gradients (float32 [1]); they are scaled so
-    that it does not exceed max_norm (inf: the norm alone)."""
+    """The global norm of a list's gradients (float32 [1], no part of them or
+    of their outputs); they are scaled so that it does not exceed max_norm (inf:
+    the norm alone)."""
     dev = grads.device
+    if norm is not None and _overlaps(grads.ranges, norm):
+        raise ValueError("norm lies in one of the list's gradients or outputs")
     with _Launch(dev, stream) as st:
         if norm is None:
             norm = torch.empty((1,), dtype=torch.float32, device=dev)

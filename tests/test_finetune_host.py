@@ -349,3 +349,24 @@ def test_clip_refuses_outputs_and_norms_inside_its_table(lib):
     assert init(ctypes.c_void_p(table - 256)) in (-5, -8)
     assert clip(ctypes.c_void_p(table + size)) in (-5, -8)
     assert clip(ctypes.c_void_p(table - 4)) in (-5, -8)
+
+
+def test_address_ranges_of_tensors():
+    """The ranges that a clip list's norm is looked up in: merged, in order,
+    empty tensors none of them."""
+    buf = torch.zeros(64)
+    at = buf.data_ptr()
+    parts = [buf[32:40], buf[0:4], buf[2:8], buf[8:8], buf[34:36], buf[8:12],
+             buf[50:52].to(torch.float16)]
+    spans = binding._address_ranges(parts)
+    other = parts[-1].data_ptr()
+    assert sorted(spans) == spans
+    assert [s for s in spans if at <= s[0] < at + 256] == [(at, at + 48), (at + 128, at + 160)]
+    assert (other, other + 4) in spans and len(spans) == 3
+    for i in range(64):
+        inside = i < 12 or 32 <= i < 40
+        assert binding._overlaps(spans, buf[i:i + 1]) == inside
+        assert binding._overlaps(spans, buf[i:i]) is False
+    assert binding._overlaps(spans, buf[12:33]) and not binding._overlaps(spans, buf[12:32])
+    assert binding._overlaps(spans, buf)
+    assert binding._address_ranges([]) == [] and not binding._overlaps([], buf)

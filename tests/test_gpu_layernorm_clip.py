@@ -317,3 +317,19 @@ def test_layernorm_of_many_rows(s, h, xt, pt):
 @pytest.mark.parametrize("s,h", [(2047, 4096), (8001, 528), (1777, 8192), (1501, 16384)])
 def test_layernorm_of_many_rows_in_place(s, h):
     test_layernorm_in_place(s, h)
+
+
+def test_clip_refuses_a_norm_that_lies_in_a_gradient():
+    """The norm's place would be scaled, or squared, while it is written."""
+    flat = torch.ones(1000, device="cuda")
+    outs = torch.zeros(1000, device="cuda")
+    lst = L.GradList([flat[10:20], flat[500:700]], [outs[10:20], outs[500:700]])
+    for t in (flat, outs):
+        for i in (10, 19, 500, 699):
+            with pytest.raises(ValueError, match="norm"):
+                L.llmint8_clip_grads(lst, 1.0, norm=t[i:i + 1])
+        for i in (9, 20, 499, 700):
+            norm = L.llmint8_clip_grads(lst, 1.0, norm=t[i:i + 1])
+            assert abs(float(norm) / math.sqrt(210) - 1) < 1e-6
+            t[i] = 1
+    assert (flat == 1).all()
