@@ -601,7 +601,11 @@ def llmint8_adapters_forward(X: torch.Tensor, adapters: Adapters, ids: torch.Ten
     whose id is outside [0, n) uses none) -> fp16 [s,o].
 
     base (fp16 [s,o], default zeros) is the projection's output; out may be
-    base itself. v (float32 [s,r]) receives X . A for the backward pass."""
+    base itself. v (float32 [s,r]) receives X . A for the backward pass.
+
+    Without a workspace the call makes one
+    of its own, whose status (a wait that ran out: llmint8_read_device_status)
+    nobody can read afterwards."""
     ad, dev = adapters, adapters.device
     s = _matrix(X, "X")[0]
     f16 = torch.float16
@@ -633,7 +637,11 @@ def llmint8_adapters_backward(X: Optional[torch.Tensor], dY: torch.Tensor, adapt
     v is what the forward call left there (default: computed again); base
     (fp16 [s,h], default zeros) is the gradient that reaches X through the
     projection and is added into dX, which may be base itself. want = (dX, dA,
-    dB) leaves out what is not wanted (None is returned in its place)."""
+    dB) leaves out what is not wanted (None is returned in its place).
+
+    Without a workspace the call makes one
+    of its own, whose status (a wait that ran out: llmint8_read_device_status)
+    nobody can read afterwards."""
     ad, dev = adapters, adapters.device
     s = _matrix(dY, "dY")[0]
     f16, f32 = torch.float16, torch.float32
@@ -665,7 +673,11 @@ def llmint8_matmul_backward(dY: torch.Tensor, w: PreparedWeight,
                             workspace: Optional[BackwardWorkspace] = None,
                             stream=None) -> torch.Tensor:
     """dX = dY . W^T through the frozen int8 weight (+ base): dY fp16 [s,o]
-    -> fp16 [s,h]. out may be base itself."""
+    -> fp16 [s,h]. out may be base itself.
+
+    Without a workspace the call makes one
+    of its own, whose status (a wait that ran out: llmint8_read_device_status)
+    nobody can read afterwards."""
     s = _matrix(dY, "dY")[0]
     dev, f16 = w.wq.device, torch.float16
     py, pb = _tensor(dY, "dY", f16, (s, w.o), dev), _optional(base, "base", f16, (s, w.h), dev)
@@ -714,7 +726,11 @@ def llmint8_layernorm_backward(dY: torch.Tensor, X: torch.Tensor, gamma: torch.T
                                workspace: Optional[LayerNormWorkspace] = None, stream=None):
     """(dX in X's type, dgamma float32 [h], dbeta float32 [h]) for dY fp16
     [s,h], with the forward call's mean and rstd. dX may be X itself, or dY
-    where X is fp16."""
+    where X is fp16.
+
+    Without a workspace the call makes one
+    of its own, whose status (a wait that ran out: llmint8_read_device_status)
+    nobody can read afterwards."""
     s, h = _matrix(X, "X")
     dev, f32 = X.device, torch.float32
     tx, tp = _ln_type(X, "X"), _ln_type(gamma, "gamma")

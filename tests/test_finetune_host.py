@@ -370,3 +370,13 @@ def test_address_ranges_of_tensors():
     assert binding._overlaps(spans, buf[12:33]) and not binding._overlaps(spans, buf[12:32])
     assert binding._overlaps(spans, buf)
     assert binding._address_ranges([]) == [] and not binding._overlaps([], buf)
+
+
+def test_documents_say_how_a_wait_that_ran_out_is_seen():
+    """Only a caller's workspace can be asked for its status: the calls that
+    can do without one say so."""
+    calls = ("llmint8_adapters_forward", "llmint8_adapters_backward", "llmint8_matmul_backward",
+             "llmint8_layernorm_backward")
+    for name in calls:
+        doc = getattr(binding, name).__doc__
+        assert "llmint8_read_device_status" in doc and "workspace" in doc, name
