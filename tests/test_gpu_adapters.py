@@ -612,3 +612,11 @@ def test_input_gradient_of_a_long_reduction(s, h, o, sign):
     else:
         lim += (o / 16 + 16) * 2.0 ** -23 * dY.double().norm(dim=1)[:, None] * WR.norm(dim=0)
     assert ((got - ref).abs() <= lim).all()
+
+
+# as many adapters as a call takes, more than most rows can name
+@pytest.mark.parametrize("s", [100, 300])
+def test_most_adapters(s):
+    case = (s, 32, 48, 65535, 8, "mixed", "mixed")
+    test_forward_exact(case)
+    test_backward_exact(case)

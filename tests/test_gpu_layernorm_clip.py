@@ -333,3 +333,36 @@ def test_clip_refuses_a_norm_that_lies_in_a_gradient():
             assert abs(float(norm) / math.sqrt(210) - 1) < 1e-6
             t[i] = 1
     assert (flat == 1).all()
+
+
+@pytest.mark.parametrize("s,h", [(5, 528), (2047, 4096), (3, 16400)])
+@pytest.mark.parametrize("xt", [torch.float16, torch.float32])
+def test_layernorm_results_that_are_not_wanted(s, h, xt):
+    """The C calls with NULL in an output's place leave the others' bits as
+    they are."""
+    lib = L.load_library()
+    X, gamma, beta, dY = ln_inputs(s, h, xt, torch.float32, "normal")
+    y, mean, rstd = L.llmint8_layernorm_forward(X, gamma, beta)
+    ws = L.LayerNormWorkspace(s, h)
+    want = L.llmint8_layernorm_backward(dY, X, gamma, mean, rstd, workspace=ws)
+    st = torch.cuda.current_stream().cuda_stream
+    code = 1 if xt is torch.float32 else 0
+    for mask in range(4):
+        got = [torch.full_like(t, 7.0) for t in (mean, rstd)]
+        out = torch.full_like(y, 7.0)
+        p = [t.data_ptr() if mask >> i & 1 else None for i, t in enumerate(got)]
+        assert lib.llmint8_layernorm_forward(X.data_ptr(), code, s, h, gamma.data_ptr(),
+                                             beta.data_ptr(), 1, 1e-5, out.data_ptr(), *p,
+                                             st) == 0
+        assert torch.equal(out, y)
+        for i, (g, ref) in enumerate(zip(got, (mean, rstd))):
+            assert torch.equal(g, ref) if mask >> i & 1 else (g == 7).all()
+    for mask in range(8):
+        got = [torch.full_like(t, 7.0) for t in want]
+        p = [t.data_ptr() if mask >> i & 1 else None for i, t in enumerate(got)]
+        assert lib.llmint8_layernorm_backward(
+            dY.data_ptr(), X.data_ptr(), code, s, h, gamma.data_ptr(), 1, mean.data_ptr(),
+            rstd.data_ptr(), *p, ws.buf.data_ptr(), ws.nbytes, st) == 0
+        for i, (g, ref) in enumerate(zip(got, want)):
+            assert torch.equal(g, ref) if mask >> i & 1 else (g == 7).all(), (mask, i)
+    assert L.llmint8_read_device_status(ws) == 0
