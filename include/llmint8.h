@@ -423,7 +423,8 @@ LLMINT8_API int64_t llmint8_decode_max_rows(void);
  * llmint8_read_device_status. A workspace may serve calls of any of them
  * whose size it covers, one after another on one stream (captured graphs
  * included); calls that can overlap need one each. No tensor of a call may lie
- * in the bytes of the workspace that it uses (LLMINT8_ERR_ARG).
+ * in the bytes of the workspace that it uses (LLMINT8_ERR_ARG). An infinity
+ * among the inputs makes the results that it reaches infinite or NaN.
  * ------------------------------------------------------------------------- */
 
 /* Element types of the operators below. */
@@ -494,8 +495,9 @@ LLMINT8_API llmint8_status llmint8_adapters_backward(
  *   WR[k][j] = fp16(wq[j][k] * (aw[j] / 127))
  * (the product of the code and an fp32 factor, rounded once: the fp16 weight
  * that llmint8_matmul recovers for its outlier rows, but for the order of its
- * fp32 roundings; w16_dev is not used), with fp32 sums; the rounding of X to
- * int8 counts as the identity. dY_dev fp16 [s][o]; base_dev (fp16 [s][h]) another gradient to add
+ * fp32 roundings; w16_dev is not used, even where llmint8_matmul takes its
+ * outlier rows from it), with fp32 sums; the rounding of X to int8 counts as the
+ * identity. dY_dev fp16 [s][o]; base_dev (fp16 [s][h]) another gradient to add
  * or NULL; dX_dev fp16 [s][h], may be base_dev itself, and overlaps no other
  * input (LLMINT8_ERR_ARG). */
 LLMINT8_API size_t llmint8_matmul_backward_workspace_size(int64_t s, int64_t h, int64_t o);
@@ -507,6 +509,7 @@ LLMINT8_API llmint8_status llmint8_matmul_backward(const uint16_t *dY_dev, int64
 /* Layer norm of the rows of x [s][h] (the projection's input):
  *   mean = sum_j x_j / h, rstd = 1 / sqrt(sum_j (x_j - mean)^2 / h + eps)
  *   y_j = fp16((x_j - mean) * rstd * gamma_j + beta_j)
+ * with fp32 sums (rstd is 0 where fp32 values' squares add up past its range).
  * x is fp16 or fp32 (x_type), gamma and beta [h] fp16 or fp32 (p_type);
  * beta_dev may be NULL (zeros). mean_dev, rstd_dev (fp32 [s], 4-byte aligned,
  * or NULL) keep the statistics for the backward pass. eps >= 0 and finite.

@@ -210,8 +210,8 @@ __device__ __forceinline__ float warp_row_max(const float *x, int r) {
 
 // Grid: (m tiles * split, y, jobs), clusters of `split` along x. Where the row
 // tiles leave SMs free, y clusters share the passes over the adapters of a tile
-// of mixed rows (150 rows of 16 adapters, rank 128, 12288 -> 512: 184 us with
-// one cluster per tile, 56 with 9).
+// of mixed rows (150 rows of 16 adapters, rank 128, 12288 -> 512, the whole
+// forward call: 148 us with one cluster per tile, 51 with 9).
 // NC: octets of terms that a thread sums in registers (r <= 8 NC).
 template <int NC>
 __global__ void __launch_bounds__(SH_THREADS, NC <= 8 ? 2 : 1)

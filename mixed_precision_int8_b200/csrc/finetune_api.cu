@@ -182,8 +182,10 @@ bool overlaps_partly(Span out, Span in) {
 // 96; sixteen 54 against 62 at 128; backward, one 34 against 37 at 48, 43
 // against 37 at 64; four 56 against 58 at 96, 71 against 57 at 128. 4096 ->
 // 4096, rank 16, one adapter at 128 rows: forward 7 against 12, backward 27
-// against 21 (17 against 18 at 64). Widths leave at most kRowMaxSlices partial
-// sums of a row.
+// against 21 (17 against 18 at 64). Every adapter held was in those batches;
+// which of them a batch uses is known on the device only, so that 128 rows of
+// one of 64 adapters held take the row kernels too (forward 47 us, 23 if it is
+// held alone). Widths leave at most kRowMaxSlices partial sums of a row.
 constexpr int64_t kRowMaxSlices = 256;
 
 bool use_row_kernels(int64_t s, const llmint8_adapters *ad, bool backward) {
@@ -274,12 +276,12 @@ struct ShrinkGrid {
 };
 
 // Powers of two up to 8 CTAs per cluster that leave every CTA its place, then
-// clusters for the passes, then clusters of 16 if there is still room (1000
-// rows of 16 adapters, rank 64, 12288 -> 12288: 87 us with 8 CTAs and one
-// cluster, 59 with 8 and 4, 64 with 16 and 2; 37 rows of one adapter, rank 64,
-// 11456 -> 1104: 21 us with 8, 17 with 16). A pass of fewer than eight stages
-// is over sooner than another cluster's start (221 rows of 5 adapters, rank
-// 16, 768 features: 31 us, 32.5 with 2).
+// clusters for the passes, then clusters of 16 if there is still room (whole
+// forward calls, 1000 rows of 16 adapters, rank 64, 12288 -> 12288: 80 us with 8
+// CTAs and one cluster, 57 with 8 and 4, 61 with 16 and 2; 200 rows of one
+// adapter, rank 64, 11456 -> 1104: 22 us with 8, 18 with 16). A pass of fewer
+// than eight stages is over sooner than another cluster's start (221 rows of 5
+// adapters, rank 16, 768 -> 768: 15.0 us, 15.6 with 2).
 ShrinkGrid shrink_grid(int64_t s, int64_t k, const llmint8_adapters *ad, int n_jobs,
                        const Device &dev) {
   const int64_t room = (ad->r <= 64 ? 2 : 1) * dev.sm_count;  // two CTAs per SM up to r = 64

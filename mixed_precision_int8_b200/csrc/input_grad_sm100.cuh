@@ -9,8 +9,20 @@
 // operand, so nothing is transposed; each int8 tile is turned into fp16 on
 // its way into shared memory.
 //
+// The weight is rounded to fp16, as in the layer's outlier rows, because one
+// fp16 operand holds no more of a code times its factor: results are 2.9e-4 off
+// (rms, relative) instead of the 2.1e-4 of their own rounding to fp16. Splitting
+// it, or dY times the factor, into two numbers would double the MMAs, which are
+// the bound. The fp32 sums stay in their accumulators over a part's whole
+// reduction; the tensor cores round them toward zero at every MMA of 16
+// products: they end 1.5e-6 of their size too small after 4096 products of
+// either sign, 3.0e-6 after 20480, 5.7e-6 after 49152, 1.5e-5 after 262144
+// (products of one sign: 5.6e-6, 1.8e-5, 3.4e-5, 9.3e-5), which a rounding to
+// fp16 outweighs; k_shrink and k_outer, whose results are fp32, change
+// accumulators for that reason.
+//
 // Bound: the fp16 tensor cores (2 s h o operations) and, back to back, the
-// power cap at prefill sizes (4096 x 5120 x 20480: 679 us in a burst, 800 us
+// power cap at prefill sizes (4096 x 5120 x 20480: 670 us in a burst, 800 us
 // under the cap; 596 us in a burst with the conversion switched off). A pair of
 // CTAs computes a tile of MT x 256 rows by 256 columns (tcgen05
 // cta_group::2), so that per stage of 64 reduction indices a CTA stores and

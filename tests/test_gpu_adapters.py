@@ -620,3 +620,32 @@ def test_most_adapters(s):
     case = (s, 32, 48, 65535, 8, "mixed", "mixed")
     test_forward_exact(case)
     test_backward_exact(case)
+
+
+@pytest.mark.parametrize("s", [12, 300])
+def test_infinities_reach_their_own_results_only(s):
+    """An infinity of X, dY or a factor: what it enters is infinite or NaN,
+    everything else keeps its bits."""
+    c = Case(s, 528, 784, 3, 16, "mixed", "full", seed=7)
+    ref = L.llmint8_adapters_backward(c.X, c.dY, c.ad, c.ids, base=c.dbase)
+    row = next(i for i, a in enumerate(c.ids_list) if a == 1)
+    c.dY[row, 5] = float("inf")
+    dX, dA, dB = L.llmint8_adapters_backward(c.X, c.dY, c.ad, c.ids, base=c.dbase)
+    v = c.X[row].double() @ c.A[1].double().T
+    others = torch.arange(s, device="cuda") != row
+    assert torch.equal(dX[others], ref[0][others]) and not dX[row].isfinite().any()
+    for got, want in ((dA, ref[1]), (dB, ref[2])):
+        assert torch.equal(got[[0, 2]], want[[0, 2]])
+    keep = torch.arange(c.o, device="cuda") != 5
+    assert torch.equal(dB[1][:, keep], ref[2][1][:, keep])
+    assert not dB[1][v != 0, 5].isfinite().any()
+    c.dY[row, 5] = 0
+    c.B[1, 2, 9] = float("-inf")
+    out = L.llmint8_adapters_forward(c.X, c.ad, c.ids, base=c.base)
+    got_v = c.X.double() @ c.A[1].double().T
+    hit = (c.ids == 1) & (got_v[:, 2] != 0)
+    assert not out[hit, 9].isfinite().any()
+    c.B[1, 2, 9] = 0
+    want = L.llmint8_adapters_forward(c.X, c.ad, c.ids, base=c.base)
+    mine = (c.ids == 1)[:, None] & (torch.arange(c.o, device="cuda") == 9)
+    assert torch.equal(out[~mine], want[~mine])

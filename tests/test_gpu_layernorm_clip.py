@@ -366,3 +366,14 @@ def test_layernorm_results_that_are_not_wanted(s, h, xt):
         for i, (g, ref) in enumerate(zip(got, want)):
             assert torch.equal(g, ref) if mask >> i & 1 else (g == 7).all(), (mask, i)
     assert L.llmint8_read_device_status(ws) == 0
+
+
+def test_layernorm_of_values_whose_squares_leave_fp32():
+    X = torch.randn(3, 528, device="cuda")
+    X[1] *= 1e30
+    gamma, beta = torch.ones(528, device="cuda"), torch.randn(528, device="cuda")
+    y, mean, rstd = L.llmint8_layernorm_forward(X, gamma, beta)
+    assert rstd[1] == 0 and torch.equal(y[1], beta.half())
+    ok = [0, 2]
+    for a, b in zip((y, mean, rstd), L.llmint8_layernorm_forward(X[ok], gamma, beta)):
+        assert torch.equal(a[ok], b)
