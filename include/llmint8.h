@@ -551,7 +551,8 @@ typedef struct {
  * table_dev (device memory, 256-byte aligned) and table_bytes (at least
  * llmint8_grad_list_size(n)); llmint8_grad_list_init fills the rest and the
  * table. Two outputs, an output and another entry's gradient, or an output and
- * the table must not overlap (LLMINT8_ERR_ARG). */
+ * the table must not overlap (LLMINT8_ERR_ARG); no more may a gradient that is
+ * only read and the table, which is not checked. */
 typedef struct {
     void *table_dev;
     size_t table_bytes;

@@ -603,9 +603,8 @@ def llmint8_adapters_forward(X: torch.Tensor, adapters: Adapters, ids: torch.Ten
     base (fp16 [s,o], default zeros) is the projection's output; out may be
     base itself. v (float32 [s,r]) receives X . A for the backward pass.
 
-    Without a workspace the call makes one
-    of its own, whose status (a wait that ran out: llmint8_read_device_status)
-    nobody can read afterwards."""
+    Without a workspace the call makes one of its own, whose status (a wait
+    that ran out: llmint8_read_device_status) nobody can read afterwards."""
     ad, dev = adapters, adapters.device
     s = _matrix(X, "X")[0]
     f16 = torch.float16
@@ -639,9 +638,8 @@ def llmint8_adapters_backward(X: Optional[torch.Tensor], dY: torch.Tensor, adapt
     projection and is added into dX, which may be base itself. want = (dX, dA,
     dB) leaves out what is not wanted (None is returned in its place).
 
-    Without a workspace the call makes one
-    of its own, whose status (a wait that ran out: llmint8_read_device_status)
-    nobody can read afterwards."""
+    Without a workspace the call makes one of its own, whose status (a wait
+    that ran out: llmint8_read_device_status) nobody can read afterwards."""
     ad, dev = adapters, adapters.device
     s = _matrix(dY, "dY")[0]
     f16, f32 = torch.float16, torch.float32
@@ -675,9 +673,8 @@ def llmint8_matmul_backward(dY: torch.Tensor, w: PreparedWeight,
     """dX = dY . W^T through the frozen int8 weight (+ base): dY fp16 [s,o]
     -> fp16 [s,h]. out may be base itself.
 
-    Without a workspace the call makes one
-    of its own, whose status (a wait that ran out: llmint8_read_device_status)
-    nobody can read afterwards."""
+    Without a workspace the call makes one of its own, whose status (a wait
+    that ran out: llmint8_read_device_status) nobody can read afterwards."""
     s = _matrix(dY, "dY")[0]
     dev, f16 = w.wq.device, torch.float16
     py, pb = _tensor(dY, "dY", f16, (s, w.o), dev), _optional(base, "base", f16, (s, w.h), dev)
@@ -728,9 +725,8 @@ def llmint8_layernorm_backward(dY: torch.Tensor, X: torch.Tensor, gamma: torch.T
     [s,h], with the forward call's mean and rstd. dX may be X itself, or dY
     where X is fp16.
 
-    Without a workspace the call makes one
-    of its own, whose status (a wait that ran out: llmint8_read_device_status)
-    nobody can read afterwards."""
+    Without a workspace the call makes one of its own, whose status (a wait
+    that ran out: llmint8_read_device_status) nobody can read afterwards."""
     s, h = _matrix(X, "X")
     dev, f32 = X.device, torch.float32
     tx, tp = _ln_type(X, "X"), _ln_type(gamma, "gamma")

@@ -15,8 +15,8 @@
 // Bound: bytes. A row is read once and kept in registers (forward; NV vectors
 // of eight elements per thread) or shared memory (backward) between the sums
 // and the store; rows too long for that are re-read from L2 by the *_long
-// kernels. y may be x, and dx may be x or dy: a thread reads an element before
-// it writes it, and none of these pointers is __restrict__.
+// kernels. y may be x, and dx may be x or dy: every read of an element comes
+// before its write, and none of these pointers is __restrict__.
 #pragma once
 
 #include <cstdint>
